@@ -460,6 +460,153 @@ moe_status_t moe_quantize_nvfp4(const uint16_t* x, int64_t batches, int64_t rows
 moe_status_t moe_quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, int elem, uint8_t* q, uint8_t* sf,
                              moe_stream_t stream);
 
+/* ---- Around the routed experts: norm, router, balance loss, linear ---- */
+
+/* Element types of arguments that come in more than one. */
+typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
+
+/* moe_rmsnorm: the layer's input for the experts.  For every row of M rows
+ * of H values
+ *   h = bf16(x + residual)           (h = x without a residual)
+ *   r = 1 / sqrt(mean(h^2) + eps)    (fp32)
+ *   y = bf16(h * r * weight)
+ *   q, q_sf = the MX quantisation of that bf16 y, bit for bit what
+ *             moe_quantize_mx(y, M, H, elem) gives
+ * in one pass.  x, residual: bf16 with row strides in elements (0 =
+ * contiguous; shorter than H: MOE_ERR_INVALID_ARGUMENT); residual NULL: none.
+ * weight: bf16 or fp32 [H] by weight_dtype.  Outputs, all contiguous:
+ *   residual_out bf16 [M, H]  h, the new residual stream; NULL: not stored;
+ *                             only with a residual
+ *   y    bf16 [M, H]          NULL: not stored
+ *   q    elem 0: E4M3 [M, H], elem 1: packed E2M1 [M, H/2]; q_sf E8M0
+ *        [M, H/32]; both or neither; at least one of y and q
+ *   rstd fp32 [M]             r, for moe_rmsnorm_backward; NULL: not stored
+ * residual_out may be the (contiguous) residual itself or x, and y may be x;
+ * other overlaps are not allowed.  h is rounded before it is normalised, so
+ * that the backward pass, which reads the stored h, differentiates what ran.
+ * 0 <= eps < inf.  H a multiple of 8 (of 32 with q), at most 65536; row
+ * strides multiples of 8; bf16 arrays, weight and q 16-byte aligned (else
+ * MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_rmsnorm(const uint16_t* x, int64_t x_row_stride, const uint16_t* residual,
+                         int64_t residual_row_stride, const void* weight, moe_dtype_t weight_dtype, float eps, int M,
+                         int H, uint16_t* residual_out, uint16_t* y, int elem, uint8_t* q, uint8_t* q_sf, float* rstd,
+                         moe_stream_t stream);
+
+/* Bytes of device workspace moe_rmsnorm_backward needs for dweight (row
+ * partials; any initial contents).  0 for M < 0 or an H it rejects. */
+size_t moe_rmsnorm_backward_workspace_size(int M, int H);
+
+/* moe_rmsnorm_backward: gradients of moe_rmsnorm's y (a quantised output
+ * passes its gradient straight through) in its rows and its weight:
+ *   g = dy * weight
+ *   dx = bf16(dh + r g - h r^3 mean(g h)),   dweight = sum over rows of dy h r
+ * dx is the gradient of x and of the residual alike.  dy, h bf16 [M, H]
+ * (h: residual_out, or x without a residual), rstd fp32 [M]; dh bf16 [M, H]:
+ * the gradient that reached residual_out by other ways, NULL: none.  dweight
+ * fp32 [H], overwritten (M = 0: zeros); the sum's order depends on M and H
+ * alone, so it is reproducible bit for bit.  dweight NULL: not computed, no
+ * workspace needed (NULL, 0).  dx may be dy or dh.  All rows contiguous;
+ * limits on H and alignment as in moe_rmsnorm; workspace 256-byte aligned.
+ * MOE_ERR_WORKSPACE: missing, unaligned or short. */
+moe_status_t moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const void* weight,
+                                  moe_dtype_t weight_dtype, const float* rstd, const uint16_t* dh, int M, int H,
+                                  uint16_t* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream);
+
+/* Scores of an expert from its router logit l (fp32):
+ *   SOFTMAX: s = exp(l) / sum over the experts of exp(l)
+ *   SIGMOID: s = 1 / (1 + exp(-l)) */
+typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
+
+/* moe_router_topk: the experts of each token and their routing weights, in
+ * the form moe_sort and moe_forward take them (topk_ids int32 [M, top_k],
+ * topk_weights fp32 [M, top_k], by descending key):
+ *   key    = logit, or score + select_bias[e] in fp64 when select_bias (fp32
+ *            [E]) is given (it acts on the choice only); equal keys: the
+ *            lower expert id first
+ *   weight = the score, with `renormalize` divided by the sum of the chosen
+ *            ones
+ * logits bf16 or fp32 [M, E] by logits_dtype, row stride in elements (0 =
+ * contiguous).  An expert whose logit or key is -inf or NaN is not chosen
+ * (and scores 0); a logit of +inf counts as FLT_MAX.  A token with fewer
+ * than top_k choosable experts gets id -1 and weight 0 in the places left,
+ * and so does every place of a token with token_mask[t] == 0 (uint8 [M], NULL: all
+ * tokens count): moe_sort drops those routes.
+ * E at most 1024 and top_k at most 64 (else MOE_ERR_UNSUPPORTED); top_k <= E.
+ *
+ * expert_counts, mean_probs, prob_grad and loss: all NULL, or all given; then
+ * the call also does what moe_balance_loss does on the ids it chose, from
+ * the same reading of the logits (coef, workspace as there). */
+moe_status_t moe_router_topk(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                             const float* select_bias, const uint8_t* token_mask, moe_score_t score, int renormalize,
+                             int M, int E, int top_k, int32_t* topk_ids, float* topk_weights, float coef,
+                             int32_t* expert_counts, float* mean_probs, float* prob_grad, float* loss,
+                             void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Bytes of device workspace the balance loss needs (any initial contents);
+ * 0 for M < 0 or an E outside [1, 1024]. */
+size_t moe_balance_workspace_size(int M, int E);
+
+/* moe_balance_loss: load-balancing loss of a routing.  Over the T tokens with
+ * token_mask[t] != 0 (all of them without a mask):
+ *   n_e = routes of those tokens to expert e (ids outside [0, E) count for none)
+ *   p_te = score_te / sum over the experts of score_te (SOFTMAX: the softmax)
+ *   f_e = n_e / (T top_k),  P_e = sum_t p_te / T
+ *   loss = coef * E * sum_e f_e P_e     (coef when both are uniform)
+ * Outputs: expert_counts int32 [E] = n_e; mean_probs fp32 [E] = P_e; loss
+ * fp32 [1]; prob_grad fp32 [E] = coef E / T (f_e - 1 / E), the gradient of
+ * the loss in p_te less a constant over the experts, which changes no
+ * gradient of a logit because the p of a token sum to 1 (and without which
+ * a balanced routing's gradients would be differences of equal numbers).
+ * T = 0: zeros.  Counts and sums do not depend on the order workgroups run
+ * in: results are reproducible bit for bit.  An expert with logit -inf or
+ * NaN has p = 0; a token without any other has p = 0 throughout.
+ * logits as in moe_router_topk, topk_ids int32 [M, top_k]; workspace
+ * 256-byte aligned, not shared by two calls in flight (MOE_ERR_WORKSPACE:
+ * missing, unaligned or short).  coef must be finite. */
+moe_status_t moe_balance_loss(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                              const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score, int M, int E,
+                              int top_k, float coef, int32_t* expert_counts, float* mean_probs, float* prob_grad,
+                              float* loss, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_router_backward: the gradient of the logits, in the logits' type,
+ * contiguous [M, E], overwritten, from either or both of
+ *   d_topk_weights fp32 [M, top_k]: the gradient of the routing weights of
+ *     moe_router_topk (the choice itself has none); NULL: none
+ *   prob_grad fp32 [E]: moe_balance_loss's, times the device scalar *d_loss
+ *     (NULL: 1); NULL: none
+ * With u_e = d_loss prob_grad_e and, for score weights, the weights'
+ * gradient on top of the chosen experts:
+ *   SOFTMAX: d_e = p_e (u_e - sum u p)
+ *   SIGMOID: d_e = p_e (1 - s_e) (u_e - sum u p)  of the loss,
+ *            s_e (1 - s_e) dw_e                   of a weight
+ *   renormalize: w_j (dw_j - sum dw w) (SIGMOID: times 1 - s) on the chosen
+ * topk_ids, token_mask, score and renormalize as in the forward calls; places
+ * with an id outside [0, E) have no weight, and the ids of a token must
+ * otherwise differ.  Tokens masked out get zeros.  MOE_ERR_INVALID_ARGUMENT:
+ * neither gradient given, d_loss without prob_grad. */
+moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                                 const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score,
+                                 int renormalize, int M, int E, int top_k, const float* d_topk_weights,
+                                 const float* prob_grad, const float* d_loss, void* d_logits, moe_stream_t stream);
+
+/* moe_linear_mx: the product of the MX formats without a routing plan, for
+ * the layers that every token takes (a shared expert, a dense layer):
+ *   y[m, n] = alpha * sum_k x[m, k] w[n, k] + bias[n]   (+ y[m, n] when accumulating)
+ * x_elem 0: x E4M3 [M, K]; 1: packed E2M1 [M, K/2]; x_sf E8M0 [M, K/32] (the
+ * outputs of moe_rmsnorm or moe_quantize_mx); w packed E2M1 [N, K/2], w_sf
+ * E8M0 [N, K/32], laid out as an expert's w1 or w2; alpha a device fp32
+ * scalar (NULL: 1); bias device fp32 [N] (NULL: none); y bf16 or fp32
+ * [M, N] by y_dtype.  The products accumulate in fp32; alpha, bias and the
+ * accumulation onto y are fp32 steps, and y is rounded once.  M, N >= 0; K a
+ * positive multiple of 32 (else MOE_ERR_INVALID_ARGUMENT).  x and w 16-byte
+ * aligned, y aligned to its elements, K at most 2^24, N * K/2 and
+ * M * K below 2^40 (else MOE_ERR_UNSUPPORTED).  Each output is one sum in an order that depends
+ * on the shape alone: reproducible bit for bit. */
+moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, const uint8_t* w, const uint8_t* w_sf,
+                           const float* alpha, const float* bias, int M, int N, int K, int accumulate, void* y,
+                           moe_dtype_t y_dtype, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

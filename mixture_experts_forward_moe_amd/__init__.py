@@ -22,11 +22,15 @@ NUM_PHASE_EVENTS = 5
 FLT_MAX = 3.4028234663852886e38
 NOALLOC_SCRATCH_BYTES = 64 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 ACT_SWIGLU, ACT_GEGLU_TANH, ACT_RELU2 = 0, 1, 2   # moe_activation_t (SiTU: ACT_SWIGLU with situ_beta > 0)
+DTYPE_BF16, DTYPE_F32 = 0, 1             # moe_dtype_t
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1      # moe_score_t
 
 EXPORTS = [
     "moe_status_string", "moe_route_slots", "moe_plan_workspace_size", "moe_plan_init", "moe_sort",
     "moe_grouped_gemm1_swiglu", "moe_grouped_gemm1_act", "moe_grouped_gemm2", "moe_grouped_gemm2_bias", "moe_finalize", "moe_opts_init", "moe_default_tile",
     "moe_workspace_size", "moe_forward_plan", "moe_forward", "moe_forward_noalloc", "moe_fc2_input_scale", "moe_nvfp4_global_scale", "moe_quantize_nvfp4", "moe_quantize_mx",
+    "moe_rmsnorm", "moe_rmsnorm_backward_workspace_size", "moe_rmsnorm_backward", "moe_router_topk",
+    "moe_balance_workspace_size", "moe_balance_loss", "moe_router_backward", "moe_linear_mx",
 ]
 
 
@@ -92,6 +96,14 @@ def lib() -> ctypes.CDLL:
             "moe_nvfp4_global_scale": ([P, I64, I64, P, P], I),
             "moe_quantize_nvfp4": ([P, I64, I64, I64, P, P, P, P], I),
             "moe_quantize_mx": ([P, I64, I64, I, P, P, P], I),
+            "moe_rmsnorm": ([P, I64, P, I64, P, I, F, I, I, P, P, I, P, P, P, P], I),
+            "moe_rmsnorm_backward_workspace_size": ([I, I], SZ),
+            "moe_rmsnorm_backward": ([P, P, P, I, P, P, I, I, P, P, P, SZ, P], I),
+            "moe_router_topk": ([P, I, I64, P, P, I, I, I, I, I, P, P, F, P, P, P, P, P, SZ, P], I),
+            "moe_balance_workspace_size": ([I, I], SZ),
+            "moe_balance_loss": ([P, I, I64, P, P, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
+            "moe_router_backward": ([P, I, I64, P, P, I, I, I, I, I, P, P, P, P, P], I),
+            "moe_linear_mx": ([P, P, I, P, P, P, P, I, I, I, I, P, I, P], I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -336,3 +348,172 @@ def moe_quantize_nvfp4(x, batches: int, rows: int, cols: int, gscale, q, sf, str
 
 def moe_quantize_mx(x, rows: int, cols: int, elem: int, q, sf, stream=None):
     _check(lib().moe_quantize_mx(_ptr(x), rows, cols, elem, _ptr(q), _ptr(sf), _stream(stream)), "moe_quantize_mx")
+
+
+# ---- around the routed experts: norm, router, balance loss, linear ----------
+
+def _arg(where: str, name: str, t, shape, size: int, optional=False, strided=False):
+    """The device address of tensor `t`, checked against the shape and the
+    element size the call reads or writes; `strided`: rows may be apart.
+    An optional tensor may be None."""
+    if t is None:
+        if optional:
+            return None
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} is required")
+    if tuple(t.shape) != shape or t.element_size() != size:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be {shape} of {size}-byte elements, "
+                                             f"is {tuple(t.shape)} of {t.element_size()}")
+    if not (t.stride(-1) == 1 or shape[-1] == 1 if strided else t.is_contiguous()):
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be contiguous" + (" in a row" if strided else ""))
+    if not t.is_cuda:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be on the GPU")
+    return t.data_ptr()
+
+
+def _rows(t):
+    """Row stride in elements of a [rows, columns] tensor (0: contiguous)."""
+    return 0 if t is None or t.is_contiguous() else t.stride(0)
+
+
+def _dtype(where: str, name: str, t) -> int:
+    """moe_dtype_t of a floating tensor (bf16 also as 16-bit integers)."""
+    import torch
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+        return DTYPE_BF16
+    raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be bf16 or fp32, is {t.dtype}")
+
+
+def _raw_stream(t, stream):
+    """The stream of a call on `t`'s device."""
+    import torch
+    return (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
+
+
+def _workspace(nbytes: int, given, t, stream):
+    """(tensor, bytes): the caller's workspace, or one from torch's allocator,
+    which is told of a stream other than the one it allocates for."""
+    if given is None:
+        given = _alloc(nbytes, t.device)
+        if stream is not None:
+            given.record_stream(stream)
+    return given, given.numel() * given.element_size()
+
+
+def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_sf=None, elem=0, rstd=None, eps=1e-6,
+                stream=None):
+    """h = bf16(x + residual), y = bf16(h * rsqrt(mean(h^2) + eps) * weight),
+    and y's MX codes, in one pass (see moe_rmsnorm in moe.h).  x, residual
+    bf16 [M, H], rows may be strided; weight bf16 or fp32 [H]."""
+    w = "moe_rmsnorm"
+    M, H = x.shape
+    wd = _dtype(w, "weight", weight)
+    _check(lib().moe_rmsnorm(
+        _arg(w, "x", x, (M, H), 2, strided=True), _rows(x),
+        _arg(w, "residual", residual, (M, H), 2, optional=True, strided=True), _rows(residual),
+        _arg(w, "weight", weight, (H,), 4 if wd else 2), wd, eps, M, H,
+        _arg(w, "residual_out", residual_out, (M, H), 2, optional=True), _arg(w, "y", y, (M, H), 2, optional=True),
+        elem, _arg(w, "q", q, (M, H if elem == 0 else H // 2), 1, optional=True),
+        _arg(w, "q_sf", q_sf, (M, H // 32), 1, optional=True), _arg(w, "rstd", rstd, (M,), 4, optional=True),
+        _raw_stream(x, stream)), w)
+
+
+def rmsnorm_backward_workspace_size(M: int, H: int) -> int:
+    return lib().moe_rmsnorm_backward_workspace_size(M, H)
+
+
+def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspace=None, stream=None):
+    """Gradients of moe_rmsnorm's rows and weight.  A workspace (only with
+    dweight) is taken from `workspace`, or allocated here when None."""
+    w = "moe_rmsnorm_backward"
+    M, H = dy.shape
+    wd = _dtype(w, "weight", weight)
+    nbytes = 0
+    if dweight is not None:
+        workspace, nbytes = _workspace(rmsnorm_backward_workspace_size(M, H), workspace, dy, stream)
+    _check(lib().moe_rmsnorm_backward(
+        _arg(w, "dy", dy, (M, H), 2), _arg(w, "h", h, (M, H), 2), _arg(w, "weight", weight, (H,), 4 if wd else 2), wd,
+        _arg(w, "rstd", rstd, (M,), 4), _arg(w, "dh", dh, (M, H), 2, optional=True), M, H,
+        _arg(w, "dx", dx, (M, H), 2), _arg(w, "dweight", dweight, (H,), 4, optional=True),
+        workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(dy, stream)), w)
+
+
+def _router_args(w, logits, token_mask):
+    M, E = logits.shape
+    d = _dtype(w, "logits", logits)
+    return M, E, d, _arg(w, "logits", logits, (M, E), 4 if d else 2, strided=True), \
+        _arg(w, "token_mask", token_mask, (M,), 1, optional=True)
+
+
+def _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss):
+    return (_arg(w, "expert_counts", expert_counts, (E,), 4), _arg(w, "mean_probs", mean_probs, (E,), 4),
+            _arg(w, "prob_grad", prob_grad, (E,), 4), _arg(w, "loss", loss, (1,), 4))
+
+
+def balance_workspace_size(M: int, E: int) -> int:
+    return lib().moe_balance_workspace_size(M, E)
+
+
+def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renormalize=True, select_bias=None,
+                    token_mask=None, coef=0.0, expert_counts=None, mean_probs=None, prob_grad=None, loss=None,
+                    workspace=None, stream=None):
+    """Experts (int32 [M, top_k]) and routing weights (fp32 [M, top_k]) of
+    router logits [M, E], as moe_forward takes them.  With expert_counts,
+    mean_probs, prob_grad and loss (all four) also the balance loss of that
+    choice, from the same reading of the logits."""
+    w = "moe_router_topk"
+    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    k = topk_ids.shape[-1]
+    balance, nbytes = (None, None, None, None), 0
+    if expert_counts is not None or mean_probs is not None or prob_grad is not None or loss is not None:
+        balance = _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss)
+        workspace, nbytes = _workspace(balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_router_topk(
+        lp, d, _rows(logits), _arg(w, "select_bias", select_bias, (E,), 4, optional=True), mp, score,
+        int(bool(renormalize)), M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), 4),
+        _arg(w, "topk_weights", topk_weights, (M, k), 4), coef, *balance,
+        workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(logits, stream)), w)
+
+
+def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_grad, loss, score=SCORE_SOFTMAX,
+                     token_mask=None, workspace=None, stream=None):
+    """Per-expert counts, mean probabilities and the load-balancing loss of
+    given expert ids, and the loss's gradient in the probabilities."""
+    w = "moe_balance_loss"
+    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    k = topk_ids.shape[-1]
+    balance = _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss)
+    workspace, nbytes = _workspace(balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_balance_loss(lp, d, _rows(logits), _arg(w, "topk_ids", topk_ids, (M, k), 4), mp, score, M, E, k,
+                                  coef, *balance, workspace.data_ptr(), nbytes, _raw_stream(logits, stream)), w)
+
+
+def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_grad=None, d_loss=None,
+                        score=SCORE_SOFTMAX, renormalize=True, token_mask=None, stream=None):
+    """The gradient of the logits, in their type, from that of the routing
+    weights and / or of the balance loss (a device scalar; None: 1)."""
+    w = "moe_router_backward"
+    if _dtype(w, "d_logits", d_logits) != _dtype(w, "logits", logits):
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: d_logits must have the type of logits")
+    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    k = topk_ids.shape[-1]
+    _check(lib().moe_router_backward(
+        lp, d, _rows(logits), _arg(w, "topk_ids", topk_ids, (M, k), 4), mp, score, int(bool(renormalize)), M, E, k,
+        _arg(w, "d_topk_weights", d_topk_weights, (M, k), 4, optional=True),
+        _arg(w, "prob_grad", prob_grad, (E,), 4, optional=True), _arg(w, "d_loss", d_loss, (1,), 4, optional=True),
+        _arg(w, "d_logits", d_logits, (M, E), 4 if d else 2), _raw_stream(logits, stream)), w)
+
+
+def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumulate=False, stream=None):
+    """y = alpha * x w^T + bias (+ y) of MX operands: x E4M3 [M, K] (x_elem 0)
+    or packed E2M1 [M, K/2] (1) with E8M0 x_sf [M, K/32]; w packed E2M1
+    [N, K/2] with w_sf [N, K/32]; y bf16 or fp32 [M, N]."""
+    f = "moe_linear_mx"
+    M, N, K = x.shape[0], w.shape[0], 2 * w.shape[-1]
+    d = _dtype(f, "y", y)
+    _check(lib().moe_linear_mx(
+        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), 1), _arg(f, "x_sf", x_sf, (M, K // 32), 1), x_elem,
+        _arg(f, "w", w, (N, K // 2), 1), _arg(f, "w_sf", w_sf, (N, K // 32), 1),
+        _arg(f, "alpha", alpha, (1,), 4, optional=True), _arg(f, "bias", bias, (N,), 4, optional=True), M, N, K,
+        int(bool(accumulate)), _arg(f, "y", y, (M, N), 4 if d else 2), d, _raw_stream(x, stream)), f)

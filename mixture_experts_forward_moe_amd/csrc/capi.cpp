@@ -546,4 +546,265 @@ moe_status_t moe_quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, int 
   return dev(launch_quantize_mx(x, rows, cols, elem, q, sf, (hipStream_t)stream));
 }
 
+// ---- around the routed experts -------------------------------------------
+
+namespace {
+
+bool dtype_ok(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F32; }
+bool score_ok(int s) { return s == MOE_SCORE_SOFTMAX || s == MOE_SCORE_SIGMOID; }
+bool unaligned16(const void* p) { return ((uintptr_t)p & 15) != 0; }
+bool unaligned4(const void* p) { return ((uintptr_t)p & 3) != 0; }
+
+// sizes both norm calls take
+moe_status_t norm_shape(int M, int H) {
+  if (M < 0 || H < 1) return MOE_ERR_INVALID_ARGUMENT;
+  return H % 8 != 0 || H > NORM_MAX_H ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// what the router calls share: sizes, types and the logits' layout
+moe_status_t router_shape(const void* logits, int dtype, int64_t* stride, int score, int M, int E, int top_k) {
+  if (M < 0 || E < 1 || top_k < 1 || !dtype_ok(dtype) || !score_ok(score)) return MOE_ERR_INVALID_ARGUMENT;
+  if (E > ROUTER_MAX_EXPERTS || top_k > ROUTER_MAX_TOP_K) return MOE_ERR_UNSUPPORTED;
+  if (top_k > E || (M > 0 && !logits) || (*stride != 0 && *stride < E)) return MOE_ERR_INVALID_ARGUMENT;
+  if ((int64_t)M * top_k > INT32_MAX) return MOE_ERR_UNSUPPORTED;  // the counts are int32
+  if (((uintptr_t)logits & (dtype == MOE_DTYPE_F32 ? 3 : 1)) != 0) return MOE_ERR_UNSUPPORTED;
+  if (*stride == 0) *stride = E;
+  return MOE_OK;
+}
+
+// Balance workspace: ticket and loss terms, then each workgroup's token
+// count, probability sums and route counts, all 256-byte aligned.
+struct BalanceLayout {
+  int partials;
+  size_t loss, tokens, probs, counts, total;
+};
+BalanceLayout balance_layout(int M, int E) {
+  BalanceLayout L;
+  L.partials = router_partials(M, E);
+  L.loss = 256;
+  L.tokens = align256(L.loss + sizeof(double) * balance_finish_blocks(E));
+  L.probs = align256(L.tokens + sizeof(int32_t) * (size_t)L.partials);
+  L.counts = align256(L.probs + sizeof(float) * (size_t)L.partials * E);
+  L.total = align256(L.counts + sizeof(int32_t) * (size_t)L.partials * E);
+  return L;
+}
+
+// One reading of the logits (choice and / or statistics), then the join.
+moe_status_t run_router(RouterParams& p, float coef, int32_t* counts, float* mean_probs, float* prob_grad,
+                        float* loss, void* workspace, size_t workspace_bytes, hipStream_t st) {
+  if (!counts) return p.M == 0 ? MOE_OK : dev(launch_router(p, st));
+  const BalanceLayout L = balance_layout((int)p.M, p.E);
+  if (!workspace || ((uintptr_t)workspace & 255) != 0 || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  uint8_t* b = (uint8_t*)workspace;
+  p.ticket = (unsigned*)b;
+  p.token_partial = (int32_t*)(b + L.tokens);
+  p.prob_partial = (float*)(b + L.probs);
+  p.count_partial = (int32_t*)(b + L.counts);
+  if (launch_router(p, st) != hipSuccess) return MOE_ERR_DEVICE;
+  BalanceParams f = {};
+  f.prob_partial = p.prob_partial;
+  f.count_partial = p.count_partial;
+  f.token_partial = p.token_partial;
+  f.partials = L.partials;
+  f.E = p.E;
+  f.top_k = p.top_k;
+  f.coef = coef;
+  f.counts = counts;
+  f.mean_probs = mean_probs;
+  f.prob_grad = prob_grad;
+  f.loss = loss;
+  f.loss_partial = (double*)(b + L.loss);
+  f.ticket = p.ticket;
+  return dev(launch_balance_finish(f, st));
+}
+
+}  // namespace
+
+moe_status_t moe_rmsnorm(const uint16_t* x, int64_t x_row_stride, const uint16_t* residual,
+                         int64_t residual_row_stride, const void* weight, moe_dtype_t weight_dtype, float eps, int M,
+                         int H, uint16_t* residual_out, uint16_t* y, int elem, uint8_t* q, uint8_t* q_sf, float* rstd,
+                         moe_stream_t stream) {
+  if (!dtype_ok(weight_dtype) || !(eps >= 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARGUMENT;
+  moe_status_t s = norm_shape(M, H);
+  if (s != MOE_OK) return s;
+  if ((x_row_stride != 0 && x_row_stride < H) || (residual_row_stride != 0 && residual_row_stride < H))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if ((q == NULL) != (q_sf == NULL) || (!q && !y) || (residual_out && !residual) || !weight)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (M > 0 && !x) return MOE_ERR_INVALID_ARGUMENT;
+  if (q && elem != 0 && elem != 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (q && H % 32 != 0) return MOE_ERR_UNSUPPORTED;
+  if (x_row_stride % 8 != 0 || residual_row_stride % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (unaligned16(x) || unaligned16(residual) || unaligned16(weight) || unaligned16(residual_out) || unaligned16(y) ||
+      unaligned16(q) || unaligned4(rstd))
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  NormParams p = {};
+  p.x = x;
+  p.x_row_stride = x_row_stride ? x_row_stride : H;
+  p.residual = residual;
+  p.residual_row_stride = residual_row_stride ? residual_row_stride : H;
+  p.weight = weight;
+  p.weight_f32 = weight_dtype == MOE_DTYPE_F32;
+  p.eps = eps;
+  p.M = M;
+  p.H = H;
+  p.residual_out = residual_out;
+  p.y = y;
+  p.elem = elem;
+  p.q = q;
+  p.q_sf = q_sf;
+  p.rstd = rstd;
+  return dev(launch_rmsnorm(p, (hipStream_t)stream));
+}
+
+size_t moe_rmsnorm_backward_workspace_size(int M, int H) {
+  if (norm_shape(M, H) != MOE_OK) return 0;
+  return align256(sizeof(float) * (size_t)norm_backward_partials(M) * H);
+}
+
+moe_status_t moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const void* weight,
+                                  moe_dtype_t weight_dtype, const float* rstd, const uint16_t* dh, int M, int H,
+                                  uint16_t* dx, float* dweight, void* workspace, size_t workspace_bytes,
+                                  moe_stream_t stream) {
+  if (!dtype_ok(weight_dtype)) return MOE_ERR_INVALID_ARGUMENT;
+  moe_status_t s = norm_shape(M, H);
+  if (s != MOE_OK) return s;
+  if (!weight || (M > 0 && (!dy || !h || !rstd || !dx))) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(dy) || unaligned16(h) || unaligned16(weight) || unaligned16(dh) || unaligned16(dx) ||
+      unaligned4(rstd) || unaligned4(dweight))
+    return MOE_ERR_UNSUPPORTED;
+  if (dweight && (!workspace || ((uintptr_t)workspace & 255) != 0 ||
+                  workspace_bytes < moe_rmsnorm_backward_workspace_size(M, H)))
+    return MOE_ERR_WORKSPACE;
+  NormBackwardParams p = {};
+  p.dy = dy;
+  p.h = h;
+  p.weight = weight;
+  p.weight_f32 = weight_dtype == MOE_DTYPE_F32;
+  p.rstd = rstd;
+  p.dh = dh;
+  p.M = M;
+  p.H = H;
+  p.dx = dx;
+  p.partial = dweight ? (float*)workspace : NULL;
+  return dev(launch_rmsnorm_backward(p, dweight, (hipStream_t)stream));
+}
+
+moe_status_t moe_router_topk(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                             const float* select_bias, const uint8_t* token_mask, moe_score_t score, int renormalize,
+                             int M, int E, int top_k, int32_t* topk_ids, float* topk_weights, float coef,
+                             int32_t* expert_counts, float* mean_probs, float* prob_grad, float* loss,
+                             void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  moe_status_t s = router_shape(logits, logits_dtype, &logits_row_stride, score, M, E, top_k);
+  if (s != MOE_OK) return s;
+  if (M > 0 && (!topk_ids || !topk_weights)) return MOE_ERR_INVALID_ARGUMENT;
+  const int given = !!expert_counts + !!mean_probs + !!prob_grad + !!loss;
+  if ((given != 0 && given != 4) || (given && !std::isfinite(coef))) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned4(select_bias) || unaligned4(topk_ids) || unaligned4(topk_weights)) return MOE_ERR_UNSUPPORTED;
+  RouterParams p = {};
+  p.logits = logits;
+  p.logits_f32 = logits_dtype == MOE_DTYPE_F32;
+  p.row_stride = logits_row_stride;
+  p.select_bias = select_bias;
+  p.token_mask = token_mask;
+  p.sigmoid = score == MOE_SCORE_SIGMOID;
+  p.renormalize = renormalize ? 1 : 0;
+  p.M = M;
+  p.E = E;
+  p.top_k = top_k;
+  p.select = 1;
+  p.ids = topk_ids;
+  p.weights = topk_weights;
+  return run_router(p, coef, expert_counts, mean_probs, prob_grad, loss, workspace, workspace_bytes,
+                    (hipStream_t)stream);
+}
+
+size_t moe_balance_workspace_size(int M, int E) {
+  if (M < 0 || E < 1 || E > ROUTER_MAX_EXPERTS) return 0;
+  return balance_layout(M, E).total;
+}
+
+moe_status_t moe_balance_loss(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                              const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score, int M, int E,
+                              int top_k, float coef, int32_t* expert_counts, float* mean_probs, float* prob_grad,
+                              float* loss, void* workspace, size_t workspace_bytes, moe_stream_t stream) {
+  moe_status_t s = router_shape(logits, logits_dtype, &logits_row_stride, score, M, E, top_k);
+  if (s != MOE_OK) return s;
+  if ((M > 0 && !topk_ids) || !expert_counts || !mean_probs || !prob_grad || !loss || !std::isfinite(coef))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned4(topk_ids)) return MOE_ERR_UNSUPPORTED;
+  RouterParams p = {};
+  p.logits = logits;
+  p.logits_f32 = logits_dtype == MOE_DTYPE_F32;
+  p.row_stride = logits_row_stride;
+  p.token_mask = token_mask;
+  p.sigmoid = score == MOE_SCORE_SIGMOID;
+  p.M = M;
+  p.E = E;
+  p.top_k = top_k;
+  p.ids = const_cast<int32_t*>(topk_ids);  // read only: select is 0
+  return run_router(p, coef, expert_counts, mean_probs, prob_grad, loss, workspace, workspace_bytes,
+                    (hipStream_t)stream);
+}
+
+moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
+                                 const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score,
+                                 int renormalize, int M, int E, int top_k, const float* d_topk_weights,
+                                 const float* prob_grad, const float* d_loss, void* d_logits, moe_stream_t stream) {
+  moe_status_t s = router_shape(logits, logits_dtype, &logits_row_stride, score, M, E, top_k);
+  if (s != MOE_OK) return s;
+  if ((!d_topk_weights && !prob_grad) || (d_loss && !prob_grad)) return MOE_ERR_INVALID_ARGUMENT;
+  if (M > 0 && (!d_logits || (d_topk_weights && !topk_ids))) return MOE_ERR_INVALID_ARGUMENT;
+  if (((uintptr_t)d_logits & (logits_dtype == MOE_DTYPE_F32 ? 3 : 1)) != 0 || unaligned4(d_topk_weights) ||
+      unaligned4(prob_grad) || unaligned4(d_loss) || unaligned4(topk_ids))
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0) return MOE_OK;
+  RouterBackwardParams p = {};
+  p.logits = logits;
+  p.logits_f32 = logits_dtype == MOE_DTYPE_F32;
+  p.row_stride = logits_row_stride;
+  p.ids = topk_ids;
+  p.token_mask = token_mask;
+  p.sigmoid = score == MOE_SCORE_SIGMOID;
+  p.renormalize = renormalize ? 1 : 0;
+  p.M = M;
+  p.E = E;
+  p.top_k = top_k;
+  p.d_weights = d_topk_weights;
+  p.prob_grad = prob_grad;
+  p.d_loss = d_loss;
+  p.d_logits = d_logits;
+  return dev(launch_router_backward(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, const uint8_t* w, const uint8_t* w_sf,
+                           const float* alpha, const float* bias, int M, int N, int K, int accumulate, void* y,
+                           moe_dtype_t y_dtype, moe_stream_t stream) {
+  if (M < 0 || N < 0 || K < 1 || K % 32 != 0 || (x_elem != 0 && x_elem != 1) || !dtype_ok(y_dtype))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (M > 0 && N > 0 && (!x || !x_sf || !w || !w_sf || !y)) return MOE_ERR_INVALID_ARGUMENT;
+  if (K > 1 << 24 || (int64_t)M * K >= (int64_t)1 << 40 || (int64_t)N * K >= (int64_t)1 << 41)
+    return MOE_ERR_UNSUPPORTED;
+  if (unaligned16(x) || unaligned16(w) || ((uintptr_t)y & (y_dtype == MOE_DTYPE_F32 ? 3 : 1)) != 0 ||
+      unaligned4(alpha) || unaligned4(bias))
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MOE_OK;
+  LinearParams p = {};
+  p.x = x;
+  p.x_sf = x_sf;
+  p.x_elem = x_elem;
+  p.w = w;
+  p.w_sf = w_sf;
+  p.alpha = alpha;
+  p.bias = bias;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.accumulate = accumulate ? 1 : 0;
+  p.y = y;
+  p.y_f32 = y_dtype == MOE_DTYPE_F32;
+  return dev(launch_linear_mx(p, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -139,4 +139,103 @@ hipError_t launch_quantize_nvfp4(const uint16_t* x, int64_t batches, int64_t row
 hipError_t launch_quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, int elem, uint8_t* q, uint8_t* sf,
                               hipStream_t stream);
 
+// residual addition + RMS norm (+ MX codes), and its gradients
+constexpr int NORM_MAX_H = 32768;
+struct NormParams {
+  const uint16_t* x;
+  int64_t x_row_stride;
+  const uint16_t* residual;  // NULL: none
+  int64_t residual_row_stride;
+  const void* weight;
+  int weight_f32;
+  float eps;
+  int64_t M;
+  int H;
+  uint16_t* residual_out;    // NULL: not stored (as y, q, rstd)
+  uint16_t* y;
+  int elem;
+  uint8_t *q, *q_sf;
+  float* rstd;
+};
+struct NormBackwardParams {
+  const uint16_t *dy, *h;
+  const void* weight;
+  int weight_f32;
+  const float* rstd;
+  const uint16_t* dh;        // NULL: none
+  int64_t M;
+  int H;
+  uint16_t* dx;
+  float* partial;            // [norm_backward_partials(M), H], or NULL: no weight gradient
+};
+int norm_backward_partials(int64_t M);
+hipError_t launch_rmsnorm(const NormParams& p, hipStream_t stream);
+hipError_t launch_rmsnorm_backward(const NormBackwardParams& p, float* dweight, hipStream_t stream);
+
+// router: choice, balance loss, gradients
+constexpr int ROUTER_MAX_EXPERTS = 1024;
+constexpr int ROUTER_MAX_TOP_K = 64;
+struct RouterParams {
+  const void* logits;
+  int logits_f32;
+  int64_t row_stride;
+  const float* select_bias;   // NULL: none
+  const uint8_t* token_mask;  // NULL: every token counts
+  int sigmoid, renormalize;
+  int64_t M;
+  int E, top_k;
+  int select;                 // 1: write ids and weights; 0: read ids
+  int32_t* ids;
+  float* weights;
+  float* prob_partial;        // balance statistics [workgroups, E], or NULL: none
+  int32_t* count_partial;     // [workgroups, E]
+  int32_t* token_partial;     // [workgroups]
+  unsigned* ticket;           // cleared here for the finishing launch
+};
+struct BalanceParams {
+  const float* prob_partial;
+  const int32_t* count_partial;
+  const int32_t* token_partial;
+  int partials;
+  int E, top_k;
+  float coef;
+  int32_t* counts;
+  float *mean_probs, *prob_grad, *loss;
+  double* loss_partial;       // [finishing workgroups]
+  unsigned* ticket;
+};
+struct RouterBackwardParams {
+  const void* logits;
+  int logits_f32;
+  int64_t row_stride;
+  const int32_t* ids;
+  const uint8_t* token_mask;
+  int sigmoid, renormalize;
+  int64_t M;
+  int E, top_k;
+  const float* d_weights;     // NULL: none
+  const float* prob_grad;     // NULL: none
+  const float* d_loss;        // NULL: 1
+  void* d_logits;
+};
+int router_partials(int64_t M, int E);
+int balance_finish_blocks(int E);
+hipError_t launch_router(const RouterParams& p, hipStream_t stream);
+hipError_t launch_balance_finish(const BalanceParams& p, hipStream_t stream);
+hipError_t launch_router_backward(const RouterBackwardParams& p, hipStream_t stream);
+
+// MX product without a plan
+struct LinearParams {
+  const uint8_t *x, *x_sf;
+  int x_elem;                 // 0 E4M3, 1 E2M1
+  const uint8_t *w, *w_sf;
+  const float* alpha;         // NULL: 1
+  const float* bias;          // NULL: none
+  int M, N, K;
+  int accumulate;
+  void* y;
+  int y_f32;
+};
+hipError_t launch_linear_mx(const LinearParams& p, hipStream_t stream);
+
 }  // namespace moe

@@ -1,0 +1,479 @@
+"""The operators around the routed experts on the GPU, each against its fp64
+form (tests/layer_ref.py), at the sizes, masks and values where they can go
+wrong.  Tolerances count roundings (U24: half a step of fp32, U8: of bf16)."""
+import numpy as np
+import pytest
+import torch
+
+import layer_ref as ref
+import mixture_experts_forward_moe_amd as moe
+import oracle
+from layer_ref import INF, U8, U24
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+NAN = float("nan")
+GUARD = 173  # byte that outputs and the room behind them start with
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def guarded(shape, dtype):
+    """(tensor, check): a GPU tensor with room behind it, all bytes GUARD;
+    check() asserts that the room is untouched."""
+    n = int(np.prod(shape)) * torch.empty(0, dtype=dtype).element_size()
+    room = torch.full((n + 512,), GUARD, dtype=torch.uint8, device="cuda")
+
+    def check():
+        assert bool((room[n:] == GUARD).all()), "written past the end"
+    return room[:n].view(dtype).view(shape), check
+
+
+def near(got, want, tol, what=""):
+    """Every |got - want| <= tol (tensors of tolerances), non-finite equal."""
+    got, want = got.cpu().double(), want.double()
+    tol = torch.as_tensor(tol, dtype=F64).expand(want.shape)
+    fin = torch.isfinite(want)
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    assert torch.equal(got[~fin & ~torch.isnan(want)], want[~fin & ~torch.isnan(want)]), what
+    over = ((got - want).abs() - tol)[fin]
+    if over.numel() and over.max() > 0:
+        i = int(over.argmax())
+        raise AssertionError(f"{what}: {got[fin][i]} against {want[fin][i]}, tolerance {tol[fin][i]}")
+
+
+# ------------------------------------------------------------------ norm
+
+# Sum of squares: a thread adds at most 96 products one after another, then at
+# most 6 + 16 steps join them; division, addition of eps, root and reciprocal
+# add 4 more roundings, and the square root halves what came before it.
+R_TOL = (96 + 22 + 4 + 2) * U24
+
+
+def norm_case(M, H, seed, std=2.0):
+    g = gen(seed)
+    x = torch.randn(M, H, generator=g).to(BF16)
+    res = (torch.randn(M, H, generator=g) * std).to(BF16)
+    return x, res, 1.0 + 0.2 * torch.randn(H, generator=g), g
+
+
+@pytest.mark.parametrize("M,H,residual,wdtype,elem", [
+    (1, 32, True, F32, 0), (1, 8, False, BF16, None), (3, 40, True, BF16, None), (5, 2048, False, F32, 1),
+    (8, 6144, True, BF16, 0), (17, 8224, True, F32, 0), (2, 32768, True, BF16, 1), (2050, 512, True, F32, 0),
+    (2051, 1024, False, BF16, 1), (2048, 1504, True, BF16, 0), (2049, 4128, True, F32, 0), (2500, 6144, True, BF16, 0),
+    (7, 16384, True, F32, None), (300, 4096, False, F32, 0),
+])
+def test_norm(M, H, residual, wdtype, elem):
+    say(f"norm M={M} H={H} residual={residual} {wdtype} elem={elem}")
+    x, res, w, _ = norm_case(M, H, M + H)
+    w = w.to(wdtype)
+    res = res if residual else None
+    h64, r64, y64 = ref.rmsnorm(x, res, w, 1e-5)
+    y, c1 = guarded((M, H), BF16)
+    h, c2 = guarded((M, H), BF16)
+    r, c3 = guarded((M,), F32)
+    q = sf = None
+    checks = [c1, c2, c3]
+    if elem is not None:
+        q, c4 = guarded((M, H if elem == 0 else H // 2), torch.uint8)
+        sf, c5 = guarded((M, H // 32), torch.uint8)
+        checks += [c4, c5]
+    moe.moe_rmsnorm(x.cuda(), w.cuda(), y=y, residual=None if res is None else res.cuda(),
+                    residual_out=h if residual else None, q=q, q_sf=sf, elem=elem or 0, rstd=r, eps=1e-5)
+    torch.cuda.synchronize()
+    for c in checks:
+        c()
+    if residual:
+        assert torch.equal(h.cpu(), h64)
+    near(r, r64, r64 * R_TOL, "rstd")
+    near(y, y64, y64.abs() * (U8 + R_TOL + 2 * U24) + 2.0 ** -133, "y")
+    if elem is not None:
+        rq, rs = oracle.mx_quantize_bf16(y.cpu().view(torch.int16).numpy().view(np.uint16), elem)
+        assert np.array_equal(sf.cpu().numpy(), rs) and np.array_equal(q.cpu().numpy(), rq)
+        # without y: the same codes
+        q2, sf2 = torch.empty_like(q), torch.empty_like(sf)
+        moe.moe_rmsnorm(x.cuda(), w.cuda(), residual=None if res is None else res.cuda(), q=q2, q_sf=sf2, elem=elem,
+                        eps=1e-5)
+        assert torch.equal(q, q2) and torch.equal(sf, sf2)
+
+
+def test_norm_strided_and_in_place():
+    say("norm strided, in place")
+    M, H = 37, 96
+    x, res, w, g = norm_case(M, H, 5)
+    wide = torch.randn(M, 3 * H, generator=g).to(BF16)
+    wide[:, H:2 * H] = x
+    xs = wide.cuda()[:, H:2 * H]
+    h64, _, y64 = ref.rmsnorm(x, res, w, 0.0)
+    stream = res.cuda()
+    y = torch.empty(M, H, dtype=BF16, device="cuda")
+    moe.moe_rmsnorm(xs, w.cuda(), y=y, residual=stream, residual_out=stream, eps=0.0)
+    assert torch.equal(stream.cpu(), h64)
+    near(y, y64, y64.abs() * (U8 + R_TOL), "y")
+    a = x.cuda()
+    moe.moe_rmsnorm(a, w.cuda(), y=a, residual=res.cuda(), eps=0.0)
+    assert torch.equal(a, y)
+
+
+def test_norm_values():
+    """Zero rows, infinities and NaN stay in their rows."""
+    say("norm values")
+    H = 64
+    x = torch.ones(5, H).to(BF16)
+    x[0] = 0
+    x[1, 3] = INF
+    x[2, 5] = NAN
+    x[3] = torch.finfo(BF16).tiny
+    w = torch.ones(H)
+    y = torch.empty(5, H, dtype=BF16, device="cuda")
+    moe.moe_rmsnorm(x.cuda(), w.cuda(), y=y, eps=1e-6)
+    got = y.cpu().float()
+    assert bool((got[0] == 0).all())
+    assert bool(torch.isnan(got[1, 3])) and bool((got[1, :3] == 0).all())   # rstd 0: 0 * inf, 0 * finite
+    assert bool(torch.isnan(got[2]).all())
+    assert bool((got[3] >= 0).all()) and bool((got[3] < 1e-30).all())
+    assert bool(((got[4] - 1).abs() <= U8).all())
+
+
+@pytest.mark.parametrize("M,H,dh,wdtype", [
+    (1, 8, False, F32), (1, 6144, True, BF16), (15, 40, True, F32), (33, 2048, True, BF16), (257, 4128, True, F32),
+    (100, 6144, False, BF16), (64, 8192, True, F32), (9, 8224, True, BF16), (5, 32768, True, F32),
+    (9000, 96, True, F32),
+])
+def test_norm_backward(M, H, dh, wdtype):
+    say(f"norm backward M={M} H={H} dh={dh} {wdtype}")
+    x, hid, w, g = norm_case(M, H, 3 * M + H)
+    w = w.to(wdtype)
+    dy = (torch.randn(M, H, generator=g) * 0.1).to(BF16)
+    d = (torch.randn(M, H, generator=g) * 0.1).to(BF16) if dh else None
+    r = (1 / torch.sqrt(hid.double().square().mean(-1) + 1e-6)).float()
+    dx64, dw64, size = ref.rmsnorm_backward(dy, hid, w, r, d)
+    dx, c1 = guarded((M, H), BF16)
+    dw, c2 = guarded((H,), F32)
+    args = (dy.cuda(), hid.cuda(), w.cuda(), r.cuda())
+    moe.moe_rmsnorm_backward(*args, dx, dw, dh=None if d is None else d.cuda())
+    torch.cuda.synchronize()
+    c1()
+    c2()
+    # dx: the mean is a sum like the forward's, the rest six roundings
+    near(dx, dx64, dx64.abs() * U8 + size * (R_TOL + 8 * U24) + 2.0 ** -133, "dx")
+    # dweight: three roundings a term; a workgroup adds M / P rows one after
+    # another, and P / 32 + 32 additions join the partial sums
+    P = max(1, min(512, (M + 15) // 16))
+    mag = (dy.double() * hid.double() * r.double()[:, None]).abs().sum(0)
+    near(dw, dw64, mag * (3 + -(-M // P) + P // 32 + 33) * U24, "dweight")
+    again, dw2 = torch.empty_like(dx), torch.empty_like(dw)
+    ws = torch.full((moe.rmsnorm_backward_workspace_size(M, H),), 255, dtype=torch.uint8, device="cuda")
+    moe.moe_rmsnorm_backward(*args, again, dw2, dh=None if d is None else d.cuda(), workspace=ws)
+    assert torch.equal(dx, again) and torch.equal(dw, dw2)
+    # without dweight, and in place of dy
+    inplace = dy.cuda()
+    moe.moe_rmsnorm_backward(inplace, *args[1:], inplace, dh=None if d is None else d.cuda())
+    assert torch.equal(inplace, dx)
+
+
+def test_norm_backward_of_nothing():
+    dw = torch.full((64,), 7.0, device="cuda")
+    e = torch.empty(0, 64, dtype=BF16, device="cuda")
+    moe.moe_rmsnorm_backward(e, e, torch.ones(64, device="cuda"), torch.empty(0, device="cuda"), e, dw)
+    assert bool((dw == 0).all())
+
+
+# ------------------------------------------------------------------ router
+
+def make_logits(M, E, dtype, g, masked=0.2):
+    l = torch.randn(M, E, generator=g) * 2 + torch.randn(E, generator=g)
+    if masked:
+        l[torch.rand(M, E, generator=g) < masked] = -INF
+        l[torch.rand(M, E, generator=g) < masked / 10] = NAN
+    return l.to(dtype)
+
+
+def weight_tol(l, E):
+    """Relative: exp of a difference with |d| U24 of its own rounding and one
+    step of expf, the sum's roundings, the quotients'."""
+    c = ref.clean(l)
+    c = torch.where(c > -1e30, c, 0.0)
+    return (2 * c.abs().amax(-1, keepdim=True) + E / 16 + 24) * U24
+
+
+SIZES = [(1, 1, 1), (3, 5, 5), (8, 256, 8), (16, 8, 2), (17, 60, 4), (33, 64, 8), (70, 65, 6), (45, 128, 17),
+         (1000, 159, 6), (531, 256, 8), (129, 257, 10), (40, 512, 64), (21, 1000, 33), (50, 1024, 8)]
+
+
+@pytest.mark.parametrize("M,E,k", SIZES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_router(M, E, k, dtype):
+    """Every score, normalisation, bias and mask at each size."""
+    g = gen(M * E + k)
+    l = make_logits(M, E, dtype, g, 0.2 if E > 8 else 0.0)
+    bias = torch.randn(E, generator=g) * 0.2
+    mask = (torch.rand(M, generator=g) < 0.7).to(torch.uint8)
+    lg = l.cuda()
+    for sigmoid in (0, 1):
+        for renorm in (False, True):
+            for b in (None, bias):
+                for m in (None, mask):
+                    say(f"router M={M} E={E} k={k} {dtype} sigmoid={sigmoid} renorm={renorm} "
+                        f"bias={b is not None} mask={m is not None}")
+                    ids, c1 = guarded((M, k), torch.int32)
+                    w, c2 = guarded((M, k), F32)
+                    moe.moe_router_topk(lg, ids, w, score=sigmoid, renormalize=renorm,
+                                        select_bias=None if b is None else b.cuda(),
+                                        token_mask=None if m is None else m.cuda())
+                    torch.cuda.synchronize()
+                    c1()
+                    c2()
+                    ids64, w64 = ref.router_topk(l, k, sigmoid, renorm, b, m)
+                    assert torch.equal(ids.cpu(), ids64)
+                    near(w, w64, w64 * weight_tol(l, E) + 1e-37, "weights")
+
+
+def test_router_ties_and_extremes():
+    say("router ties and extremes")
+    E, k = 200, 9
+    big = torch.finfo(F32).max
+    l = torch.zeros(12, E)
+    l[1] = -INF
+    l[2] = -INF
+    l[2, 77] = -big
+    l[3] = -big
+    l[4, ::3] = INF
+    l[5] = NAN
+    l[6] = -200.0                    # sigmoid scores below fp32's range
+    l[6, 50] = -190.0
+    l[7] = 1e-30
+    l[8, 10:] = -0.0                 # equal to 0
+    l[9] = torch.arange(E) % 4       # ties across lanes and registers
+    l[10] = torch.arange(E).float()
+    l[11] = -torch.arange(E).float()
+    for sigmoid in (0, 1):
+        for renorm in (False, True):
+            for bias in (None, torch.zeros(E)):
+                ids = torch.empty(12, k, dtype=torch.int32, device="cuda")
+                w = torch.empty(12, k, device="cuda")
+                moe.moe_router_topk(l.cuda(), ids, w, score=sigmoid, renormalize=renorm,
+                                    select_bias=None if bias is None else bias.cuda())
+                ids64, w64 = ref.router_topk(l, k, sigmoid, renorm, bias)
+                assert torch.equal(ids.cpu(), ids64), (sigmoid, renorm, bias is not None)
+                near(w, w64, w64 * weight_tol(l, E) + 2e-38, "weights")
+    # an infinite or NaN bias takes its expert out, or puts it first
+    bias = torch.zeros(E)
+    bias[3], bias[4], bias[5] = -INF, NAN, 1e30
+    ids = torch.empty(12, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(12, k, device="cuda")
+    moe.moe_router_topk(l.cuda(), ids, w, score=1, select_bias=bias.cuda())
+    assert torch.equal(ids.cpu(), ref.router_topk(l, k, 1, True, bias)[0])
+
+
+def test_router_strided_rows():
+    say("router strided rows")
+    g = gen(9)
+    for dtype in (F32, BF16):
+        for E, total, start in [(64, 80, 8), (63, 80, 3), (64, 81, 0)]:
+            wide = make_logits(30, total, dtype, g, 0.0)
+            l = wide[:, start:start + E]
+            lg = wide.cuda()[:, start:start + E]
+            ids = torch.empty(30, 6, dtype=torch.int32, device="cuda")
+            w = torch.empty(30, 6, device="cuda")
+            moe.moe_router_topk(lg, ids, w)
+            assert torch.equal(ids.cpu(), ref.router_topk(l, 6, 0, True)[0])
+            d = torch.empty(30, E, dtype=dtype, device="cuda")
+            moe.moe_router_backward(lg, ids, d, d_topk_weights=torch.ones_like(w) * 0.1, renormalize=False)
+            want, size = ref.router_backward(l, ids.cpu(), 0, False, torch.full((30, 6), 0.1))
+            near(d, want, want.abs() * (U8 if dtype == BF16 else U24) + size * weight_tol(l, E) * 3, "d_logits")
+
+
+@pytest.mark.parametrize("M,E,k", SIZES + [(0, 7, 2), (20000, 64, 6), (9001, 256, 8)])
+@pytest.mark.parametrize("sigmoid", [0, 1])
+def test_balance_and_gradient(M, E, k, sigmoid):
+    """The loss of the router's own choice (one call) equals that of given
+    ids bit for bit; the gradients of loss and weights together and alone."""
+    g = gen(7 * M + E + k)
+    dtype = BF16 if (M + E) % 2 else F32
+    l = make_logits(M, E, dtype, g, 0.1 if E > 8 else 0.0)
+    mask = (torch.rand(M, generator=g) < 0.8).to(torch.uint8) if M % 3 else None
+    coef, renorm = 0.3, bool(E % 2)
+    say(f"balance M={M} E={E} k={k} {dtype} sigmoid={sigmoid} mask={mask is not None} renorm={renorm}")
+    lg, mg = l.cuda(), None if mask is None else mask.cuda()
+    ids = torch.empty(M, k, dtype=torch.int32, device="cuda")
+    w = torch.empty(M, k, device="cuda")
+    outs = [(guarded((E,), torch.int32), guarded((E,), F32), guarded((E,), F32), guarded((1,), F32)) for _ in range(2)]
+    (counts, c1), (mean, c2), (grad, c3), (loss, c4) = outs[0]
+    moe.moe_router_topk(lg, ids, w, score=sigmoid, renormalize=renorm, token_mask=mg, coef=coef, expert_counts=counts,
+                        mean_probs=mean, prob_grad=grad, loss=loss)
+    n = moe.balance_workspace_size(M, E)
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(lg, ids, coef, *(o[0] for o in outs[1]), score=sigmoid, token_mask=mg, workspace=ws)
+    torch.cuda.synchronize()
+    for a, b in zip(*outs):
+        a[1]()
+        b[1]()
+        assert torch.equal(a[0], b[0])
+    ids64, _ = ref.router_topk(l, k, sigmoid, renorm, None, mask)
+    assert torch.equal(ids.cpu(), ids64)
+    n64, m64, g64, l64 = ref.balance(l, ids64, k, sigmoid, coef, mask)
+    assert torch.equal(counts.cpu().long(), n64)
+    tol = weight_tol(l, E).max().item() if M else 0.0
+    # a lane adds the probabilities of M / 512 / 16 tokens, six steps join a
+    # workgroup's; from there on fp64
+    near(mean, m64, m64 * (tol + (M / 8192 + 8) * U24) + 1e-37, "mean_probs")
+    near(grad, g64, g64.abs() * 2 * U24 + 1e-37, "prob_grad")
+    near(loss[0], l64, l64 * (tol + (M / 8192 + 10) * U24) + 1e-37, "loss")
+    if M == 0:
+        return
+    dw = torch.randn(M, k, generator=g)
+    dl = torch.tensor([1.7])
+    for a, b in ((dw, None), (None, grad), (dw, grad)):
+        d, check = guarded((M, E), dtype)
+        moe.moe_router_backward(lg, ids, d, d_topk_weights=None if a is None else a.cuda(), prob_grad=b,
+                                d_loss=None if b is None else dl.cuda(), score=sigmoid, renormalize=renorm,
+                                token_mask=mg)
+        torch.cuda.synchronize()
+        check()
+        want, size = ref.router_backward(l, ids64, sigmoid, renorm, a, None if b is None else b.cpu(), 1.7, mask)
+        near(d, want, want.abs() * (U8 if dtype == BF16 else U24) + size * 3 * weight_tol(l, E) + 1e-37, "d_logits")
+
+
+def test_balance_of_foreign_ids():
+    """Ids outside the experts, equal ids in a token, an empty mask."""
+    say("balance of foreign ids")
+    g = gen(3)
+    M, E, k = 40, 12, 4
+    l = torch.randn(M, E, generator=g)
+    ids = torch.randint(-2, E + 3, (M, k), generator=g, dtype=torch.int32)
+    ids[0] = 5
+    ids[1] = torch.tensor([2**31 - 1, -2**31, 0, 0])
+    out = [torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda"),
+           torch.empty(E, device="cuda"), torch.empty(1, device="cuda")]
+    moe.moe_balance_loss(l.cuda(), ids.cuda(), 1.0, *out, score=0)
+    n64, m64, g64, l64 = ref.balance(l, ids, k, 0, 1.0)
+    assert torch.equal(out[0].cpu().long(), n64)
+    near(out[3][0], l64, l64 * 64 * U24, "loss")
+    d = torch.empty(M, E, device="cuda")
+    dw = torch.randn(M, k, generator=g)
+    for renorm in (False, True):
+        for sigmoid in (0, 1):
+            moe.moe_router_backward(l.cuda(), ids.cuda(), d, d_topk_weights=dw.cuda(), score=sigmoid,
+                                    renormalize=renorm)
+            want, size = ref.router_backward(l, ids, sigmoid, renorm, dw)
+            near(d, want, size * 4 * weight_tol(l, E) + 1e-37, "d_logits")
+    mask = torch.zeros(M, dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(l.cuda(), ids.cuda(), 1.0, *out, token_mask=mask)
+    assert all(bool((o == 0).all()) for o in out)
+    moe.moe_router_backward(l.cuda(), ids.cuda(), d, prob_grad=out[2], token_mask=mask)
+    assert bool((d == 0).all())
+
+
+# ------------------------------------------------------------------ linear
+
+def mx(rows, K, elem, g, std=1.0):
+    v = (torch.randn(rows, K, generator=g) * std).to(BF16)
+    q, sf = oracle.mx_quantize_bf16(v.view(torch.int16).numpy().view(np.uint16), elem)
+    return torch.from_numpy(np.asarray(q)), torch.from_numpy(np.asarray(sf))
+
+
+def linear_tol(xv, wv, K, elem):
+    """fp32: a matrix instruction joins the sums of its 8-product groups to the
+    accumulator with two steps of 2^-23 of their size; K / 64 instructions and
+    the joins of split sums follow.  E4M3: inside a group of 8 consecutive
+    products the instruction keeps the bits down to 2^-13 of the power of two
+    of the largest one (measured: beside a product of 2^8 one of 2^-5 counts
+    and one of 2^-6 does not, for places 0..7 of a group; places in other
+    groups count down to 2^-27).  Each of 8 products so loses less than 2^-13
+    of the group's largest, which is at most the product of the group's
+    largest factors.  E2M1 products span 2^-2 .. 2^5.2: nothing is lost."""
+    tol = (xv.abs() @ wv.abs().t()) * (2 * (K / 64 + 16) * U24 * 2)
+    if elem == 0:
+        g = lambda v: v.abs().unflatten(-1, (-1, 8)).amax(-1)  # noqa: E731
+        tol = tol + 8 * 2.0 ** -13 * (g(xv) @ g(wv).t())
+    return tol
+
+
+def near_in_norm(got, want, u, elem, what):
+    """The 2-norm: `u` for the output's own rounding, and per group of 8
+    products, whose sum is about the largest one, 8 * 2^-13 of it (E4M3) or
+    the fp32 steps.  A wrong or missing 32-block of K = 8192 is 2^-4."""
+    got, want = got.cpu().double(), want.double()
+    rel = (torch.linalg.norm(got - want) / torch.linalg.norm(want)).item()
+    assert rel <= u + (2.0 ** -10 if elem == 0 else 2.0 ** -18), (what, rel)
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (1, 1, 32), (1, 16, 128), (3, 17, 96), (8, 4096, 6144), (16, 100, 2048), (17, 33, 160), (5, 640, 8192),
+    (32, 256, 512), (33, 1000, 1568), (64, 512, 4096), (65, 264, 256), (100, 130, 1024), (128, 128, 384),
+    (200, 2056, 1568), (256, 256, 512), (300, 515, 1536), (512, 1024, 2048), (1025, 768, 1024), (1300, 2304, 4096),
+    (2111, 1111, 736),
+])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_linear(M, N, K, elem):
+    say(f"linear M={M} N={N} K={K} elem={elem}")
+    g = gen(M + N + K)
+    xq, xs = mx(M, K, elem, g)
+    wq, ws = mx(N, K, 1, g, 0.02)
+    xv, wv = ref.mx_values(xq, xs, elem).cuda(), ref.mx_values(wq, ws, 1).cuda()
+    want = (xv @ wv.t().contiguous()).cpu()
+    tol = linear_tol(xv, wv, K, elem).cpu()
+    args = (xq.cuda(), xs.cuda(), wq.cuda(), ws.cuda())
+    y, check = guarded((M, N), BF16)
+    moe.moe_linear_mx(*args, y, x_elem=elem)
+    torch.cuda.synchronize()
+    check()
+    near(y, want, want.abs() * U8 + tol, "y")
+    near_in_norm(y, want, U8, elem, "y")
+    y32, check = guarded((M, N), F32)
+    bias = torch.randn(N, generator=g)
+    alpha = torch.tensor([0.75])
+    moe.moe_linear_mx(*args, y32, x_elem=elem, alpha=alpha.cuda(), bias=bias.cuda())
+    torch.cuda.synchronize()
+    check()
+    full = want * 0.75 + bias.double()
+    near(y32, full, tol + (full.abs() + want.abs()) * 2 * U24, "y fp32")
+    near_in_norm(y32, full, U24, elem, "y fp32")
+    for dtype, u in ((BF16, U8), (F32, U24)):
+        old = torch.randn(M, N, generator=g).to(dtype)
+        acc = old.cuda()
+        moe.moe_linear_mx(*args, acc, x_elem=elem, bias=bias.cuda(), accumulate=True)
+        full = want + bias.double() + old.double()
+        near(acc, full, full.abs() * u + tol + (want.abs() + bias.double().abs()) * 2 * U24, "accumulated")
+    again = torch.empty_like(y)
+    moe.moe_linear_mx(*args, again, x_elem=elem)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 64, 512), (300, 512, 1024), (600, 700, 2080)])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_linear_rows_keep_to_themselves(M, N, K, elem):
+    """NaN and large scales in one row reach that row alone; E8M0 codes over
+    the whole range; offset views of the scale arrays."""
+    say(f"linear rows M={M} N={N} K={K} elem={elem}")
+    g = gen(1)
+    xq, xs = mx(M, K, elem, g)
+    wq, ws = mx(N, K, 1, g)
+    xs[1, 1] = 255          # NaN
+    xs[2] = 254 - 20        # 2^107: products stay finite
+    xs[3] = 0               # 2^-127
+    ws[5, 0] = 255
+    ws[6] = 2
+    buf = torch.zeros(xs.numel() + 1, dtype=torch.uint8, device="cuda")
+    xsd = buf[1:].view(xs.shape)  # scale rows need no alignment
+    xsd.copy_(xs)
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear_mx(xq.cuda(), xsd, wq.cuda(), ws.cuda(), y, x_elem=elem)
+    got = y.cpu()
+    assert bool(torch.isnan(got[1]).all()) and bool(torch.isnan(got[:, 5]).all())
+    ok_m = torch.arange(M) != 1
+    ok_n = torch.arange(N) != 5
+    xs[1, 1] = 127
+    ws[5, 0] = 127
+    xv, wv = ref.mx_values(xq, xs, elem).cuda(), ref.mx_values(wq, ws, 1).cuda()
+    want = (xv @ wv.t().contiguous()).cpu()
+    tol = linear_tol(xv, wv, K, elem).cpu() + want.abs() * U24 + 2.0 ** -126  # below fp32's normal range: flushed or kept
+    near(got[ok_m][:, ok_n], want[ok_m][:, ok_n], tol[ok_m][:, ok_n], "y")
