@@ -600,9 +600,9 @@ moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, i
  * [M, N] by y_dtype.  The products accumulate in fp32; alpha, bias and the
  * accumulation onto y are fp32 steps, and y is rounded once.  M, N >= 0; K a
  * positive multiple of 32 (else MOE_ERR_INVALID_ARGUMENT).  x and w 16-byte
- * aligned, y aligned to its elements, K at most 2^24, N * K/2 and
- * M * K below 2^40 (else MOE_ERR_UNSUPPORTED).  Each output is one sum in an order that depends
- * on the shape alone: reproducible bit for bit. */
+ * aligned, y aligned to its elements, K at most 2^20, M and N at most 2^26, M * N
+ * at most 2^36 (else MOE_ERR_UNSUPPORTED).  Each output is one sum in an order that
+ * depends on the shape alone: reproducible bit for bit. */
 moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, const uint8_t* w, const uint8_t* w_sf,
                            const float* alpha, const float* bias, int M, int N, int K, int accumulate, void* y,
                            moe_dtype_t y_dtype, moe_stream_t stream);

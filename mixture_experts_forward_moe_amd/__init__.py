@@ -124,15 +124,14 @@ def _check(status: int, where: str):
 
 def _ptr(t):
     """device pointer of a tensor (or None)"""
-    if t is None:
-        return None
-    return ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream=None):
+    if stream is not None:
+        return stream.cuda_stream
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def route_slots(M: int, top_k: int, num_local_experts: int, tile: int) -> int:
@@ -352,52 +351,70 @@ def moe_quantize_mx(x, rows: int, cols: int, elem: int, q, sf, stream=None):
 
 # ---- around the routed experts: norm, router, balance loss, linear ----------
 
-def _arg(where: str, name: str, t, shape, size: int, optional=False, strided=False):
-    """The device address of tensor `t`, checked against the shape and the
-    element size the call reads or writes; `strided`: rows may be apart.
-    An optional tensor may be None."""
+def _refuse(where, name, t, shape, size, dev, strided):
     if t is None:
-        if optional:
-            return None
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} is required")
-    if tuple(t.shape) != shape or t.element_size() != size:
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be {shape} of {size}-byte elements, "
-                                             f"is {tuple(t.shape)} of {t.element_size()}")
-    if not (t.stride(-1) == 1 or shape[-1] == 1 if strided else t.is_contiguous()):
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be contiguous" + (" in a row" if strided else ""))
-    if not t.is_cuda:
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be on the GPU")
+        what = "is required"
+    elif t.shape != shape or t.element_size() != size:
+        what = f"must be {shape} of {size}-byte elements, is {tuple(t.shape)} of {t.element_size()}"
+    elif not (t.is_contiguous() or strided and t.stride(-1) == 1):
+        what = "must be contiguous" + (" in a row" if strided else "")
+    else:
+        what = "must be on the GPU, with the call's other tensors"
+    raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} {what}")
+
+
+def _arg(where: str, name: str, t, shape, size: int, dev: int):
+    """The device address of tensor `t`, checked against the shape, the element
+    size and the device that the call takes it with."""
+    if t is None or t.shape != shape or t.element_size() != size or t.get_device() != dev or dev < 0 \
+            or not t.is_contiguous():
+        _refuse(where, name, t, shape, size, dev, False)
     return t.data_ptr()
 
 
-def _rows(t):
-    """Row stride in elements of a [rows, columns] tensor (0: contiguous)."""
-    return 0 if t is None or t.is_contiguous() else t.stride(0)
+def _opt(where, name, t, shape, size, dev):
+    """The same of a tensor that may be None."""
+    return None if t is None else _arg(where, name, t, shape, size, dev)
+
+
+def _rows(where, name, t, shape, size, dev):
+    """(address, row stride in elements; 0: contiguous) of a [rows, columns]
+    tensor whose rows may be apart."""
+    if t is not None and t.shape == shape and t.element_size() == size and t.get_device() == dev and dev >= 0:
+        if t.is_contiguous():
+            return t.data_ptr(), 0
+        if t.stride(1) == 1 or shape[1] == 1:
+            return t.data_ptr(), t.stride(0)
+    _refuse(where, name, t, shape, size, dev, True)
 
 
 def _dtype(where: str, name: str, t) -> int:
     """moe_dtype_t of a floating tensor (bf16 also as 16-bit integers)."""
-    import torch
-    if t.dtype == torch.float32:
+    d = t.dtype
+    if d.itemsize == 4 and d.is_floating_point:
         return DTYPE_F32
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
+    if d.itemsize == 2 and str(d) != "torch.float16":
         return DTYPE_BF16
     raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be bf16 or fp32, is {t.dtype}")
 
 
-def _raw_stream(t, stream):
-    """The stream of a call on `t`'s device."""
+def _raw_stream(where, dev, stream):
+    """The stream of a call on device `dev`, which must be the current one."""
     import torch
-    return (stream if stream is not None else torch.cuda.current_stream(t.device)).cuda_stream
+    if torch.cuda.current_device() != dev:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: the tensors are on cuda:{dev}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _workspace(nbytes: int, given, t, stream):
+def _workspace(where, nbytes: int, given, t, stream):
     """(tensor, bytes): the caller's workspace, or one from torch's allocator,
     which is told of a stream other than the one it allocates for."""
     if given is None:
         given = _alloc(nbytes, t.device)
         if stream is not None:
             given.record_stream(stream)
+    elif given.get_device() != t.get_device() or not given.is_contiguous():
+        _refuse(where, "workspace", given, given.shape, given.element_size(), t.get_device(), False)
     return given, given.numel() * given.element_size()
 
 
@@ -407,16 +424,16 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
     and y's MX codes, in one pass (see moe_rmsnorm in moe.h).  x, residual
     bf16 [M, H], rows may be strided; weight bf16 or fp32 [H]."""
     w = "moe_rmsnorm"
-    M, H = x.shape
+    M, H = shape = x.shape
+    dev = x.get_device()
     wd = _dtype(w, "weight", weight)
+    xp, xs = _rows(w, "x", x, shape, 2, dev)
+    rp, rs = (None, 0) if residual is None else _rows(w, "residual", residual, shape, 2, dev)
     _check(lib().moe_rmsnorm(
-        _arg(w, "x", x, (M, H), 2, strided=True), _rows(x),
-        _arg(w, "residual", residual, (M, H), 2, optional=True, strided=True), _rows(residual),
-        _arg(w, "weight", weight, (H,), 4 if wd else 2), wd, eps, M, H,
-        _arg(w, "residual_out", residual_out, (M, H), 2, optional=True), _arg(w, "y", y, (M, H), 2, optional=True),
-        elem, _arg(w, "q", q, (M, H if elem == 0 else H // 2), 1, optional=True),
-        _arg(w, "q_sf", q_sf, (M, H // 32), 1, optional=True), _arg(w, "rstd", rstd, (M,), 4, optional=True),
-        _raw_stream(x, stream)), w)
+        xp, xs, rp, rs, _arg(w, "weight", weight, (H,), 4 if wd else 2, dev), wd, eps, M, H,
+        _opt(w, "residual_out", residual_out, shape, 2, dev), _opt(w, "y", y, shape, 2, dev), elem,
+        _opt(w, "q", q, (M, H if elem == 0 else H // 2), 1, dev), _opt(w, "q_sf", q_sf, (M, H // 32), 1, dev),
+        _opt(w, "rstd", rstd, (M,), 4, dev), _raw_stream(w, dev, stream)), w)
 
 
 def rmsnorm_backward_workspace_size(M: int, H: int) -> int:
@@ -427,32 +444,28 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     """Gradients of moe_rmsnorm's rows and weight.  A workspace (only with
     dweight) is taken from `workspace`, or allocated here when None."""
     w = "moe_rmsnorm_backward"
-    M, H = dy.shape
+    M, H = shape = dy.shape
+    dev = dy.get_device()
     wd = _dtype(w, "weight", weight)
-    nbytes = 0
+    args = (_arg(w, "dy", dy, shape, 2, dev), _arg(w, "h", h, shape, 2, dev),
+            _arg(w, "weight", weight, (H,), 4 if wd else 2, dev), wd, _arg(w, "rstd", rstd, (M,), 4, dev),
+            _opt(w, "dh", dh, shape, 2, dev), M, H, _arg(w, "dx", dx, shape, 2, dev),
+            _opt(w, "dweight", dweight, (H,), 4, dev))
+    st = _raw_stream(w, dev, stream)
+    wp, nbytes = None, 0
     if dweight is not None:
-        workspace, nbytes = _workspace(rmsnorm_backward_workspace_size(M, H), workspace, dy, stream)
-    _check(lib().moe_rmsnorm_backward(
-        _arg(w, "dy", dy, (M, H), 2), _arg(w, "h", h, (M, H), 2), _arg(w, "weight", weight, (H,), 4 if wd else 2), wd,
-        _arg(w, "rstd", rstd, (M,), 4), _arg(w, "dh", dh, (M, H), 2, optional=True), M, H,
-        _arg(w, "dx", dx, (M, H), 2), _arg(w, "dweight", dweight, (H,), 4, optional=True),
-        workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(dy, stream)), w)
-
-
-def _router_args(w, logits, token_mask):
-    M, E = logits.shape
-    d = _dtype(w, "logits", logits)
-    return M, E, d, _arg(w, "logits", logits, (M, E), 4 if d else 2, strided=True), \
-        _arg(w, "token_mask", token_mask, (M,), 1, optional=True)
-
-
-def _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss):
-    return (_arg(w, "expert_counts", expert_counts, (E,), 4), _arg(w, "mean_probs", mean_probs, (E,), 4),
-            _arg(w, "prob_grad", prob_grad, (E,), 4), _arg(w, "loss", loss, (1,), 4))
+        workspace, nbytes = _workspace(w, rmsnorm_backward_workspace_size(M, H), workspace, dy, stream)
+        wp = workspace.data_ptr()
+    _check(lib().moe_rmsnorm_backward(*args, wp, nbytes, st), w)
 
 
 def balance_workspace_size(M: int, E: int) -> int:
     return lib().moe_balance_workspace_size(M, E)
+
+
+def _balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss):
+    return (_arg(w, "expert_counts", expert_counts, (E,), 4, dev), _arg(w, "mean_probs", mean_probs, (E,), 4, dev),
+            _arg(w, "prob_grad", prob_grad, (E,), 4, dev), _arg(w, "loss", loss, (1,), 4, dev))
 
 
 def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renormalize=True, select_bias=None,
@@ -463,17 +476,21 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
     mean_probs, prob_grad and loss (all four) also the balance loss of that
     choice, from the same reading of the logits."""
     w = "moe_router_topk"
-    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    M, E = logits.shape
     k = topk_ids.shape[-1]
-    balance, nbytes = (None, None, None, None), 0
-    if expert_counts is not None or mean_probs is not None or prob_grad is not None or loss is not None:
-        balance = _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss)
-        workspace, nbytes = _workspace(balance_workspace_size(M, E), workspace, logits, stream)
-    _check(lib().moe_router_topk(
-        lp, d, _rows(logits), _arg(w, "select_bias", select_bias, (E,), 4, optional=True), mp, score,
-        int(bool(renormalize)), M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), 4),
-        _arg(w, "topk_weights", topk_weights, (M, k), 4), coef, *balance,
-        workspace.data_ptr() if nbytes else None, nbytes, _raw_stream(logits, stream)), w)
+    dev = logits.get_device()
+    d = _dtype(w, "logits", logits)
+    lp, ls = _rows(w, "logits", logits, (M, E), 4 if d else 2, dev)
+    args = (lp, d, ls, _opt(w, "select_bias", select_bias, (E,), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev),
+            score, 1 if renormalize else 0, M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev),
+            _arg(w, "topk_weights", topk_weights, (M, k), 4, dev), coef)
+    st = _raw_stream(w, dev, stream)
+    if expert_counts is None and mean_probs is None and prob_grad is None and loss is None:
+        _check(lib().moe_router_topk(*args, None, None, None, None, None, 0, st), w)
+        return
+    balance = _balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss)
+    workspace, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_router_topk(*args, *balance, workspace.data_ptr(), nbytes, st), w)
 
 
 def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_grad, loss, score=SCORE_SOFTMAX,
@@ -481,12 +498,16 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     """Per-expert counts, mean probabilities and the load-balancing loss of
     given expert ids, and the loss's gradient in the probabilities."""
     w = "moe_balance_loss"
-    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    M, E = logits.shape
     k = topk_ids.shape[-1]
-    balance = _balance_args(w, E, expert_counts, mean_probs, prob_grad, loss)
-    workspace, nbytes = _workspace(balance_workspace_size(M, E), workspace, logits, stream)
-    _check(lib().moe_balance_loss(lp, d, _rows(logits), _arg(w, "topk_ids", topk_ids, (M, k), 4), mp, score, M, E, k,
-                                  coef, *balance, workspace.data_ptr(), nbytes, _raw_stream(logits, stream)), w)
+    dev = logits.get_device()
+    d = _dtype(w, "logits", logits)
+    lp, ls = _rows(w, "logits", logits, (M, E), 4 if d else 2, dev)
+    args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev),
+            score, M, E, k, coef, *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
+    st = _raw_stream(w, dev, stream)
+    workspace, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_balance_loss(*args, workspace.data_ptr(), nbytes, st), w)
 
 
 def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_grad=None, d_loss=None,
@@ -494,15 +515,19 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
     """The gradient of the logits, in their type, from that of the routing
     weights and / or of the balance loss (a device scalar; None: 1)."""
     w = "moe_router_backward"
-    if _dtype(w, "d_logits", d_logits) != _dtype(w, "logits", logits):
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: d_logits must have the type of logits")
-    M, E, d, lp, mp = _router_args(w, logits, token_mask)
+    M, E = logits.shape
     k = topk_ids.shape[-1]
+    dev = logits.get_device()
+    d = _dtype(w, "logits", logits)
+    if _dtype(w, "d_logits", d_logits) != d:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: d_logits must have the type of logits")
+    size = 4 if d else 2
+    lp, ls = _rows(w, "logits", logits, (M, E), size, dev)
     _check(lib().moe_router_backward(
-        lp, d, _rows(logits), _arg(w, "topk_ids", topk_ids, (M, k), 4), mp, score, int(bool(renormalize)), M, E, k,
-        _arg(w, "d_topk_weights", d_topk_weights, (M, k), 4, optional=True),
-        _arg(w, "prob_grad", prob_grad, (E,), 4, optional=True), _arg(w, "d_loss", d_loss, (1,), 4, optional=True),
-        _arg(w, "d_logits", d_logits, (M, E), 4 if d else 2), _raw_stream(logits, stream)), w)
+        lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev), score,
+        1 if renormalize else 0, M, E, k, _opt(w, "d_topk_weights", d_topk_weights, (M, k), 4, dev),
+        _opt(w, "prob_grad", prob_grad, (E,), 4, dev), _opt(w, "d_loss", d_loss, (1,), 4, dev),
+        _arg(w, "d_logits", d_logits, (M, E), size, dev), _raw_stream(w, dev, stream)), w)
 
 
 def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumulate=False, stream=None):
@@ -511,9 +536,10 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
     [N, K/2] with w_sf [N, K/32]; y bf16 or fp32 [M, N]."""
     f = "moe_linear_mx"
     M, N, K = x.shape[0], w.shape[0], 2 * w.shape[-1]
+    dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_mx(
-        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), 1), _arg(f, "x_sf", x_sf, (M, K // 32), 1), x_elem,
-        _arg(f, "w", w, (N, K // 2), 1), _arg(f, "w_sf", w_sf, (N, K // 32), 1),
-        _arg(f, "alpha", alpha, (1,), 4, optional=True), _arg(f, "bias", bias, (N,), 4, optional=True), M, N, K,
-        int(bool(accumulate)), _arg(f, "y", y, (M, N), 4 if d else 2), d, _raw_stream(x, stream)), f)
+        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), 1, dev), _arg(f, "x_sf", x_sf, (M, K // 32), 1, dev), x_elem,
+        _arg(f, "w", w, (N, K // 2), 1, dev), _arg(f, "w_sf", w_sf, (N, K // 32), 1, dev),
+        _opt(f, "alpha", alpha, (1,), 4, dev), _opt(f, "bias", bias, (N,), 4, dev), M, N, K,
+        1 if accumulate else 0, _arg(f, "y", y, (M, N), 4 if d else 2, dev), d, _raw_stream(f, dev, stream)), f)

@@ -784,8 +784,8 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
   if (M < 0 || N < 0 || K < 1 || K % 32 != 0 || (x_elem != 0 && x_elem != 1) || !dtype_ok(y_dtype))
     return MOE_ERR_INVALID_ARGUMENT;
   if (M > 0 && N > 0 && (!x || !x_sf || !w || !w_sf || !y)) return MOE_ERR_INVALID_ARGUMENT;
-  if (K > 1 << 24 || (int64_t)M * K >= (int64_t)1 << 40 || (int64_t)N * K >= (int64_t)1 << 41)
-    return MOE_ERR_UNSUPPORTED;
+  // 32-bit offsets in a tile, launch sizes
+  if (K > 1 << 20 || M > 1 << 26 || N > 1 << 26 || (int64_t)M * N > (int64_t)1 << 36) return MOE_ERR_UNSUPPORTED;
   if (unaligned16(x) || unaligned16(w) || ((uintptr_t)y & (y_dtype == MOE_DTYPE_F32 ? 3 : 1)) != 0 ||
       unaligned4(alpha) || unaligned4(bias))
     return MOE_ERR_UNSUPPORTED;

@@ -115,6 +115,7 @@ def test_layer_replayed_from_a_graph():
     another layer in between; every replay equals the eager result."""
     say("layer graph")
     L, other = Layer(70), Layer(90, seed=2)
+    torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
         L.forward()
@@ -160,6 +161,7 @@ def test_layers_on_two_streams():
         torch.cuda.synchronize()
         want.append(L.results())
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
     for i in range(3):
         for L, s in zip(layers, streams):
             with torch.cuda.stream(s):

@@ -124,7 +124,7 @@ LINEAR = dict(x=F, x_sf=F, elem=0, w=F, w_sf=F, alpha=None, bias=None, M=4, N=16
     (dict(y=None), INVALID), (dict(elem=2), INVALID), (dict(K=48), INVALID), (dict(K=0), INVALID), (dict(M=-1), INVALID),
     (dict(N=-1), INVALID), (dict(d=2), INVALID), (dict(x=F + 8), UNSUPPORTED), (dict(w=F + 8), UNSUPPORTED),
     (dict(y=ODD), UNSUPPORTED), (dict(d=1, y=F + 2), UNSUPPORTED), (dict(alpha=F + 2), UNSUPPORTED),
-    (dict(bias=F + 2), UNSUPPORTED), (dict(K=1 << 25), UNSUPPORTED), (dict(M=1 << 30, K=1 << 11), UNSUPPORTED),
+    (dict(bias=F + 2), UNSUPPORTED), (dict(K=(1 << 20) + 32), UNSUPPORTED), (dict(M=1 << 26, N=2048), UNSUPPORTED), (dict(N=(1 << 26) + 1), UNSUPPORTED),
     (dict(M=0), OK), (dict(N=0), OK), (dict(M=0, x=None, y=None), OK),
 ])
 def test_linear(change, status):
