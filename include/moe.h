@@ -484,7 +484,7 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
  * residual_out may be the (contiguous) residual itself or x, and y may be x;
  * other overlaps are not allowed.  h is rounded before it is normalised, so
  * that the backward pass, which reads the stored h, differentiates what ran.
- * 0 <= eps < inf.  H a multiple of 8 (of 32 with q), at most 65536; row
+ * 0 <= eps < inf.  H a multiple of 8 (of 32 with q), at most 16384; row
  * strides multiples of 8; bf16 arrays, weight and q 16-byte aligned (else
  * MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_rmsnorm(const uint16_t* x, int64_t x_row_stride, const uint16_t* residual,

@@ -655,12 +655,13 @@ moe_status_t moe_rmsnorm(const uint16_t* x, int64_t x_row_stride, const uint16_t
   p.q = q;
   p.q_sf = q_sf;
   p.rstd = rstd;
+  p.past_caches = norm_past_caches(M, H);
   return dev(launch_rmsnorm(p, (hipStream_t)stream));
 }
 
 size_t moe_rmsnorm_backward_workspace_size(int M, int H) {
   if (norm_shape(M, H) != MOE_OK) return 0;
-  return align256(sizeof(float) * (size_t)norm_backward_partials(M) * H);
+  return align256(sizeof(float) * (size_t)norm_backward_partials(M, H) * H);
 }
 
 moe_status_t moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const void* weight,
@@ -688,6 +689,7 @@ moe_status_t moe_rmsnorm_backward(const uint16_t* dy, const uint16_t* h, const v
   p.H = H;
   p.dx = dx;
   p.partial = dweight ? (float*)workspace : NULL;
+  p.past_caches = norm_past_caches(M, H);
   return dev(launch_rmsnorm_backward(p, dweight, (hipStream_t)stream));
 }
 

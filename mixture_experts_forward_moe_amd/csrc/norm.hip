@@ -65,6 +65,20 @@ DEV u32x4_t pack8(const float (&f)[8]) {
   return v;
 }
 
+// 16 bytes of a row; PAST: past the caches, where the rows are more than they
+// hold (a consumer would find none of them there)
+template <bool PAST>
+DEV u32x4_t get16(const uint16_t* p) {
+  const u32x4_t* q = reinterpret_cast<const u32x4_t*>(p);
+  if constexpr (PAST) return __builtin_nontemporal_load(q);
+  else return *q;
+}
+template <bool PAST>
+DEV void put16(uint16_t* p, const u32x4_t& v) {
+  if constexpr (PAST) __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(p));
+  else *reinterpret_cast<u32x4_t*>(p) = v;
+}
+
 // eight weights from column c
 DEV void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
   if (f32) {
@@ -81,9 +95,9 @@ DEV void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
 }
 
 // T threads a row (64: four rows a workgroup), up to VPT vectors a thread.
-template <int T, int VPT>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(const NormParams a) {
-  constexpr int ROWS = T < 256 ? 256 / T : 1;
+template <int T, int VPT, bool PAST>
+__global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormParams a) {
+  constexpr int ROWS = T < 128 ? 256 / T : 1;
   __shared__ float red[2][T > 64 ? T / 64 : 1];
   const int t = threadIdx.x % T;
   const int nv = a.H / 8;
@@ -97,14 +111,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(const NormPa
     for (int i = 0; i < VPT; i++) {
       const int v = t + T * i;
       h[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (v < nv) h[i] = *reinterpret_cast<const u32x4_t*>(x + 8 * v);
+      if (v < nv) h[i] = get16<PAST>(x + 8 * v);
     }
     if (res) {
 #pragma unroll
       for (int i = 0; i < VPT; i++) {
         const int v = t + T * i;
         rv[i] = u32x4_t{0u, 0u, 0u, 0u};
-        if (v < nv) rv[i] = *reinterpret_cast<const u32x4_t*>(res + 8 * v);
+        if (v < nv) rv[i] = get16<PAST>(res + 8 * v);
       }
     }
     float s8[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // short chains: a closer sum
@@ -132,14 +146,14 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(const NormPa
     for (int i = 0; i < VPT; i++) {
       const int v = t + T * i;
       if (v >= nv) continue;
-      if (a.residual_out) *reinterpret_cast<u32x4_t*>(a.residual_out + row * a.H + 8 * v) = h[i];
+      if (a.residual_out) put16<PAST>(a.residual_out + row * a.H + 8 * v, h[i]);
       float f[8], w[8];
       unpack8(h[i], f);
       load_weight8(a.weight, a.weight_f32, 8 * v, w);
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] = f[j] * r * w[j];
+      for (int j = 0; j < 8; j++) f[j] = f[j] * w[j] * r;  // (h w is exact for a bf16 weight)
       const u32x4_t y = pack8(f);
-      if (a.y) *reinterpret_cast<u32x4_t*>(a.y + row * a.H + 8 * v) = y;
+      if (a.y) put16<PAST>(a.y + row * a.H + 8 * v, y);
       if (a.q) {
         unpack8(y, f);  // quantised from the bf16 value, as a separate pass would
         float m = 0.0f;
@@ -171,18 +185,21 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void rmsnorm_kernel(const NormPa
 
 template <int T, int VPT>
 hipError_t launch_norm(const NormParams& p, hipStream_t s) {
-  constexpr int ROWS = T < 256 ? 256 / T : 1;
+  constexpr int ROWS = T < 128 ? 256 / T : 1;
   const int64_t blocks = (p.M + ROWS - 1) / ROWS;
-  rmsnorm_kernel<T, VPT><<<(unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), T < 256 ? 256 : T, 0, s>>>(p);
+  const unsigned grid = (unsigned)(blocks < 1 << 20 ? blocks : 1 << 20);
+  if (p.past_caches) rmsnorm_kernel<T, VPT, true><<<grid, T < 128 ? 256 : T, 0, s>>>(p);
+  else rmsnorm_kernel<T, VPT, false><<<grid, T < 128 ? 256 : T, 0, s>>>(p);
   return hipGetLastError();
 }
 
 // Rows are walked by a fixed set of workgroups (row b, b + P, ...), each
 // keeping its columns' sums of dy h r in registers: the weight gradient costs
 // one [P, H] array of partial sums instead of a second pass over the rows.
-template <int T, int VPT>
+// The next row's loads go out before this row's sum is joined.
+template <int T, int VPT, bool PAST>
 __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardParams a) {
-  __shared__ float red[2][T / 64];
+  __shared__ float red[2][T > 64 ? T / 64 : 1];
   const int t = threadIdx.x;
   const int nv = a.H / 8;
   float w[VPT][8], acc[VPT][8];
@@ -192,31 +209,44 @@ __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardP
     for (int j = 0; j < 8; j++) w[i][j] = acc[i][j] = 0.0f;
     if (t + T * i < nv) load_weight8(a.weight, a.weight_f32, 8 * (t + T * i), w[i]);
   }
-  int step = 0;
-  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, step ^= 1) {
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
+  struct Row {
     u32x4_t dy[VPT], h[VPT], dh[VPT];
+    float r;
+  };
+  auto load = [&](int64_t row) {
+    const u32x4_t zero = {0u, 0u, 0u, 0u};
+    Row x;
+    x.r = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPT; i++) {
-      const int v = t + T * i;
-      const int64_t at = row * a.H + 8 * v;
-      dy[i] = h[i] = dh[i] = zero;
-      if (v < nv) {
-        dy[i] = *reinterpret_cast<const u32x4_t*>(a.dy + at);
-        h[i] = *reinterpret_cast<const u32x4_t*>(a.h + at);
-        if (a.dh) dh[i] = *reinterpret_cast<const u32x4_t*>(a.dh + at);
+    for (int i = 0; i < VPT; i++) x.dy[i] = x.h[i] = x.dh[i] = zero;
+    if (row < a.M) {
+      x.r = a.rstd[row];
+#pragma unroll
+      for (int i = 0; i < VPT; i++) {
+        const int v = t + T * i;
+        const int64_t at = row * a.H + 8 * v;
+        if (v < nv) {
+          x.dy[i] = get16<PAST>(a.dy + at);
+          x.h[i] = get16<PAST>(a.h + at);
+          if (a.dh) x.dh[i] = get16<PAST>(a.dh + at);
+        }
       }
     }
-    const float r = a.rstd[row];
+    return x;
+  };
+  int step = 0;
+  Row x = load(blockIdx.x);
+  for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x, step ^= 1) {
+    const Row next = load(row + gridDim.x);
     float c = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; i++) {
       float d[8], f[8];
-      unpack8(dy[i], d);
-      unpack8(h[i], f);
+      unpack8(x.dy[i], d);
+      unpack8(x.h[i], f);
 #pragma unroll
       for (int j = 0; j < 8; j++) {
-        const float n = f[j] * r;
+        const float n = f[j] * x.r;
         acc[i][j] = fmaf(d[j], n, acc[i][j]);
         c = fmaf(d[j] * w[i][j], n, c);
       }
@@ -227,13 +257,14 @@ __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardP
       const int v = t + T * i;
       if (v >= nv) continue;
       float d[8], f[8], e[8];
-      unpack8(dy[i], d);
-      unpack8(h[i], f);
-      unpack8(dh[i], e);
+      unpack8(x.dy[i], d);
+      unpack8(x.h[i], f);
+      unpack8(x.dh[i], e);
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] = e[j] + r * (d[j] * w[i][j] - f[j] * r * c);
-      *reinterpret_cast<u32x4_t*>(a.dx + row * a.H + 8 * v) = pack8(f);
+      for (int j = 0; j < 8; j++) f[j] = e[j] + x.r * (d[j] * w[i][j] - f[j] * x.r * c);
+      put16<PAST>(a.dx + row * a.H + 8 * v, pack8(f));
     }
+    x = next;
   }
   if (a.partial) {
 #pragma unroll
@@ -248,69 +279,77 @@ __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardP
 }
 
 // dweight[c] = sum over P partial rows, 32 columns a workgroup: 8 lanes of
-// four columns, 32 row groups, joined in a fixed order.
-__global__ __launch_bounds__(256) void dweight_kernel(const float* __restrict__ partial, int P, int H,
-                                                      float* __restrict__ dweight) {
-  __shared__ float sum[32][33];
+// four columns, 128 row groups, joined in a fixed order.
+__global__ __launch_bounds__(1024) void dweight_kernel(const float* __restrict__ partial, int P, int H,
+                                                       float* __restrict__ dweight) {
+  __shared__ float sum[128][33];
   const int cg = threadIdx.x & 7, rg = threadIdx.x >> 3;
   const int c0 = blockIdx.x * 32 + 4 * cg;
   f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
   if (c0 < H) {
-    for (int p = rg; p < P; p += 32) s += *reinterpret_cast<const f32x4_t*>(partial + (int64_t)p * H + c0);
+    for (int p = rg; p < P; p += 128) s += *reinterpret_cast<const f32x4_t*>(partial + (int64_t)p * H + c0);
   }
 #pragma unroll
   for (int j = 0; j < 4; j++) sum[rg][4 * cg + j] = s[j];
   __syncthreads();
-  const int c = blockIdx.x * 32 + threadIdx.x;
-  if (threadIdx.x < 32 && c < H) {
-    float v = 0.0f;
-    for (int g = 0; g < 32; g++) v += sum[g][threadIdx.x];
-    dweight[c] = v;
-  }
+  const int c = threadIdx.x >> 5, g = threadIdx.x & 31;
+  float v = (sum[g][c] + sum[g + 32][c]) + (sum[g + 64][c] + sum[g + 96][c]);
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) v += __shfl_xor(v, d);
+  if (g == 0 && blockIdx.x * 32 + c < H) dweight[blockIdx.x * 32 + c] = v;
 }
 
 template <int T, int VPT>
 hipError_t launch_back(const NormBackwardParams& p, hipStream_t s) {
-  rmsnorm_backward_kernel<T, VPT><<<norm_backward_partials(p.M), T, 0, s>>>(p);
+  const int grid = norm_backward_partials(p.M, p.H);
+  if (p.past_caches) rmsnorm_backward_kernel<T, VPT, true><<<grid, T, 0, s>>>(p);
+  else rmsnorm_backward_kernel<T, VPT, false><<<grid, T, 0, s>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-int norm_backward_partials(int64_t M) {
-  const int64_t p = (M + 15) / 16;
-  return (int)(p < 1 ? 1 : p > 512 ? 512 : p);
+// Threads of a row in the backward pass: 16 bytes each up to 256 threads.
+static int backward_threads(int H) { return H <= 512 ? 64 : H <= 1024 ? 128 : H <= 8192 ? 256 : 512; }
+
+// Workgroups of the backward pass: two rows each at least, 131072 threads at
+// most, which fill the CUs.
+int norm_backward_partials(int64_t M, int H) {
+  const int64_t p = (M + 1) / 2, most = 131072 / backward_threads(H);
+  return (int)(p < 1 ? 1 : p > most ? most : p);
 }
 
 hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
   const int nv = p.H / 8;
-  if (p.M >= 2048 && nv <= 64 * 12) {
-    if (nv <= 64) return launch_norm<64, 1>(p, s);
-    if (nv <= 64 * 2) return launch_norm<64, 2>(p, s);
-    if (nv <= 64 * 4) return launch_norm<64, 4>(p, s);
-    if (nv <= 64 * 8) return launch_norm<64, 8>(p, s);
-    return launch_norm<64, 12>(p, s);
-  }
+  // (H = 6144: 65536 rows take 637 us in 256 threads x 3 vectors, 976 us in a
+  // wavefront each with 12; 64 rows 4.0 us in 1024 threads, 4.8 us in 256)
+  if (nv <= 64) return launch_norm<64, 1>(p, s);
+  if (nv <= 128) return launch_norm<128, 1>(p, s);
   if (nv <= 256) return launch_norm<256, 1>(p, s);
+  if (p.M >= 1024) {
+    if (nv <= 512) return launch_norm<256, 2>(p, s);
+    if (nv <= 768) return launch_norm<256, 3>(p, s);
+    if (nv <= 1024) return launch_norm<256, 4>(p, s);
+  }
   if (nv <= 1024) return launch_norm<1024, 1>(p, s);
-  if (nv <= 2048) return launch_norm<1024, 2>(p, s);
-  return launch_norm<1024, 4>(p, s);
+  return launch_norm<1024, 2>(p, s);
 }
 
 hipError_t launch_rmsnorm_backward(const NormBackwardParams& p, float* dweight, hipStream_t s) {
   const int nv = p.H / 8;
   hipError_t e = hipSuccess;
   if (p.M > 0) {
-    if (nv <= 256) e = launch_back<256, 1>(p, s);
+    if (nv <= 64) e = launch_back<64, 1>(p, s);
+    else if (nv <= 128) e = launch_back<128, 1>(p, s);
+    else if (nv <= 256) e = launch_back<256, 1>(p, s);
     else if (nv <= 512) e = launch_back<256, 2>(p, s);
     else if (nv <= 768) e = launch_back<256, 3>(p, s);
     else if (nv <= 1024) e = launch_back<256, 4>(p, s);
-    else if (nv <= 2048) e = launch_back<1024, 2>(p, s);
-    else e = launch_back<1024, 4>(p, s);
+    else e = launch_back<512, 4>(p, s);
     if (e != hipSuccess) return e;
   }
   if (!dweight) return hipSuccess;
-  dweight_kernel<<<(p.H + 31) / 32, 256, 0, s>>>(p.partial, p.M > 0 ? norm_backward_partials(p.M) : 0, p.H, dweight);
+  dweight_kernel<<<(p.H + 31) / 32, 1024, 0, s>>>(p.partial, p.M > 0 ? norm_backward_partials(p.M, p.H) : 0, p.H, dweight);
   return hipGetLastError();
 }
 

@@ -66,7 +66,7 @@ def norm_case(M, H, seed, std=2.0):
 
 @pytest.mark.parametrize("M,H,residual,wdtype,elem", [
     (1, 32, True, F32, 0), (1, 8, False, BF16, None), (3, 40, True, BF16, None), (5, 2048, False, F32, 1),
-    (8, 6144, True, BF16, 0), (17, 8224, True, F32, 0), (2, 32768, True, BF16, 1), (2050, 512, True, F32, 0),
+    (8, 6144, True, BF16, 0), (17, 8224, True, F32, 0), (2, 16384, True, BF16, 1), (2050, 512, True, F32, 0),
     (2051, 1024, False, BF16, 1), (2048, 1504, True, BF16, 0), (2049, 4128, True, F32, 0), (2500, 6144, True, BF16, 0),
     (7, 16384, True, F32, None), (300, 4096, False, F32, 0),
 ])
@@ -144,7 +144,7 @@ def test_norm_values():
 
 @pytest.mark.parametrize("M,H,dh,wdtype", [
     (1, 8, False, F32), (1, 6144, True, BF16), (15, 40, True, F32), (33, 2048, True, BF16), (257, 4128, True, F32),
-    (100, 6144, False, BF16), (64, 8192, True, F32), (9, 8224, True, BF16), (5, 32768, True, F32),
+    (100, 6144, False, BF16), (64, 8192, True, F32), (9, 8224, True, BF16), (5, 16384, True, F32),
     (9000, 96, True, F32),
 ])
 def test_norm_backward(M, H, dh, wdtype):
@@ -165,10 +165,11 @@ def test_norm_backward(M, H, dh, wdtype):
     # dx: the mean is a sum like the forward's, the rest six roundings
     near(dx, dx64, dx64.abs() * U8 + size * (R_TOL + 8 * U24) + 2.0 ** -133, "dx")
     # dweight: three roundings a term; a workgroup adds M / P rows one after
-    # another, and P / 32 + 32 additions join the partial sums
-    P = max(1, min(512, (M + 15) // 16))
+    # another, and P / 128 + 7 additions join the P partial sums, whose array
+    # is the workspace
+    P = max(1, moe.rmsnorm_backward_workspace_size(M, H) // (4 * H))
     mag = (dy.double() * hid.double() * r.double()[:, None]).abs().sum(0)
-    near(dw, dw64, mag * (3 + -(-M // P) + P // 32 + 33) * U24, "dweight")
+    near(dw, dw64, mag * (3 + -(-M // P) + P // 128 + 8) * U24, "dweight")
     again, dw2 = torch.empty_like(dx), torch.empty_like(dw)
     ws = torch.full((moe.rmsnorm_backward_workspace_size(M, H),), 255, dtype=torch.uint8, device="cuda")
     moe.moe_rmsnorm_backward(*args, again, dw2, dh=None if d is None else d.cuda(), workspace=ws)
@@ -177,6 +178,33 @@ def test_norm_backward(M, H, dh, wdtype):
     inplace = dy.cuda()
     moe.moe_rmsnorm_backward(inplace, *args[1:], inplace, dh=None if d is None else d.cuda())
     assert torch.equal(inplace, dx)
+
+
+def test_norm_of_many_rows():
+    """Rows beyond the caches' size: the same as in two calls of half as many,
+    bit for bit; offsets of rows past 2^31 bytes are in range."""
+    say("norm of many rows")
+    M, H = 132000, 8192
+    x = torch.randn(M, H, device="cuda", dtype=BF16)
+    w = torch.rand(H, device="cuda")
+    y, q = torch.empty_like(x), torch.empty(M, H, dtype=torch.uint8, device="cuda")
+    sf, r = torch.empty(M, H // 32, dtype=torch.uint8, device="cuda"), torch.empty(M, device="cuda")
+    moe.moe_rmsnorm(x, w, y=y, q=q, q_sf=sf, rstd=r)
+    dx, dw = torch.empty_like(x), torch.empty(H, device="cuda")
+    moe.moe_rmsnorm_backward(y, x, w, r, dx, dw, dh=y)
+    total = torch.zeros(H, device="cuda", dtype=F64)
+    for at in range(0, M, 8000):
+        s = slice(at, at + 8000)
+        y1, q1, sf1, r1 = (torch.empty_like(t[s]) for t in (y, q, sf, r))
+        moe.moe_rmsnorm(x[s], w, y=y1, q=q1, q_sf=sf1, rstd=r1)
+        assert torch.equal(y1, y[s]) and torch.equal(q1, q[s]) and torch.equal(sf1, sf[s]) and torch.equal(r1, r[s])
+        dx1, dw1 = torch.empty_like(y1), torch.empty_like(dw)
+        moe.moe_rmsnorm_backward(y1, x[s], w, r1, dx1, dw1, dh=y1)
+        assert torch.equal(dx1, dx[s])
+        total += dw1
+    # both sums add the same terms with at most 600 roundings each
+    mag = (y.float() * x.float() * r[:, None]).abs().sum(0, dtype=F64)
+    assert bool(((dw - total).abs() <= mag * 1200 * U24).all())
 
 
 def test_norm_backward_of_nothing():

@@ -31,7 +31,7 @@ NORM = dict(x=F, xs=0, residual=F, rs=0, weight=F, wd=0, eps=1e-6, M=4, H=64, h=
     (dict(sf=None), INVALID), (dict(q=None), INVALID), (dict(residual=None), INVALID), (dict(eps=-1.0), INVALID),
     (dict(eps=NAN), INVALID), (dict(eps=float("inf")), INVALID), (dict(M=-1), INVALID), (dict(H=0), INVALID),
     (dict(wd=2), INVALID), (dict(elem=2), INVALID), (dict(xs=56), INVALID), (dict(rs=56), INVALID),
-    (dict(H=60), UNSUPPORTED), (dict(H=72), UNSUPPORTED), (dict(H=65536), UNSUPPORTED), (dict(xs=68), UNSUPPORTED),
+    (dict(H=60), UNSUPPORTED), (dict(H=72), UNSUPPORTED), (dict(H=16416), UNSUPPORTED), (dict(xs=68), UNSUPPORTED),
     (dict(rs=68), UNSUPPORTED), (dict(x=ODD), UNSUPPORTED), (dict(residual=ODD), UNSUPPORTED),
     (dict(weight=ODD), UNSUPPORTED), (dict(h=ODD), UNSUPPORTED), (dict(y=ODD), UNSUPPORTED),
     (dict(q=ODD), UNSUPPORTED), (dict(rstd=ODD), UNSUPPORTED), (dict(M=0), OK), (dict(M=0, x=None), OK),
@@ -47,7 +47,7 @@ BACK = dict(dy=F, h=F, weight=F, wd=1, rstd=F, dh=None, M=4, H=64, dx=F, dweight
     (dict(dy=None), INVALID), (dict(h=None), INVALID), (dict(weight=None), INVALID), (dict(rstd=None), INVALID),
     (dict(dx=None), INVALID), (dict(M=-1), INVALID), (dict(H=-8), INVALID), (dict(wd=-1), INVALID),
     (dict(H=60), UNSUPPORTED), (dict(dh=ODD), UNSUPPORTED), (dict(dx=ODD), UNSUPPORTED),
-    (dict(dweight=ODD), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=F + 16), WORKSPACE), (dict(n=255), WORKSPACE),
+    (dict(dweight=ODD), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(ws=F + 16), WORKSPACE), (dict(n=511), WORKSPACE),
     (dict(M=0, dweight=None, ws=None, n=0), OK),
 ])
 def test_norm_backward(change, status):
@@ -55,7 +55,7 @@ def test_norm_backward(change, status):
 
 
 def test_norm_backward_workspace():
-    assert moe.rmsnorm_backward_workspace_size(4, 64) == 256
+    assert moe.rmsnorm_backward_workspace_size(4, 64) == 512
     assert moe.rmsnorm_backward_workspace_size(4, 60) == 0
     assert moe.rmsnorm_backward_workspace_size(-1, 64) == 0
     n = moe.rmsnorm_backward_workspace_size(4096, 6144)
