@@ -580,7 +580,7 @@ struct BalanceLayout {
 };
 BalanceLayout balance_layout(int M, int E) {
   BalanceLayout L;
-  L.partials = router_partials(M, E);
+  L.partials = router_partials(M);
   L.loss = 256;
   L.tokens = align256(L.loss + sizeof(double) * balance_finish_blocks(E));
   L.probs = align256(L.tokens + sizeof(int32_t) * (size_t)L.partials);

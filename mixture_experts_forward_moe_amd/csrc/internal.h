@@ -224,7 +224,7 @@ struct RouterBackwardParams {
   const float* d_loss;        // NULL: 1
   void* d_logits;
 };
-int router_partials(int64_t M, int E);
+int router_partials(int64_t M);
 int balance_finish_blocks(int E);
 hipError_t launch_router(const RouterParams& p, hipStream_t stream);
 hipError_t launch_balance_finish(const BalanceParams& p, hipStream_t stream);

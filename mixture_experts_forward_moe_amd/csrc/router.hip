@@ -9,10 +9,22 @@
 //   d logit_e = p_e (u_e - sum u p) [(1 - s_e) for sigmoid],  u_e = coef E / T (f_e - 1 / E)
 //
 // One DPP row of 16 lanes owns a token: lane j holds the logits 64 c + 4 j ..
-// + 3 (16-byte loads, 256 bytes a row of lanes), so a maximum or a sum over
-// the experts is a loop over a lane's registers and four DPP steps, and a
-// wavefront serves four tokens with each instruction.
+// + 3 (16-byte loads, 256 bytes a row of lanes; up to 64 experts one logit in
+// 16 instead), so a maximum or a sum over the experts is a loop over a lane's
+// registers and four DPP steps, and a wavefront serves four tokens with each
+// instruction.
+//
+// The choice: the k-th largest of the half lanes' maxima bounds the k-th key
+// from below, and only keys above the bound (about nine of 256 for k = 8) go
+// on, one to a lane, where each lane counts the ones before its own.  The
+// k rounds of maximum and removal that this replaces cost five instructions a
+// register and round; they stay for k > 16 and for rows where more than 32
+// keys pass (many equal ones).  score + bias is compared in fp32 first, and in
+// fp64 for a token any two of whose candidates are closer than the error of
+// that.
+#include <algorithm>
 #include <cfloat>
+#include <type_traits>
 
 #include "device_common.h"
 #include "internal.h"
@@ -21,8 +33,12 @@ namespace moe {
 
 namespace {
 
-constexpr int RT = 256;        // threads: 16 tokens at a time
-constexpr int TOKENS = RT / 16;
+// Threads, and tokens at a time.  With statistics 512 threads: a workgroup's
+// partial sums are joined later, so there are at most 512 workgroups, and 256
+// threads each would leave two wavefronts a SIMD.
+constexpr int threads_of(bool stats) { return stats ? 512 : 256; }
+constexpr int RT = 256, TOKENS = RT / 16;  // of the backward pass
+constexpr int STAT_TOKENS = threads_of(true) / 16;
 
 constexpr int QUAD_XOR1 = 0xB1, QUAD_XOR2 = 0x4E, ROW_HALF_MIRROR = 0x141, ROW_MIRROR = 0x140;
 
@@ -39,6 +55,12 @@ DEV double dpp(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = (uint32_t)dpp<CTRL>((int)(uint32_t)b), hi = (uint32_t)dpp<CTRL>((int)(uint32_t)(b >> 32));
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// the value d lanes before in the row (0x110 + d), 0 in front of the first
+template <int CTRL>
+DEV int dpp_zero(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, false);
 }
 
 // a reduction over the 16 lanes of a token
@@ -62,117 +84,314 @@ DEV T row_add(T v) {
   return row_reduce(v, [](T a, T b) { return a + b; });
 }
 
+// A copy of v that the compiler cannot see through: what a token's work derives
+// from the lane's number is made anew for each token instead of being kept in
+// registers over all of them (which cost a third of the wavefronts).
+DEV int opaque(int v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
 // NaN and -inf: not choosable; +inf counts as FLT_MAX
 DEV float clean(float l) { return l == l ? fminf(l, FLT_MAX) : -INFINITY; }
 
-// expert of register i of lane j
-DEV int expert_of(int i, int j) { return (i >> 2) * 64 + 4 * j + (i & 3); }
-
-// logits of a row; -inf past E.  vec: rows of whole, aligned groups of four
+// expert of register i of lane j, of V
 template <int V>
-DEV void load_row(const void* logits, int f32, int64_t at, int E, int j, bool vec, float (&l)[V]) {
-  if (vec) {
+DEV int expert_of(int i, int j) {
+  return V == 4 ? 16 * i + j : (i >> 2) * 64 + 4 * j + (i & 3);
+}
+
+// e^x for x <= 0 to about one step: the product with log2(e) is carried in two
+// parts into the hardware's exp2; below the normal range 0
+DEV float exp_neg(float x) {
+  x = fmaxf(x, -200.0f);
+  const float t = x * 1.44269502f;
+  const float e = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -t));
+  const float p = __builtin_amdgcn_exp2f(t);
+  return fmaf(p, e * 0.693147182f, p);
+}
+
+// logits of a row; -inf past E.  vec: rows of whole, aligned groups of four.
+// Groups of 64 experts that the row fills are loaded without a test; in the
+// last one a lane past the end reads the row's last ones again.
+template <int V, bool F32>
+DEV void load_row_as(const void* logits, int64_t at, int E, int j, bool vec, float (&l)[V]) {
+  constexpr int G = V == 4 ? 1 : V / 4;  // groups of 64
+  const float* f = reinterpret_cast<const float*>(logits) + (F32 ? at : 0);
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(logits) + (F32 ? 0 : at);
+  auto one = [&](int e) {
+    if constexpr (F32) return f[e];
+    else return bf16_to_f32(h[e]);
+  };
 #pragma unroll
-    for (int c = 0; c < V / 4; c++) {
-      const int e = expert_of(4 * c, j);
-      f32x4_t v = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      if (e < E) {
-        if (f32) {
-          v = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(logits) + at + e);
-        } else {
-          const uint2 b = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(logits) + at + e);
-          v = f32x4_t{__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u), __uint_as_float(b.y << 16),
-                      __uint_as_float(b.y & 0xffff0000u)};
-        }
+  for (int c = 0; c < G; c++) {
+    const bool full = 64 * (c + 1) <= E;
+    if (V > 4 && vec) {
+      const int e = full ? expert_of<V>(4 * c, j) : min(expert_of<V>(4 * c, j), E - 4);
+      if constexpr (F32) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(f + e);
+#pragma unroll
+        for (int i = 0; i < 4; i++) l[4 * c + i] = v[i];
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(h + e);
+        l[4 * c] = __uint_as_float(v.x << 16);
+        l[4 * c + 1] = __uint_as_float(v.x & 0xffff0000u);
+        l[4 * c + 2] = __uint_as_float(v.y << 16);
+        l[4 * c + 3] = __uint_as_float(v.y & 0xffff0000u);
       }
+    } else if (full) {
 #pragma unroll
-      for (int i = 0; i < 4; i++) l[4 * c + i] = clean(v[i]);
-    }
-  } else {
+      for (int i = 0; i < 4; i++) l[4 * c + i] = one(expert_of<V>(4 * c + i, j));
+    } else {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = expert_of(i, j);
-      float v = -INFINITY;
-      if (e < E)
-        v = f32 ? reinterpret_cast<const float*>(logits)[at + e]
-                : bf16_to_f32(reinterpret_cast<const uint16_t*>(logits)[at + e]);
-      l[i] = clean(v);
+      for (int i = 0; i < 4; i++) l[4 * c + i] = one(min(expert_of<V>(4 * c + i, j), E - 1));
     }
   }
+#pragma unroll
+  for (int i = 0; i < V; i++) l[i] = expert_of<V>(i, j) < E ? clean(l[i]) : -INFINITY;
+}
+template <int V>
+DEV void load_row(const void* logits, int f32, int64_t at, int E, int j, bool vec, float (&l)[V]) {
+  if (f32) load_row_as<V, true>(logits, at, E, j, vec, l);
+  else load_row_as<V, false>(logits, at, E, j, vec, l);
+}
+
+// sigmoid and 1 - sigmoid: with z = e^-|l|, 1 / (1 + z) and z / (1 + z)
+DEV float sigmoid_f32(float l) {
+  const float z = exp_neg(-fabsf(l));
+  return (l < 0.0f ? z : 1.0f) * __builtin_amdgcn_rcpf(1.0f + z);
 }
 
 // Probabilities of a row: the softmax, or the sigmoid scores over their sum.
 // Both are taken relative to the largest logit, so that a row of very
 // negative logits does not become 0 / 0: s = exp(min(l, 0)) / (1 + exp(-|l|)),
-// and the factor exp(-min(max, 0)) cancels in the quotient.
+// and the factor exp(-min(max, 0)) cancels in the quotient (it is 1 unless
+// every logit of the row is negative).
 template <int V>
 DEV void probabilities(const float (&l)[V], float top, int sigmoid, float (&p)[V]) {
   float sum = 0.0f;
-  const float ref = sigmoid ? fminf(top, 0.0f) : top;
+  if (!sigmoid) {
 #pragma unroll
-  for (int i = 0; i < V; i++) {
-    float e = expf((sigmoid ? fminf(l[i], 0.0f) : l[i]) - ref);
-    if (sigmoid) e = e / (1.0f + expf(-fabsf(l[i])));
-    p[i] = l[i] == -INFINITY ? 0.0f : e;
-    sum += p[i];
+    for (int i = 0; i < V; i++) p[i] = l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
+  } else if (__all(top >= 0.0f)) {
+#pragma unroll
+    for (int i = 0; i < V; i++) p[i] = sigmoid_f32(l[i]);
+  } else {
+    const float ref = fminf(top, 0.0f);
+#pragma unroll
+    for (int i = 0; i < V; i++) {
+      const float e = exp_neg(fminf(l[i], 0.0f) - ref) * __builtin_amdgcn_rcpf(1.0f + exp_neg(-fabsf(l[i])));
+      p[i] = l[i] == -INFINITY ? 0.0f : e;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < V; i++) sum += p[i];
   sum = row_add(sum);
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int i = 0; i < V; i++) p[i] *= inv;
 }
 
-DEV float sigmoid_f32(float l) { return 1.0f / (1.0f + expf(-l)); }
-
 // Score of a chosen logit before the division by the sum over the chosen
 // (renormalize), relative to the largest chosen one as in probabilities()
 DEV float chosen_score(float l, float top, int sigmoid) {
   if (l == -INFINITY) return 0.0f;
-  if (!sigmoid) return expf(l - top);
-  return expf(fminf(l, 0.0f) - fminf(top, 0.0f)) / (1.0f + expf(-fabsf(l)));
+  if (!sigmoid) return exp_neg(l - top);
+  return exp_neg(fminf(l, 0.0f) - fminf(top, 0.0f)) / (1.0f + exp_neg(-fabsf(l)));
 }
 
 constexpr int SLOTS = ROUTER_MAX_TOP_K / 16;  // chosen places a lane holds: j, j + 16, ...
 
-// The key of the choice: the logit, or score + bias in fp64.
-template <int V, bool BIAS>
-struct Keys;
-template <int V>
-struct Keys<V, false> {
-  typedef float type;
-  static DEV void make(const float (&l)[V], float, int, const float*, int, int, float (&k)[V]) {
-#pragma unroll
-    for (int i = 0; i < V; i++) k[i] = l[i];
-  }
-};
-template <int V>
-struct Keys<V, true> {
-  typedef double type;
-  static DEV void make(const float (&l)[V], float top, int sigmoid, const float* bias, int E, int j, double (&k)[V]) {
-    double sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-      const double d = (double)l[i];
-      k[i] = sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - (double)top);
-      if (!sigmoid && l[i] != -INFINITY) sum += k[i];
-    }
-    if (!sigmoid) sum = row_add(sum);
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = expert_of(i, j);
-      const double b = e < E ? (double)bias[e] : 0.0;
-      const double v = (sigmoid ? k[i] : k[i] / sum) + b;
-      k[i] = l[i] != -INFINITY && v == v ? v : -INFINITY;
-    }
-  }
+// A key as an integer of the same order (no NaN, -0 as 0).
+DEV uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+// What a lane holds of a choice: expert and logit of places place[q]
+struct Chosen {
+  int id[SLOTS], place[SLOTS];
+  float l[SLOTS];
 };
 
+// A logit of the row that starts at element `at`.
+DEV float logit(const RouterParams& a, int64_t at, int e) {
+  return clean(a.logits_f32 ? reinterpret_cast<const float*>(a.logits)[at + e]
+                            : bf16_to_f32(reinterpret_cast<const uint16_t*>(a.logits)[at + e]));
+}
+
+// The key in fp64 of expert e with logit l: score + bias.  sum: sum_f64 of the
+// row (SOFTMAX).
+DEV double key_f64(const RouterParams& a, float l, int e, float top, double sum) {
+  const double d = (double)l;
+  return (a.sigmoid ? 1.0 / (1.0 + exp(-d)) : exp(d - (double)top) / sum) + (double)a.select_bias[e];
+}
+DEV double sum_f64(const RouterParams& a, int64_t at, float top, int j) {
+  if (a.sigmoid) return 1.0;
+  double sum = 0.0;
+#pragma unroll 1
+  for (int e = j; e < a.E; e += 16) {
+    const float l = logit(a, at, e);
+    if (l != -INFINITY) sum += exp((double)l - (double)top);
+  }
+  return row_add(sum);
+}
+
+// The choice by candidates (see above) of the wavefront's four tokens: the
+// number of slots used, one candidate a lane or two (17 to 32 of them).  key:
+// the logits, or with BIAS fp32 forms of the keys, each off by at most err;
+// where two candidates are closer than that the candidates' keys are compared
+// in fp64.  0, and nothing chosen, if any of the tokens needs the other way.
+template <int V, bool BIAS>
+DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, const float (&key)[V], float err, int j,
+                           uint2* cand, Chosen& c) {
+  const int k = a.top_k;
+  if (k > 16) return 0;
+  // the k-th largest of the maxima of half lanes, the least of those with
+  // fewer than k above them (of whole lanes: more than 16 keys would pass for
+  // 0.7% of the rows at 8 of 256, a quarter at 10 of 512)
+  float ma = key[0], mb = key[V / 2];
+#pragma unroll
+  for (int i = 1; i < V / 2; i++) {
+    ma = fmaxf(ma, key[i]);
+    mb = fmaxf(mb, key[V / 2 + i]);
+  }
+  int na = mb > ma, nb = ma > mb;
+#define ROTATE(R)                                                     \
+  {                                                                   \
+    const float oa = dpp<0x120 + R>(ma), ob = dpp<0x120 + R>(mb);     \
+    na += (oa > ma) + (ob > ma);                                      \
+    nb += (oa > mb) + (ob > mb);                                      \
+  }
+  ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
+  ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)
+#undef ROTATE
+  float bound = fminf(na < k ? ma : INFINITY, nb < k ? mb : INFINITY);
+  bound = row_min(bound) - 2.0f * err;
+  // candidates of this lane, and of the lanes before it
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < V; i++) n += key[i] >= bound && key[i] > -INFINITY;
+  int at = n;
+  at += dpp_zero<0x111>(at);
+  at += dpp_zero<0x112>(at);
+  at += dpp_zero<0x114>(at);
+  at += dpp_zero<0x118>(at);
+  const int total = __shfl(at, 15, 16);
+  if (__any(total > 32)) return 0;
+  at -= n;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    if (key[i] >= bound && key[i] > -INFINITY) {
+      cand[at] = make_uint2(__float_as_uint(key[i]), (uint32_t)expert_of<V>(i, j));
+      at++;
+    }
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const bool two = __any(total > 16);
+  const bool have = j < total, have2 = j + 16 < total;
+  const uint2 own = have ? cand[j] : make_uint2(0u, 0u), own2 = have2 ? cand[j + 16] : make_uint2(0u, 0u);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  const float v = __uint_as_float(own.x), v2 = __uint_as_float(own2.x);
+  const int e = have ? (int)own.y : INT32_MAX, e2 = have2 ? (int)own2.y : INT32_MAX;
+  // places by descending key, then ascending expert
+  int rank = 0, rank2 = 0;
+  bool exactly = BIAS && two;
+  if (!two) {
+    const uint32_t hi = have ? ordered(v) : 0u, lo = ~(uint32_t)e;
+    bool close = false;
+#define ROTATE(R)                                                                                        \
+  {                                                                                                      \
+    const uint32_t h2 = (uint32_t)dpp<0x120 + R>((int)hi), l2 = (uint32_t)dpp<0x120 + R>((int)lo);        \
+    rank += (((uint64_t)h2 << 32) | l2) > (((uint64_t)hi << 32) | lo);                                   \
+    if (BIAS) close |= have && h2 != 0u && fabsf(dpp<0x120 + R>(v) - v) <= 2.0f * err;                   \
+  }
+    ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
+    ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)
+#undef ROTATE
+    if (BIAS) exactly = __any(close);
+  }
+  if (two || exactly) {
+    typedef typename std::conditional<BIAS, double, float>::type K;
+    K x = -INFINITY, y = -INFINITY;
+    if constexpr (BIAS) {
+      const double sum = sum_f64(a, at_row, top, j);
+      if (have) x = key_f64(a, logit(a, at_row, e), e, top, sum);
+      if (have2) y = key_f64(a, logit(a, at_row, e2), e2, top, sum);
+    } else {
+      if (have) x = v;
+      if (have2) y = v2;
+    }
+    auto before = [](K a, int ea, K b, int eb) { return (int)(a > b || (a == b && ea < eb)); };
+    rank = before(y, e2, x, e);
+    rank2 = before(x, e, y, e2);
+#pragma unroll 1
+    for (int s = 1; s < 16; s++) {
+      // (lane j + s of the row; rarely taken, so small rather than fast)
+      const int from = (j + s) & 15;
+      const K ox = __shfl(x, from, 16), oy = __shfl(y, from, 16);
+      const int ex = __shfl(e, from, 16), ey = __shfl(e2, from, 16);
+      rank += before(ox, ex, x, e) + before(oy, ey, x, e);
+      rank2 += before(ox, ex, y, e2) + before(oy, ey, y, e2);
+    }
+  }
+  c.id[0] = have ? e : -1;
+  c.place[0] = have ? rank : j;
+  c.l[0] = have ? v : -INFINITY;  // (without a bias, the logit)
+  c.id[1] = have2 ? e2 : -1;
+  c.place[1] = have2 ? rank2 : j + 16;
+  c.l[1] = have2 ? v2 : -INFINITY;
+  return two ? 2 : 1;
+}
+
+// The choice by k rounds of maximum and removal, the row read again in each
+// (it is in the first-level cache; registers for it would halve the wavefronts
+// of the other way).  Lane j looks at the experts j, j + 16, ..
+template <bool BIAS>
+DEV void choose_rounds(const RouterParams& a, int64_t at_row, float top, int j, Chosen& c) {
+  uint64_t taken = 0;
+  const double sum = BIAS ? sum_f64(a, at_row, top, j) : 1.0;
+#pragma unroll
+  for (int q = 0; q < SLOTS; q++) {
+    c.id[q] = -1;
+    c.place[q] = j + 16 * q;
+  }
+#pragma unroll 1
+  for (int s = 0; s < a.top_k; s++) {
+    // the largest key; of equal ones the lowest expert
+    typename std::conditional<BIAS, double, float>::type best = -INFINITY;
+    int e = INT32_MAX;
+#pragma unroll 2
+    for (int x = j; x < a.E; x += 16) {
+      const float l = logit(a, at_row, x);
+      if (l == -INFINITY || (taken >> (x >> 4) & 1)) continue;
+      decltype(best) v;
+      if constexpr (BIAS) v = key_f64(a, l, x, top, sum);
+      else v = l;
+      if (v > best) {  // (not for NaN)
+        best = v;
+        e = x;
+      }
+    }
+    const auto win = row_max(best);
+    e = row_min(best == win ? e : INT32_MAX);
+    const bool any = win > -INFINITY;
+    if (any && (e & 15) == j) taken |= (uint64_t)1 << (e >> 4);
+    if (any && (s & 15) == j) {
+#pragma unroll
+      for (int q = 0; q < SLOTS; q++)
+        if (q == s >> 4) c.id[q] = e;
+    }
+  }
+}
+
 template <int V, bool SELECT, bool BIAS, bool STATS>
-__global__ __launch_bounds__(RT) void router_kernel(const RouterParams a, bool vec) {
+__global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterParams a, bool vec) {
+  constexpr int RT = threads_of(STATS), TOKENS = RT / 16;
   __shared__ int counts[STATS ? 16 * V : 1];
   __shared__ float psums[STATS ? RT / 64 : 1][STATS ? 16 * V : 1];
   __shared__ int tokens;
-  const int j = threadIdx.x & 15;
+  __shared__ uint2 cand[SELECT ? TOKENS : 1][32];
   float psum[STATS ? V : 1];
   int seen = 0;
   if constexpr (STATS) {
@@ -184,6 +403,7 @@ __global__ __launch_bounds__(RT) void router_kernel(const RouterParams a, bool v
     __syncthreads();
   }
   for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.M; t0 += (int64_t)gridDim.x * TOKENS) {
+    const int j = opaque(threadIdx.x & 15);
     const int64_t t = t0 + (threadIdx.x >> 4);
     const bool in = t < a.M;
     const bool on = in && (!a.token_mask || a.token_mask[t] != 0);
@@ -205,107 +425,102 @@ __global__ __launch_bounds__(RT) void router_kernel(const RouterParams a, bool v
       }
     }
 
-    int id[SLOTS];
+    Chosen c;
     if constexpr (SELECT) {
-      typename Keys<V, BIAS>::type key[V];
-      Keys<V, BIAS>::make(l, top, a.sigmoid, a.select_bias, a.E, j, key);
-      float cl[SLOTS];
+      const int64_t at_row = row * a.row_stride;
+      float sum = 0.0f;  // of the scores' numerators: over all experts, or over the chosen ones
+      if (!a.renormalize && !a.sigmoid) {
 #pragma unroll
-      for (int q = 0; q < SLOTS; q++) {
-        id[q] = -1;
-        cl[q] = -INFINITY;
+        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
       }
-      for (int s = 0; s < a.top_k; s++) {
-        // the largest key; of equal ones the lowest expert
-        auto best = key[0];
-        int at = 0;
+      int used = (a.top_k + 15) / 16;
+      bool read_logits = true;
+      uint2* own_cand = cand[threadIdx.x >> 4];
+      if constexpr (BIAS) {
+        // a sigmoid is off by a few steps of 1, a softmax by its sum's V + 4
+        // roundings and those too; the addition rounds relative to the key
+        float big = 0.0f;
+        if (!a.sigmoid) {
+          if constexpr (STATS) {
 #pragma unroll
-        for (int i = 1; i < V; i++) {
-          if (key[i] > best) {
-            best = key[i];
-            at = i;
+            for (int i = 0; i < V; i++) p[i] = l[i] == -INFINITY ? -INFINITY : p[i];
+#pragma unroll
+            for (int i = 0; i < V; i++) l[i] = p[i];
+          } else {
+            float q[V];
+            probabilities<V>(l, top, 0, q);
+#pragma unroll
+            for (int i = 0; i < V; i++) l[i] = l[i] == -INFINITY ? -INFINITY : q[i];
           }
         }
-        const auto win = row_max(best);
-        const bool any = win > -INFINITY;
-        const int e = row_min(best == win ? expert_of(at, j) : INT32_MAX);
-        float wl = -INFINITY;
 #pragma unroll
         for (int i = 0; i < V; i++) {
-          const bool mine = any && expert_of(i, j) == e;
-          if (mine) {
-            wl = l[i];
-            key[i] = -INFINITY;
-          }
+          const int e = expert_of<V>(i, j);
+          const float v = (a.sigmoid ? sigmoid_f32(l[i]) : l[i]) + a.select_bias[min(e, a.E - 1)];
+          l[i] = l[i] != -INFINITY && v == v ? v : -INFINITY;
+          big = fmaxf(big, l[i] == -INFINITY ? 0.0f : fabsf(l[i]));
         }
-        wl = row_max(wl);
-        if (any && (s & 15) == j) {
-#pragma unroll
-          for (int q = 0; q < SLOTS; q++)
-            if (q == s >> 4) {
-              id[q] = e;
-              cl[q] = wl;
-            }
-        }
-      }
-      // weights
-      float ctop = -INFINITY, sum = 0.0f, w[SLOTS];
-#pragma unroll
-      for (int q = 0; q < SLOTS; q++) ctop = fmaxf(ctop, cl[q]);
-      ctop = row_max(ctop);
-      if (a.renormalize) {
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) {
-          w[q] = chosen_score(cl[q], ctop, a.sigmoid);
-          sum += w[q];
-        }
-        sum = row_add(sum);
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) w[q] = sum > 0.0f ? w[q] / sum : 0.0f;
-      } else if (a.sigmoid) {
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) w[q] = cl[q] == -INFINITY ? 0.0f : sigmoid_f32(cl[q]);
+        const float err = (a.sigmoid ? 0x1p-20f : (V + 16) * 0x1p-24f) + 0x1p-22f * row_max(big);
+        const int n = __all(err < INFINITY) ? choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c) : 0;
+        if (n) used = n;
+        else choose_rounds<true>(a, at_row, top, j, c);
       } else {
-#pragma unroll
-        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
-        sum = row_add(sum);
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) w[q] = cl[q] == -INFINITY ? 0.0f : expf(cl[q] - top) / sum;
+        const int n = choose_candidates<V, false>(a, at_row, top, l, 0.0f, j, own_cand, c);
+        read_logits = n == 0;
+        if (n) used = n;
+        else choose_rounds<false>(a, at_row, top, j, c);
       }
-      if (in) {
-#pragma unroll
-        for (int q = 0; q < SLOTS; q++) {
-          const int s = j + 16 * q;
-          if (s < a.top_k) {
-            if (!on) id[q] = -1;
-            a.ids[t * a.top_k + s] = id[q];
-            a.weights[t * a.top_k + s] = on ? w[q] : 0.0f;
-          }
-        }
-      }
-    } else {
 #pragma unroll
       for (int q = 0; q < SLOTS; q++) {
-        const int s = j + 16 * q;
-        id[q] = on && s < a.top_k ? a.ids[t * a.top_k + s] : -1;
+        if (q >= used) c.id[q] = -1;
+        if (c.id[q] < 0 || c.place[q] >= a.top_k) c.l[q] = -INFINITY;
+        else if (read_logits) c.l[q] = logit(a, at_row, c.id[q]);
       }
-    }
-    if constexpr (STATS) {
-      if (on) {
+      // weights
+      float ctop = -INFINITY, w[SLOTS];
+#pragma unroll
+      for (int q = 0; q < SLOTS; q++) ctop = fmaxf(ctop, c.l[q]);
+      ctop = a.renormalize || a.sigmoid ? row_max(ctop) : top;
+#pragma unroll
+      for (int q = 0; q < SLOTS; q++) {
+        w[q] = 0.0f;
+        if (q >= used) continue;
+        if (a.sigmoid && !a.renormalize) w[q] = c.l[q] == -INFINITY ? 0.0f : sigmoid_f32(c.l[q]);
+        else w[q] = chosen_score(c.l[q], ctop, a.sigmoid);
+        if (a.renormalize) sum += w[q];
+      }
+      if (a.renormalize || !a.sigmoid) {
+        sum = row_add(sum);
 #pragma unroll
         for (int q = 0; q < SLOTS; q++)
-          if (j + 16 * q < a.top_k && id[q] >= 0 && id[q] < a.E) atomicAdd(&counts[id[q]], 1);
+          if (q < used) w[q] = sum > 0.0f ? w[q] / sum : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < SLOTS; q++) {
+        if (q < used && in && c.place[q] < a.top_k) {
+          a.ids[t * a.top_k + c.place[q]] = on ? c.id[q] : -1;
+          a.weights[t * a.top_k + c.place[q]] = on ? w[q] : 0.0f;
+          if constexpr (STATS) {
+            if (on && c.id[q] >= 0) atomicAdd(&counts[c.id[q]], 1);
+          }
+        }
+      }
+    } else if constexpr (STATS) {
+      for (int s = j; s < a.top_k; s += 16) {
+        const int id = on ? a.ids[t * a.top_k + s] : -1;
+        if (id >= 0 && id < a.E) atomicAdd(&counts[id], 1);
       }
     }
   }
   if constexpr (STATS) {
+    const int j = threadIdx.x & 15;
     // this workgroup's sums: four tokens' rows of a wavefront, then its wavefronts
 #pragma unroll
     for (int i = 0; i < V; i++) {
       float v = psum[i];
       v += __shfl_xor(v, 16);
       v += __shfl_xor(v, 32);
-      if ((threadIdx.x & 63) < 16) psums[threadIdx.x >> 6][expert_of(i, j)] = v;
+      if ((threadIdx.x & 63) < 16) psums[threadIdx.x >> 6][expert_of<V>(i, j)] = v;
     }
     if (seen) atomicAdd(&tokens, seen);
     __syncthreads();
@@ -320,15 +535,15 @@ __global__ __launch_bounds__(RT) void router_kernel(const RouterParams a, bool v
   }
 }
 
-// Joins the workgroups' statistics, 32 experts a workgroup (32 lanes wide, 32
-// rows of lanes over the partials, joined in a fixed order in fp64); the last
-// workgroup to arrive adds the loss terms of all of them, in their order.
-constexpr int FT = 1024;
-constexpr int FE = 32;
+// Joins the workgroups' statistics, 4 experts a workgroup, 64 rows of lanes
+// over the partials, joined in a fixed order in fp64; the last workgroup to
+// arrive adds the loss terms of all of them, in a fixed order.
+constexpr int FT = 256;
+constexpr int FE = 4;
 
 __global__ __launch_bounds__(FT) void balance_finish_kernel(const BalanceParams a) {
-  __shared__ double psum[FT / FE][FE + 1];
-  __shared__ int count[FT / FE][FE + 1];
+  __shared__ double psum[FT / FE][FE];
+  __shared__ int count[FT / FE][FE];
   __shared__ int total;
   const int c = threadIdx.x % FE, r = threadIdx.x / FE;
   const int e = blockIdx.x * FE + c;
@@ -337,6 +552,7 @@ __global__ __launch_bounds__(FT) void balance_finish_kernel(const BalanceParams 
   double s = 0.0;
   int n = 0, t = 0;
   if (e < a.E) {
+#pragma unroll 8
     for (int p = r; p < a.partials; p += FT / FE) {
       s += (double)a.prob_partial[(int64_t)p * a.E + e];
       n += a.count_partial[(int64_t)p * a.E + e];
@@ -348,41 +564,55 @@ __global__ __launch_bounds__(FT) void balance_finish_kernel(const BalanceParams 
   if (t) atomicAdd(&total, t);
   __syncthreads();
   if (threadIdx.x >= 64) return;
+  // one wavefront: lane l takes rows l / 4, l / 4 + 16, .. of expert l % 4
+  s = 0.0;
+  n = 0;
+#pragma unroll
+  for (int i = 0; i < FT / FE; i += 64 / FE) {
+    s += psum[i + r][c];
+    n += count[i + r][c];
+  }
+#pragma unroll
+  for (int d = FE; d < 64; d <<= 1) {
+    s += __shfl_xor(s, d);
+    n += __shfl_xor(n, d);
+  }
   double term = 0.0;
-  if (threadIdx.x < FE && e < a.E) {
-    s = 0.0;
-    n = 0;
-    for (int k = 0; k < FT / FE; k++) {
-      s += psum[k][c];
-      n += count[k][c];
-    }
+  if (e < a.E) {
     const double T = (double)total;
     const double f = total > 0 ? (double)n / (T * a.top_k) : 0.0;
     const double mean = total > 0 ? s / T : 0.0;
-    a.counts[e] = n;
-    a.mean_probs[e] = (float)mean;
-    a.prob_grad[e] = total > 0 ? (float)((double)a.coef * a.E / T * (f - 1.0 / a.E)) : 0.0f;
+    if (threadIdx.x < FE) {
+      a.counts[e] = n;
+      a.mean_probs[e] = (float)mean;
+      a.prob_grad[e] = total > 0 ? (float)((double)a.coef * a.E / T * (f - 1.0 / a.E)) : 0.0f;
+    }
     term = f * mean;
   }
-  for (int d = 1; d < 64; d <<= 1) term += __shfl_xor(term, d);
+#pragma unroll
+  for (int d = 1; d < FE; d <<= 1) term += __shfl_xor(term, d);
+  unsigned before = 0;
   if (threadIdx.x == 0) {
     __hip_atomic_store(a.loss_partial + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    const unsigned before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    if (before == gridDim.x - 1) {
-      double sum = 0.0;
-      for (unsigned b = 0; b < gridDim.x; b++)
-        sum += __hip_atomic_load(a.loss_partial + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      *a.loss = (float)((double)a.coef * a.E * sum);
-    }
+    before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  before = __builtin_amdgcn_readfirstlane(before);
+  if (before == gridDim.x - 1) {
+    double sum = 0.0;
+    for (unsigned b = threadIdx.x; b < gridDim.x; b += 64)
+      sum += __hip_atomic_load(a.loss_partial + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    if (threadIdx.x == 0) *a.loss = (float)((double)a.coef * a.E * sum);
   }
 }
 
 template <int V>
 DEV void store_row(void* out, int f32, int64_t at, int E, int j, bool vec, const float (&d)[V]) {
-  if (vec) {
+  if (V > 4 && vec) {
 #pragma unroll
     for (int c = 0; c < V / 4; c++) {
-      const int e = expert_of(4 * c, j);
+      const int e = expert_of<V>(4 * c, j);
       if (e >= E) continue;
       if (f32) {
         *reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(out) + at + e) =
@@ -395,7 +625,7 @@ DEV void store_row(void* out, int f32, int64_t at, int E, int j, bool vec, const
   } else {
 #pragma unroll
     for (int i = 0; i < V; i++) {
-      const int e = expert_of(i, j);
+      const int e = expert_of<V>(i, j);
       if (e >= E) continue;
       if (f32) reinterpret_cast<float*>(out)[at + e] = d[i];
       else reinterpret_cast<uint16_t*>(out)[at + e] = f32_to_bf16(d[i]);
@@ -408,12 +638,18 @@ DEV void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 // The chosen experts' own terms are scattered through an LDS row of the token.
 template <int V>
 __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwardParams a, bool vec, bool vec_out) {
-  __shared__ float scatter[TOKENS][16 * V];
-  const int j = threadIdx.x & 15;
+  __shared__ __attribute__((aligned(16))) float scatter[TOKENS][16 * V];
   float* row_of = scatter[threadIdx.x >> 4];
   const float dl = a.prob_grad ? (a.d_loss ? *a.d_loss : 1.0f) : 0.0f;
   const bool need_p = a.prob_grad || (!a.sigmoid && !a.renormalize);
+  float u[V];  // the loss's gradient in the probabilities, the same for all tokens
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    const int e = expert_of<V>(i, threadIdx.x & 15);
+    u[i] = a.prob_grad ? a.prob_grad[min(e, a.E - 1)] * dl : 0.0f;
+  }
   for (int64_t t0 = (int64_t)blockIdx.x * TOKENS; t0 < a.M; t0 += (int64_t)gridDim.x * TOKENS) {
+    const int j = opaque(threadIdx.x & 15);
     const int64_t t = t0 + (threadIdx.x >> 4);
     const bool in = t < a.M;
     const bool on = in && (!a.token_mask || a.token_mask[t] != 0);
@@ -430,8 +666,9 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
 
     float all = 0.0f;  // sum of dw w, subtracted from every expert (softmax without renormalisation)
     if (a.d_weights) {
+      f32x4_t* mine = reinterpret_cast<f32x4_t*>(row_of + 4 * j);  // (all lanes clear the row)
 #pragma unroll
-      for (int i = 0; i < V; i++) row_of[expert_of(i, j)] = 0.0f;
+      for (int i = 0; i < V / 4; i++) mine[16 * i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
       int id[SLOTS];
       float w[SLOTS], dw[SLOTS], keep[SLOTS], ctop = -INFINITY, sum = 0.0f, dot = 0.0f;
 #pragma unroll
@@ -448,12 +685,12 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
           dw[q] = a.d_weights[t * a.top_k + s];
         }
         ctop = fmaxf(ctop, w[q]);
-        keep[q] = a.sigmoid ? 1.0f / (1.0f + expf(w[q])) : 1.0f;  // 1 - s
+        keep[q] = a.sigmoid ? sigmoid_f32(-w[q]) : 1.0f;  // 1 - s
       }
       ctop = row_max(ctop);
       if (!a.renormalize && !a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
+        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
         ctop = top;
       }
 #pragma unroll
@@ -479,24 +716,29 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
       for (int q = 0; q < SLOTS; q++)
         if (id[q] >= 0) atomicAdd(&row_of[id[q]], w[q] * (dw[q] - dot) * keep[q]);
       wave_fence();
+      if constexpr (V == 4) {
 #pragma unroll
-      for (int i = 0; i < V; i++) d[i] = row_of[expert_of(i, j)];
+        for (int i = 0; i < V; i++) d[i] = row_of[expert_of<V>(i, j)];
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; i++) {
+          const f32x4_t v = mine[16 * i];
+#pragma unroll
+          for (int x = 0; x < 4; x++) d[4 * i + x] = v[x];
+        }
+      }
       wave_fence();
     }
     if (need_p) {
-      float p[V], u[V], dot = 0.0f;
+      float p[V], dot = 0.0f;
       probabilities<V>(l, top, a.sigmoid, p);
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        const int e = expert_of(i, j);
-        u[i] = a.prob_grad && e < a.E ? a.prob_grad[e] * dl : 0.0f;
-        dot = fmaf(u[i], p[i], dot);
-      }
+      for (int i = 0; i < V; i++) dot = fmaf(u[i], p[i], dot);  // (p is 0 past the last expert)
       dot = row_add(dot);
 #pragma unroll
       for (int i = 0; i < V; i++) {
         float g = p[i] * (u[i] - dot);
-        if (a.sigmoid) g = g / (1.0f + expf(l[i]));
+        if (a.sigmoid) g = g * sigmoid_f32(-l[i]);
         else g -= p[i] * all;
         d[i] += g;
       }
@@ -523,26 +765,28 @@ template <int V>
 hipError_t launch_v(const RouterParams& p, hipStream_t s) {
   const bool vec = whole_groups(p.logits, p.logits_f32, p.row_stride, p.E);
   const bool stats = p.prob_partial != nullptr;
-  const unsigned grid = stats ? (unsigned)router_partials(p.M, p.E) : token_blocks(p.M);
-  if (!p.select) router_kernel<V, false, false, true><<<grid, RT, 0, s>>>(p, vec);
-  else if (p.select_bias && stats) router_kernel<V, true, true, true><<<grid, RT, 0, s>>>(p, vec);
-  else if (p.select_bias) router_kernel<V, true, true, false><<<grid, RT, 0, s>>>(p, vec);
-  else if (stats) router_kernel<V, true, false, true><<<grid, RT, 0, s>>>(p, vec);
-  else router_kernel<V, true, false, false><<<grid, RT, 0, s>>>(p, vec);
+  const unsigned grid = stats ? (unsigned)router_partials(p.M) : token_blocks(p.M);
+  const int threads = threads_of(stats);
+  if (!p.select) router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
+  else if (p.select_bias && stats) router_kernel<V, true, true, true><<<grid, threads, 0, s>>>(p, vec);
+  else if (p.select_bias) router_kernel<V, true, true, false><<<grid, threads, 0, s>>>(p, vec);
+  else if (stats) router_kernel<V, true, false, true><<<grid, threads, 0, s>>>(p, vec);
+  else router_kernel<V, true, false, false><<<grid, threads, 0, s>>>(p, vec);
   return hipGetLastError();
 }
 
 template <int V>
 hipError_t launch_back(const RouterBackwardParams& p, hipStream_t s) {
-  router_backward_kernel<V><<<token_blocks(p.M), RT, 0, s>>>(
+  // (2048 workgroups fill the CUs, and walk the rest of the tokens)
+  router_backward_kernel<V><<<std::min(2048u, token_blocks(p.M)), RT, 0, s>>>(
       p, whole_groups(p.logits, p.logits_f32, p.row_stride, p.E), whole_groups(p.d_logits, p.logits_f32, p.E, p.E));
   return hipGetLastError();
 }
 
 }  // namespace
 
-int router_partials(int64_t M, int) {
-  const int64_t b = (M + TOKENS - 1) / TOKENS;
+int router_partials(int64_t M) {
+  const int64_t b = (M + STAT_TOKENS - 1) / STAT_TOKENS;
   return (int)(b < 1 ? 1 : b > 512 ? 512 : b);
 }
 
