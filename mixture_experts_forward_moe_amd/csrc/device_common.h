@@ -120,6 +120,39 @@ DEV uint32_t mx_scale_code(float amax, int emax) {
   return (uint32_t)(c < 0 ? 0 : (c > 254 ? 254 : c));
 }
 
+// The value of the lane that CTRL (a DPP control) names.
+template <int CTRL>
+DEV float dpp_f32(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
+// DPP controls: lane XOR 1 / 2 of a quad, mirrored half row / row: a maximum or
+// a sum over 16 lanes in four steps
+constexpr int DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_HALF_MIRROR = 0x141, DPP_MIRROR = 0x140;
+
+// Eight values of a 32-value MX block that a quad of lanes holds (values `at`
+// .. at + 7 of the array, m their largest magnitude): stores their codes (elem
+// 0: E4M3, 1: packed E2M1) and returns the block's E8M0 code.
+DEV uint32_t mx_store8(const float (&v)[8], float m, int elem, uint8_t* q, int64_t at) {
+  m = fmaxf(m, dpp_f32<DPP_XOR1>(m));
+  m = fmaxf(m, dpp_f32<DPP_XOR2>(m));
+  if (elem == 0) {
+    const uint32_t code = mx_scale_code(m, 8);
+    uint2 o;
+    o.x = f32x2_to_e4m3x2_mx(v[0], v[1], code) | (f32x2_to_e4m3x2_mx(v[2], v[3], code) << 16);
+    o.y = f32x2_to_e4m3x2_mx(v[4], v[5], code) | (f32x2_to_e4m3x2_mx(v[6], v[7], code) << 16);
+    *reinterpret_cast<uint2*>(q + at) = o;
+    return code;
+  }
+  const uint32_t code = mx_scale_code(m, 2);
+  const float s = e8m0_scale_operand(code);
+  uint32_t o = 0;
+#pragma unroll
+  for (int j = 0; j < 4; j++) o |= f32x2_to_e2m1x2(v[2 * j], v[2 * j + 1], s) << (8 * j);
+  *reinterpret_cast<uint32_t*>(q + at / 2) = o;
+  return code;
+}
+
 DEV float warp_max16(float v) {
   // max over the 16 lanes of a DPP row (lanes 16q .. 16q+15)
   v = fmaxf(v, __shfl_xor(v, 1));

@@ -167,53 +167,34 @@ hipError_t launch_quantize_nvfp4(const uint16_t* x, int64_t batches, int64_t row
   return hipGetLastError();
 }
 
-// one thread per 32-element block
-__global__ void quantize_mx_kernel(const uint16_t* __restrict__ x, int elem, uint8_t* __restrict__ q,
-                                   uint8_t* __restrict__ sf, int64_t total_blocks) {
-  int64_t blk = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (blk >= total_blocks) return;
-  const u32x4_t* src = reinterpret_cast<const u32x4_t*>(x + blk * 32);
-  float v[32];
-  for (int c = 0; c < 4; c++) {
-    u32x4_t a = src[c];
+// Eight values a thread, a quad of lanes a 32-element block: neighbouring lanes
+// read and write neighbouring bytes (16384 x 4096 to E2M1: 30 us
+// against 52 with a whole block a thread, whose loads lie 64 bytes apart).
+__global__ __launch_bounds__(256) void quantize_mx_kernel(const uint16_t* __restrict__ x, int elem,
+                                                          uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
+                                                          int64_t total) {
+  // (whole quads: total is a multiple of 4)
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < total; at += (int64_t)gridDim.x * 256) {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(x + at * 8);
+    float v[8], m = 0.0f;
+#pragma unroll
     for (int k = 0; k < 4; k++) {
-      v[8 * c + 2 * k] = __uint_as_float(a[k] << 16);
-      v[8 * c + 2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u);
+      v[2 * k] = __uint_as_float(a[k] << 16);
+      v[2 * k + 1] = __uint_as_float(a[k] & 0xffff0000u);
     }
-  }
-  float m = 0.0f;
-  for (int i = 0; i < 32; i++) m = fmaxf(m, fabsf(v[i]));
-  if (elem == 0) {
-    uint32_t code = mx_scale_code(m, 8);
-    u32x4_t o[2];
-    for (int i = 0; i < 8; i++) {
-      uint32_t p0 = f32x2_to_e4m3x2_mx(v[4 * i], v[4 * i + 1], code);
-      uint32_t p1 = f32x2_to_e4m3x2_mx(v[4 * i + 2], v[4 * i + 3], code);
-      o[i / 4][i % 4] = p0 | (p1 << 16);
-    }
-    u32x4_t* dst = reinterpret_cast<u32x4_t*>(q + blk * 32);
-    dst[0] = o[0];
-    dst[1] = o[1];
-    sf[blk] = (uint8_t)code;
-  } else {
-    uint32_t code = mx_scale_code(m, 2);
-    float scale = e8m0_scale_operand(code);
-    u32x4_t o;
-    for (int i = 0; i < 4; i++) {
-      uint32_t w = 0;
-      for (int k = 0; k < 4; k++) w |= f32x2_to_e2m1x2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1], scale) << (8 * k);
-      o[i] = w;
-    }
-    reinterpret_cast<u32x4_t*>(q + blk * 16)[0] = o;
-    sf[blk] = (uint8_t)code;
+#pragma unroll
+    for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[i]));
+    const uint32_t code = mx_store8(v, m, elem, q, at * 8);
+    if ((threadIdx.x & 3) == 0) sf[at / 4] = (uint8_t)code;
   }
 }
 
 hipError_t launch_quantize_mx(const uint16_t* x, int64_t rows, int64_t cols, int elem, uint8_t* q, uint8_t* sf,
                               hipStream_t stream) {
-  int64_t total = rows * (cols / 32);
+  const int64_t total = rows * (cols / 8);
   if (total == 0) return hipSuccess;
-  quantize_mx_kernel<<<(unsigned)((total + 255) / 256), 256, 0, stream>>>(x, elem, q, sf, total);
+  const int64_t blocks = (total + 255) / 256;
+  quantize_mx_kernel<<<(unsigned)(blocks < 1 << 23 ? blocks : 1 << 23), 256, 0, stream>>>(x, elem, q, sf, total);
   return hipGetLastError();
 }
 

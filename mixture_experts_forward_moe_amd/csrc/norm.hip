@@ -17,20 +17,11 @@ namespace moe {
 
 namespace {
 
-// values of lanes XOR 1 / 2 of a quad, and of the mirrored half row / row:
-// max or sum over 16 lanes in four steps
-template <int CTRL>
-DEV float dpp(float v) {
-  return __builtin_bit_cast(
-      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-constexpr int QUAD_XOR1 = 0xB1, QUAD_XOR2 = 0x4E, ROW_HALF_MIRROR = 0x141, ROW_MIRROR = 0x140;
-
 DEV float wave_sum(float v) {
-  v += dpp<QUAD_XOR1>(v);
-  v += dpp<QUAD_XOR2>(v);
-  v += dpp<ROW_HALF_MIRROR>(v);
-  v += dpp<ROW_MIRROR>(v);
+  v += dpp_f32<DPP_XOR1>(v);
+  v += dpp_f32<DPP_XOR2>(v);
+  v += dpp_f32<DPP_HALF_MIRROR>(v);
+  v += dpp_f32<DPP_MIRROR>(v);
   v += __shfl_xor(v, 16);
   v += __shfl_xor(v, 32);
   return v;
@@ -159,24 +150,8 @@ __global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormPa
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(f[j]));
-        m = fmaxf(m, dpp<QUAD_XOR1>(m));
-        m = fmaxf(m, dpp<QUAD_XOR2>(m));
-        uint32_t code;
         const int64_t at = row * a.H + 8 * v;
-        if (a.elem == 0) {
-          code = mx_scale_code(m, 8);
-          uint2 o;
-          o.x = f32x2_to_e4m3x2_mx(f[0], f[1], code) | (f32x2_to_e4m3x2_mx(f[2], f[3], code) << 16);
-          o.y = f32x2_to_e4m3x2_mx(f[4], f[5], code) | (f32x2_to_e4m3x2_mx(f[6], f[7], code) << 16);
-          *reinterpret_cast<uint2*>(a.q + at) = o;
-        } else {
-          code = mx_scale_code(m, 2);
-          const float s = e8m0_scale_operand(code);
-          uint32_t o = 0;
-#pragma unroll
-          for (int j = 0; j < 4; j++) o |= f32x2_to_e2m1x2(f[2 * j], f[2 * j + 1], s) << (8 * j);
-          *reinterpret_cast<uint32_t*>(a.q + at / 2) = o;
-        }
+        const uint32_t code = mx_store8(f, m, a.elem, a.q, at);
         if ((t & 3) == 0) a.q_sf[at / 32] = (uint8_t)code;
       }
     }

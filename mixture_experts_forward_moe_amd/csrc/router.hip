@@ -40,8 +40,6 @@ constexpr int threads_of(bool stats) { return stats ? 512 : 256; }
 constexpr int RT = 256, TOKENS = RT / 16;  // of the backward pass
 constexpr int STAT_TOKENS = threads_of(true) / 16;
 
-constexpr int QUAD_XOR1 = 0xB1, QUAD_XOR2 = 0x4E, ROW_HALF_MIRROR = 0x141, ROW_MIRROR = 0x140;
-
 template <int CTRL>
 DEV int dpp(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xf, 0xf, true);
@@ -66,10 +64,10 @@ DEV int dpp_zero(int v) {
 // a reduction over the 16 lanes of a token
 template <typename T, typename F>
 DEV T row_reduce(T v, F f) {
-  v = f(v, dpp<QUAD_XOR1>(v));
-  v = f(v, dpp<QUAD_XOR2>(v));
-  v = f(v, dpp<ROW_HALF_MIRROR>(v));
-  return f(v, dpp<ROW_MIRROR>(v));
+  v = f(v, dpp<DPP_XOR1>(v));
+  v = f(v, dpp<DPP_XOR2>(v));
+  v = f(v, dpp<DPP_HALF_MIRROR>(v));
+  return f(v, dpp<DPP_MIRROR>(v));
 }
 template <typename T>
 DEV T row_max(T v) {
@@ -591,13 +589,17 @@ __global__ __launch_bounds__(FT) void balance_finish_kernel(const BalanceParams 
   }
 #pragma unroll
   for (int d = 1; d < FE; d <<= 1) term += __shfl_xor(term, d);
+  // The term goes to memory (agent scope) and is there (vmcnt 0) before the
+  // ticket is taken; the terms are read the same way.  No release or acquire
+  // of that scope, which would write back and drop this XCD's L2.
   unsigned before = 0;
-  if (threadIdx.x == 0) {
-    __hip_atomic_store(a.loss_partial + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  if (threadIdx.x == 0) __hip_atomic_store(a.loss_partial + blockIdx.x, term, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup");  // keeps the store above the wait
+  __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): expcnt and lgkmcnt not waited
+  if (threadIdx.x == 0) before = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   before = __builtin_amdgcn_readfirstlane(before);
   if (before == gridDim.x - 1) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup");  // keeps the loads below the ticket
     double sum = 0.0;
     for (unsigned b = threadIdx.x; b < gridDim.x; b += 64)
       sum += __hip_atomic_load(a.loss_partial + b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
