@@ -67,22 +67,39 @@ hipError_t allow_lds(int bytes, int* cus) {
 
 // ------------------------------------------------------------- tiled kernel
 
-constexpr int MK = 128;  // K per stage
-constexpr int GS = 4;    // stages per scale group (16 E8M0 bytes a row)
-
 // The column (0..31) that MFMA row i of a weight tile stands for: lane half
 // h, element j of the 32x32 result holds row 8 (j / 4) + 4 h + j % 4, which
 // is column 16 h + j: a lane has 16 consecutive columns of one y row.
 DEV int tile_col(int i) { return 16 * ((i >> 2) & 1) + 4 * (i >> 3) + (i & 3); }
 
-template <int XE, int TM, int TN, int NBUF, int KG>
+// Chunks (16 bytes) of a row in a stage: C = 4, 8 or 16 of them, 1024 / (16 C)
+// rows a LDS-DMA load.  A load fills fixed LDS positions (lane i 16 i past the
+// base), so the swizzle that spreads the fragment reads over the banks is
+// applied to what each lane loads: rows of 4 chunks are swizzled by row / 4, of
+// 8 by row / 2, of 16 by the row.  Of that number the low two bits are the
+// lane's (lane / 16), the others the load's own.
+template <int C>
+struct Chunks {
+  static constexpr int ROWS = 64 / C;
+  static constexpr int KINDS = C / 4;  // kinds of loads: load i is of kind i % KINDS
+  static DEV int row(int load, int lane) { return ROWS * load + lane / C; }
+  // byte in the row's part of a stage that a lane loads, in loads of kind v
+  static DEV int source(int v, int lane) { return 16 * (((lane & (C - 1)) ^ ((lane >> 4) & 3)) ^ (4 * v)); }
+  // byte of logical chunk c in row r of a stage
+  static DEV int at(int r, int c) {
+    return 16 * C * r + 16 * (c ^ (C == 4 ? (r >> 2) & 3 : C == 8 ? (r >> 1) & 7 : r & 15));
+  }
+};
+
+template <int XE, int TM, int TN, int KS, int NBUF, int KG>
 struct Shape {
   static constexpr int BM = 64 * TM, BN = 64 * TN;  // 2 x 2 wavefronts of 32 TM x 32 TN, KG times
-  static constexpr int XB = XE == 1 ? MK / 2 : MK;  // bytes of a row in a stage
-  static constexpr int WB = MK / 2;
+  static constexpr int XB = XE == 1 ? KS / 2 : KS;  // bytes of a row in a stage of KS
+  static constexpr int WB = KS / 2;
   static constexpr int NX = BM * XB / 4096, NW = BN * WB / 4096;  // LDS-DMA loads a wavefront and stage
   static constexpr int STAGE = BM * XB + BN * WB;
-  static constexpr int SC = (BM + BN) * 16;         // a scale group: x rows, then weight rows
+  static constexpr int GS = 512 / KS;               // stages of a scale record (16 E8M0 bytes)
+  static constexpr int SC = (BM + BN) * 16;         // the records: x rows, then weight rows
   static constexpr int SC_OFF = NBUF * STAGE;
   static constexpr int RING = SC_OFF + SC;          // a K group's part
   static constexpr int JOIN = KG > 1 ? KG / 2 * BM * BN * 4 : 0;
@@ -279,11 +296,18 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
   }
 }
 
-template <int XE, bool WIDE, int TM, int TN, int NBUF, int KG, int PER_CU>
+template <int XE, bool WIDE, int TM, int TN, int KS, int NBUF, int KG, int PER_CU>
 __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(const LinearParams a, int tiles_m,
                                                                             int tiles_n) {
-  using S = Shape<XE, TM, TN, NBUF, KG>;
-  constexpr int XB = S::XB, WB = S::WB, NX = S::NX, NW = S::NW, BM = S::BM, BN = S::BN;
+  using S = Shape<XE, TM, TN, KS, NBUF, KG>;
+  using X = Chunks<S::XB / 16>;
+  using W = Chunks<S::WB / 16>;
+  constexpr int XB = S::XB, WB = S::WB, NX = S::NX, NW = S::NW, BM = S::BM, BN = S::BN, GS = S::GS;
+  constexpr int ND = NX + NW;
+  constexpr int NQ = TN * TM;                          // MFMAs of 64 K
+  constexpr int NF = TN + TM * (XE == 1 ? 1 : 2);      // their fragment reads
+  constexpr int QS = KS / 64;                          // 64-K steps of a stage
+  static_assert(NX % X::KINDS == 0 && NW % W::KINDS == 0, "a load's kind goes by its number");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
   const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) & 3;
@@ -293,7 +317,7 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
   const int r = lane & 31, h = lane >> 5;
   const int nb = a.K / 32;
   // stages of each K group (past the end of K: scales 0)
-  const int KT = ((a.K + MK - 1) / MK + KG - 1) / KG, k_first = kg * KT;
+  const int KT = ((a.K + KS - 1) / KS + KG - 1) / KG, k_first = kg * KT;
   const int xrb = XE == 1 ? a.K / 2 : a.K, wrb = a.K / 2;
 
   // tile of this workgroup: the XCDs (workgroups are dealt to them round
@@ -314,44 +338,37 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
   }
 
   // source rows of this lane's LDS-DMA loads (rows past the end: the last
-  // row, whose products are not stored) and its 16-byte chunk of a row
+  // row, whose products are not stored)
   const uint8_t* xb = a.x + m0 * xrb;
   const uint8_t* wb = a.w + (int64_t)n0 * wrb;
   const int last_m = (int)min((int64_t)BM, a.M - m0) - 1, last_n = min(BN, a.N - n0) - 1;
   uint32_t xo[NX], wo[NW];
 #pragma unroll
-  for (int j = 0; j < NX; j++) {
-    const int row = XE == 1 ? 16 * (NX * wave + j) + (lane >> 2) : 8 * (NX * wave + j) + (lane >> 3);
-    xo[j] = (uint32_t)min(row, last_m) * (uint32_t)xrb;
-  }
+  for (int j = 0; j < NX; j++) xo[j] = (uint32_t)min(X::row(NX * wave + j, lane), last_m) * (uint32_t)xrb;
 #pragma unroll
   for (int j = 0; j < NW; j++) {
-    const int b = 16 * (NW * wave + j) + (lane >> 2);
+    const int b = W::row(NW * wave + j, lane);
     wo[j] = (uint32_t)min((b & ~31) + tile_col(b & 31), last_n) * (uint32_t)wrb;
   }
-  // logical chunk of the physical one this lane fills (fp4: 4 a row, swizzled
-  // by row / 4; fp8: 8, by row / 2, which alternates with the load's parity)
-  const int cw = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
-  const int cx = XE == 1 ? cw : 16 * ((lane & 7) ^ ((lane >> 4) & 3));
-
-  // K offsets of a stage's loads; a chunk past the end of its row: the row's
+  // the loads of stage s into st; a chunk past the end of its row: the row's
   // first one (its scale is 0)
-  struct Src {
-    uint32_t w, x0, x1;
-  };
-  auto sources = [&](int s_) {
+  auto issue = [&](int s_, uint8_t* st) {
     const int s = k_first + s_;
-    const uint32_t kw = (uint32_t)(s * WB + cw), k0 = (uint32_t)(s * XB + cx), k1 = (uint32_t)(s * XB + (cx ^ 64));
-    return Src{kw < (uint32_t)wrb ? kw : 0u, k0 < (uint32_t)xrb ? k0 : 0u, k1 < (uint32_t)xrb ? k1 : 0u};
-  };
-  auto issue_one = [&](const Src& s, uint8_t* st, int i) {
-    if (i < NX) {
-      // (fp8: row / 2 of load NX wave + i has bit 2 = that load's parity)
-      const bool odd = XE == 0 && ((NX * wave + i) & 1);
-      dma16(xb + (xo[i] + (odd ? s.x1 : s.x0)), st + 1024 * (NX * wave + i));
-    } else {
-      dma16(wb + (wo[i - NX] + s.w), st + BM * XB + 1024 * (NW * wave + i - NX));
+    uint32_t ox[X::KINDS], ow[W::KINDS];
+#pragma unroll
+    for (int v = 0; v < X::KINDS; v++) {
+      const uint32_t k = (uint32_t)(s * XB + X::source(v, lane));
+      ox[v] = k < (uint32_t)xrb ? k : 0u;
     }
+#pragma unroll
+    for (int v = 0; v < W::KINDS; v++) {
+      const uint32_t k = (uint32_t)(s * WB + W::source(v, lane));
+      ow[v] = k < (uint32_t)wrb ? k : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < NX; i++) dma16(xb + (xo[i] + ox[i % X::KINDS]), st + 1024 * (NX * wave + i));
+#pragma unroll
+    for (int i = 0; i < NW; i++) dma16(wb + (wo[i] + ow[i % W::KINDS]), st + BM * XB + 1024 * (NW * wave + i));
   };
 
   // scales: thread t carries rows t, t + 256, .. of x then w (past the last: that one again)
@@ -363,6 +380,7 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
     sp[i] = row < BM ? a.x_sf + (m0 + min(row, last_m)) * nb
                      : a.w_sf + (int64_t)(n0 + min((b & ~31) + tile_col(b & 31), last_n)) * nb;
   }
+  const int sc_first = k_first * (KS / 32);  // scale byte of this K group's first stage
   // (one LDS area: every wave has its records of group g in registers since
   // before the first barrier of the group, and g + 1 is put before the last)
   auto put_scales = [&](const u32x4_t (&v)[NS]) {
@@ -371,20 +389,19 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
       *reinterpret_cast<u32x4_t*>(smem + S::SC_OFF + 16 * min(tid + 256 * i, BM + BN - 1)) = v[i];
   };
 
+  // (the scales first: what waits for them does not wait for the stages)
   u32x4_t sv[NS];
 #pragma unroll
-  for (int i = 0; i < NS; i++) sv[i] = u32x4_t{0u, 0u, 0u, 0u};
+  for (int i = 0; i < NS; i++)
+    sv[i] = nb >= 16 ? ld16u(scale_source(sp[i], sc_first, nb)) : scale_short(sp[i], sc_first, nb);
 #pragma unroll
   for (int s = 0; s < NBUF; s++) {
     if (s >= KT) break;
-    const Src src = sources(s);
-#pragma unroll
-    for (int i = 0; i < NX + NW; i++) issue_one(src, smem + s * S::STAGE, i);
+    issue(s, smem + s * S::STAGE);
   }
 #pragma unroll
   for (int i = 0; i < NS; i++)
-    sv[i] = nb >= 16 ? scale_shift(ld16u(scale_source(sp[i], 4 * k_first, nb)), 4 * k_first, nb)
-                      : scale_short(sp[i], 4 * k_first, nb);
+    if (nb >= 16) sv[i] = scale_shift(sv[i], sc_first, nb);
   put_scales(sv);
 
   f32x16_t acc[TN][TM];
@@ -394,26 +411,23 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
     for (int m = 0; m < TM; m++)
 #pragma unroll
       for (int i = 0; i < 16; i++) acc[n][m][i] = 0.0f;
-
-  // fragment addresses in a stage
-  const int wrow = 32 * TN * wn + r, xrow = 32 * TM * wm + r;
-  const int wsw = (r >> 2) & 3, xsw = (r >> 1) & 7;
-  constexpr int ND = NX + NW;
-  constexpr int NF = TN + TM * (XE == 1 ? 1 : 2);  // fragment reads of a half stage
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+  if (NBUF <= KT) __builtin_amdgcn_s_waitcnt(waitcnt_vm((NBUF - 1) * ND));
+  else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
   ring_barrier();
 
+  const int wrow = 32 * TN * wn + r, xrow = 32 * TM * wm + r;
   u32x4_t w0[TN], w1[TN], sw[TN], sx[TM];
   XFrag<XE> x0[TM], x1[TM];
-  // fragment read i of a half stage
+  // fragment read i of 64-K step u
   auto read = [&](const uint8_t* st, int u, int i, u32x4_t (&w)[TN], XFrag<XE> (&x)[TM]) {
     if (i < TN) {
-      w[i] = *reinterpret_cast<const u32x4_t*>(st + BM * XB + (wrow + 32 * i) * WB + 16 * ((2 * u + h) ^ wsw));
+      w[i] = *reinterpret_cast<const u32x4_t*>(st + BM * XB + 32 * WB * i + W::at(wrow, 2 * u + h));
     } else if (XE == 1) {
-      x[i - TN].p[0] = *reinterpret_cast<const u32x4_t*>(st + (xrow + 32 * (i - TN)) * XB + 16 * ((2 * u + h) ^ wsw));
+      x[i - TN].p[0] = *reinterpret_cast<const u32x4_t*>(st + 32 * XB * (i - TN) + X::at(xrow, 2 * u + h));
     } else {
       const int m = (i - TN) >> 1, e = (i - TN) & 1;
-      x[m].p[XE == 1 ? 0 : e] = *reinterpret_cast<const u32x4_t*>(st + (xrow + 32 * m) * XB + 16 * ((4 * u + 2 * e + h) ^ xsw));
+      x[m].p[XE == 1 ? 0 : e] =
+          *reinterpret_cast<const u32x4_t*>(st + 32 * XB * m + X::at(xrow, 4 * u + 2 * e + h));
     }
   };
   // this lane's scale records of the group in LDS
@@ -434,27 +448,40 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
   };
   auto pin_all = [&]() {
 #pragma unroll
-    for (int i = 0; i < TN * TM; i++) pin<TN * TM>(acc[i / TM][i % TM]);
+    for (int i = 0; i < NQ; i++) pin<NQ>(acc[i / TM][i % TM]);
+  };
+  // reads of one step's fragments between the MFMAs of another
+  auto order = [&]() {
+#pragma unroll
+    for (int i = 0; i < (NF > NQ ? NF : NQ); i++) {
+      if (i < NF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i < NQ) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
   // Stage s, number I of its group.
   auto stage = [&](int s, auto I_, int next_group) {
     constexpr int I = decltype(I_)::value;
     uint8_t* st = smem + (s % NBUF) * S::STAGE;
     const uint8_t* sn = smem + ((s + 1) % NBUF) * S::STAGE;
+    auto step = [&](auto u_, const u32x4_t (&w)[TN], const XFrag<XE> (&x)[TM], u32x4_t (&wn)[TN], XFrag<XE> (&xn)[TM],
+                    const uint8_t* from) {
+      constexpr int u = decltype(u_)::value, word = I * (4 / GS) + u / 2;
 #pragma unroll
-    for (int i = 0; i < NF; i++) read(st, 1, i, w1, x1);
+      for (int i = 0; i < NF; i++) read(from, (u + 1) % QS, i, wn, xn);
 #pragma unroll
-    for (int i = 0; i < TN * TM; i++)
-      mfma_one<XE, 0>(acc[i / TM][i % TM], w0[i / TM], x0[i % TM], (int)sw[i / TM][I], (int)sx[i % TM][I]);
-#pragma unroll
-    for (int i = 0; i < (NF > TN * TM ? NF : TN * TM); i++) {
-      if (i < NF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (i < TN * TM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      for (int i = 0; i < NQ; i++)
+        mfma_one<XE, u & 1>(acc[i / TM][i % TM], w[i / TM], x[i % TM], (int)sw[i / TM][word], (int)sx[i % TM][word]);
+      order();
+    };
+    step(std::integral_constant<int, 0>{}, w0, x0, w1, x1, st);
+    if constexpr (QS == 4) {
+      step(std::integral_constant<int, 1>{}, w1, x1, w0, x0, st);
+      step(std::integral_constant<int, 2>{}, w0, x0, w1, x1, st);
     }
-    __builtin_amdgcn_sched_barrier(0);
     if (next_group > 0) {
 #pragma unroll
-      for (int i = 0; i < NS; i++) sv[i] = scale_shift(sv[i], 4 * k_first + 16 * next_group, nb);
+      for (int i = 0; i < NS; i++) sv[i] = scale_shift(sv[i], sc_first + 16 * next_group, nb);
       put_scales(sv);
     }
     // stage s + 1 has landed: with the ring full, all but the newest loads
@@ -462,29 +489,16 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
     else __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     ring_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    // every wave is done with this stage's buffer
-    if (s + NBUF < KT) {
-      const Src src = sources(s + NBUF);
-#pragma unroll
-      for (int i = 0; i < ND; i++) issue_one(src, st, i);
-    }
-#pragma unroll
-    for (int i = 0; i < (TN * TM > NF ? TN * TM : NF); i++) {
-      if (i < NF) read(sn, 0, i, w0, x0);  // (past the last stage: unused)
-      if (i < TN * TM)
-        mfma_one<XE, 1>(acc[i / TM][i % TM], w1[i / TM], x1[i % TM], (int)sw[i / TM][I], (int)sx[i % TM][I]);
-    }
-#pragma unroll
-    for (int i = 0; i < (NF > TN * TM ? NF : TN * TM); i++) {
-      if (i < NF) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (i < TN * TM) __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    }
+    // every wave has this stage's fragments: refill its buffer
+    if (s + NBUF < KT) issue(s + NBUF, st);
+    // (past the last stage: reads that are not used)
+    step(std::integral_constant<int, QS - 1>{}, w1, x1, w0, x0, sn);
     pin_all();
   };
   using I0 = std::integral_constant<int, 0>;
   using I1 = std::integral_constant<int, 1>;
-  using I2 = std::integral_constant<int, 2>;
-  using I3 = std::integral_constant<int, 3>;
+  using I2 = std::integral_constant<int, 2 % GS>;
+  using I3 = std::integral_constant<int, 3 % GS>;
 
 #pragma unroll
   for (int i = 0; i < NF; i++) read(smem, 0, i, w0, x0);
@@ -493,25 +507,24 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
   for (int g = 0; g < groups; g++) {
     read_scales();
 #pragma unroll
-    for (int i = 0; i < NS; i++) sv[i] = ld16u(scale_source(sp[i], 4 * k_first + 16 * (g + 1), nb));
+    for (int i = 0; i < NS; i++) sv[i] = ld16u(scale_source(sp[i], sc_first + 16 * (g + 1), nb));
     stage(GS * g, I0{}, 0);
-    stage(GS * g + 1, I1{}, 0);
-    stage(GS * g + 2, I2{}, 0);
-    stage(GS * g + 3, I3{}, g + 1);
+    if constexpr (GS == 4) {
+      stage(GS * g + 1, I1{}, 0);
+      stage(GS * g + 2, I2{}, 0);
+      stage(GS * g + 3, I3{}, g + 1);
+    } else {
+      stage(GS * g + 1, I1{}, g + 1);
+    }
   }
   const int s0 = GS * groups;
   if (s0 < KT) {
     read_scales();
     stage(s0, I0{}, 0);
-    if (s0 + 1 < KT) {
-      stage(s0 + 1, I1{}, 0);
-    }
-    if (s0 + 2 < KT) {
-      stage(s0 + 2, I2{}, 0);
-    }
-    if (s0 + 3 < KT) stage(s0 + 3, I3{}, 0);
+    if (s0 + 1 < KT) stage(s0 + 1, I1{}, 0);
+    if (GS == 4 && s0 + 2 < KT) stage(s0 + 2, I2{}, 0);
+    if (GS == 4 && s0 + 3 < KT) stage(s0 + 3, I3{}, 0);
   }
-
   ring_barrier();  // the other waves have read the stages that the joins and the way out overwrite
   // the K groups' sums: the upper half hands its accumulators to the lower
   // one, until the first group has all of them
@@ -544,16 +557,16 @@ __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(cons
   store_tiles<WIDE, TM, TN, 2048>(a, acc, m0 + 32 * TM * wm, n0 + 32 * TN * wn, smem + 2048 * wave, lane);
 }
 
-template <int XE, bool WIDE, int TM, int TN, int NBUF, int KG, int PER_CU>
+template <int XE, bool WIDE, int TM, int TN, int KS, int NBUF, int KG, int PER_CU>
 hipError_t launch_tile_as(const LinearParams& p, hipStream_t s) {
-  using S = Shape<XE, TM, TN, NBUF, KG>;
+  using S = Shape<XE, TM, TN, KS, NBUF, KG>;
   static_assert(S::LDS * PER_CU <= 160 * 1024, "LDS ring exceeds the CU's LDS");
   int cus = 0;
-  const hipError_t err = allow_lds<linear_tile_kernel<XE, WIDE, TM, TN, NBUF, KG, PER_CU>>(S::LDS, &cus);
+  const hipError_t err = allow_lds<linear_tile_kernel<XE, WIDE, TM, TN, KS, NBUF, KG, PER_CU>>(S::LDS, &cus);
   if (err != hipSuccess) return err;
   const int tm = (p.M + S::BM - 1) / S::BM, tn = (p.N + S::BN - 1) / S::BN;
   const unsigned grid = (unsigned)(((int64_t)tm * tn + 7) / 8 * 8);
-  linear_tile_kernel<XE, WIDE, TM, TN, NBUF, KG, PER_CU><<<grid, 256 * KG, S::LDS, s>>>(p, tm, tn);
+  linear_tile_kernel<XE, WIDE, TM, TN, KS, NBUF, KG, PER_CU><<<grid, 256 * KG, S::LDS, s>>>(p, tm, tn);
   return hipGetLastError();
 }
 
@@ -562,10 +575,10 @@ bool wide_rows(const LinearParams& p) {
   return !p.y_f32 && !p.accumulate && p.N % 8 == 0 && ((uintptr_t)p.y & 15) == 0;
 }
 
-template <int XE, int TM, int TN, int NBUF, int KG, int PER_CU>
+template <int XE, int TM, int TN, int KS, int NBUF, int KG, int PER_CU>
 hipError_t launch_tile(const LinearParams& p, hipStream_t s) {
-  return wide_rows(p) ? launch_tile_as<XE, true, TM, TN, NBUF, KG, PER_CU>(p, s)
-                      : launch_tile_as<XE, false, TM, TN, NBUF, KG, PER_CU>(p, s);
+  return wide_rows(p) ? launch_tile_as<XE, true, TM, TN, KS, NBUF, KG, PER_CU>(p, s)
+                      : launch_tile_as<XE, false, TM, TN, KS, NBUF, KG, PER_CU>(p, s);
 }
 
 // ------------------------------------------------------------- persistent kernel
@@ -988,21 +1001,33 @@ hipError_t launch(const LinearParams& p, hipStream_t s) {
     linear_stream_kernel<XE><<<grid, 64 * STREAM_WAVES, 0, s>>>(p);
     return hipGetLastError();
   }
-  // Few tiles: 64 x 64, with K split in two where it is long (128 x 4096 x
-  // 4096: 7.5 us against 8.5; 64 x 8192 x 1024: 4.4 against 4.2).
+  // Few tiles: 64 x 64, with K split in two where it is long (E2M1: 128 x 4096
+  // x 4096 7.4 us against 8.2; 64 x 8192 x 1024 4.5 against 4.3).
   if (tiles(64, 64) <= CUS)
-    return p.K >= 2048 ? launch_tile<XE, 1, 1, 4, 2, 1>(p, s) : launch_tile<XE, 1, 1, 4, 1, 2>(p, s);
-  if (!wide_rows(p)) return launch_tile_as<XE, false, 1, 2, 4, 1, 2>(p, s);
+    return p.K >= 2048 ? launch_tile<XE, 1, 1, 128, 4, 2, 1>(p, s) : launch_tile<XE, 1, 1, 256, 2, 1, 2>(p, s);
+  if (!wide_rows(p)) return launch_tile_as<XE, false, 1, 2, 256, XE == 1 ? 3 : 2, 1, 2>(p, s);
   // 256 x 256 tiles in whole rounds of the CUs, three quarters full at least
   // (2048 x 6144 x 4096, 0.75: 34.7 us against 44.5 in 128 x 128 tiles; 4096 x
   // 5120 x 2048, 0.63: 37.1 against 37.2, E4M3 53.9 against 47.0), and with
   // enough stages to fill its pipeline (8192 x 8192 x 512: 53.0 against 39.9).
-  const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS;
+  const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS, t128 = tiles(128, 128);
   if (p.K >= 1024 && 4 * big >= 3 * CUS * rounds) return launch_big<XE>(p, s);
-  // 128 x 128 tiles once they fill the CUs half (1024 x 4096 x 4096, one a CU:
-  // 18.2 us against 21.0 in 64 x 128; 512 x 4096 x 4096, half: 14.5 against 11.9)
-  if (tiles(128, 128) <= CUS / 2) return launch_tile_as<XE, true, 1, 2, 4, 1, 2>(p, s);
-  return launch_tile_as<XE, true, 2, 2, 3, 1, XE == 1 ? 3 : 2>(p, s);
+  // Between, stages of 256 K load whole lines of W (64 x 128 x 128 stages reach
+  // 14 TB/s from L2 into LDS and are bound by it).  E2M1: 64 x 64 tiles, from
+  // three quarters of a round of them on 128 x 128 (512 x 4096 x 4096, 128 of
+  // them: 11.0 us against 14.6; 1024 x 4096 x 4096, 256: 18.2 against 16.0).
+  // E4M3: 64 x 128 tiles, with K split in two up to half a round of 128 x 128
+  // (512 x 4096 x 4096: 13.4 against 15.4; 1024 x 4096 x 4096: 25.4 against
+  // 21.3), and 128 x 128 above a whole one (2048 x 4096 x 2048: 20.5 against
+  // 22.4).
+  if constexpr (XE == 1) {
+    if (t128 <= CUS * 3 / 4) return launch_tile_as<1, true, 1, 1, 256, 2, 1, 2>(p, s);
+    return launch_tile_as<1, true, 2, 2, 256, 2, 1, 2>(p, s);
+  } else {
+    if (t128 <= CUS / 2 && p.K >= 2048) return launch_tile_as<0, true, 1, 2, 256, 2, 2, 1>(p, s);
+    if (t128 <= CUS) return launch_tile_as<0, true, 1, 2, 256, 2, 1, 2>(p, s);
+    return launch_tile_as<0, true, 2, 2, 128, 3, 1, 2>(p, s);
+  }
 }
 
 }  // namespace
