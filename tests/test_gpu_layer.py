@@ -319,6 +319,41 @@ def test_router_strided_rows():
             near(d, want, want.abs() * (U8 if dtype == BF16 else U24) + size * weight_tol(l, E) * 3, "d_logits")
 
 
+@pytest.mark.parametrize("E,k", [(64, 8), (256, 12), (130, 16), (60, 24), (1000, 9)])
+def test_router_close_scores(E, k):
+    """Scores plus bias that differ by less than fp32 resolves, among fewer
+    and more experts than a token's lanes can hold; equal logits likewise."""
+    say(f"router close scores E={E} k={k}")
+    g = gen(E + k)
+    M = 24
+    for close in (k // 2 + 2, k + 3, 20, 30, 40, E):
+        close = min(close, E)
+        base = torch.randn(E, generator=g)
+        for sigmoid in (0, 1):
+            if sigmoid:
+                l = base + torch.randn(M, E, generator=g) * 2.0 ** -23
+                p = torch.sigmoid(base.double())
+            else:  # the same softmax up to the roundings of the shift
+                l = base + torch.linspace(-9, 9, M)[:, None]
+                p = torch.softmax(base.double(), 0)
+            bias = (0.75 - p).float()                    # every key about 0.75
+            bias[torch.randperm(E, generator=g)[close:]] -= 0.5
+            for b in (bias, None):
+                ids = torch.empty(M, k, dtype=torch.int32, device="cuda")
+                w = torch.empty(M, k, device="cuda")
+                moe.moe_router_topk(l.cuda(), ids, w, score=sigmoid, select_bias=None if b is None else b.cuda())
+                ids64, w64 = ref.router_topk(l, k, sigmoid, True, b)
+                assert torch.equal(ids.cpu(), ids64), (close, sigmoid, b is not None)
+                near(w, w64, w64 * weight_tol(l, E) + 1e-37, "weights")
+        # `close` equal largest logits
+        l = torch.randn(M, E, generator=g).clamp(max=3.0)
+        for m in range(M):
+            l[m, torch.randperm(E, generator=g)[:close]] = 4.0
+        for dtype in (F32, BF16):
+            moe.moe_router_topk(l.to(dtype).cuda(), ids, w)
+            assert torch.equal(ids.cpu(), ref.router_topk(l.to(dtype), k, 0, True)[0]), close
+
+
 @pytest.mark.parametrize("M,E,k", SIZES + [(0, 7, 2), (20000, 64, 6), (9001, 256, 8)])
 @pytest.mark.parametrize("sigmoid", [0, 1])
 def test_balance_and_gradient(M, E, k, sigmoid):
@@ -438,7 +473,7 @@ def near_in_norm(got, want, u, elem, what):
     (1, 1, 32), (1, 16, 128), (3, 17, 96), (8, 4096, 6144), (16, 100, 2048), (17, 33, 160), (5, 640, 8192),
     (32, 256, 512), (33, 1000, 1568), (64, 512, 4096), (65, 264, 256), (100, 130, 1024), (128, 128, 384),
     (200, 2056, 1568), (256, 256, 512), (300, 515, 1536), (512, 1024, 2048), (1025, 768, 1024), (1300, 2304, 4096),
-    (2111, 1111, 736),
+    (2111, 1111, 736), (130, 1040, 2080), (1000, 1032, 2176), (1100, 1252, 160), (2500, 2576, 544),
 ])
 @pytest.mark.parametrize("elem", [0, 1])
 def test_linear(M, N, K, elem):
@@ -474,6 +509,32 @@ def test_linear(M, N, K, elem):
     again = torch.empty_like(y)
     moe.moe_linear_mx(*args, again, x_elem=elem)
     assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("M,N,K", [(3300, 3848, 1056), (6390, 4096, 1088), (4096, 5888, 1024)])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_linear_many_tiles(M, N, K, elem):
+    """More tiles than compute units and nearly as many, ragged and whole."""
+    say(f"linear many tiles M={M} N={N} K={K} elem={elem}")
+    g = gen(M + N + K)
+    xq, xs = mx(M, K, elem, g)
+    wq, ws = mx(N, K, 1, g, 0.02)
+    xv, wv = ref.mx_values(xq, xs, elem).cuda(), ref.mx_values(wq, ws, 1).cuda()
+    bias, alpha = torch.randn(N, generator=g).cuda(), torch.tensor([1.25], device="cuda")
+    prod = xv @ wv.t().contiguous()
+    args = (xq.cuda(), xs.cuda(), wq.cuda(), ws.cuda())
+    for b, al in ((None, None), (bias, alpha)):
+        want = prod if b is None else prod * 1.25 + b.double()
+        tol = 1.25 * linear_tol(xv, wv, K, elem) + want.abs() * U8 + prod.abs() * 4 * U24
+        y, check = guarded((M, N), BF16)
+        moe.moe_linear_mx(*args, y, x_elem=elem, alpha=al, bias=b)
+        torch.cuda.synchronize()
+        check()
+        assert bool(((y.double() - want).abs() <= tol).all())
+        near_in_norm(y, want.cpu(), U8, elem, "y")
+        again = torch.empty_like(y)
+        moe.moe_linear_mx(*args, again, x_elem=elem, alpha=al, bias=b)
+        assert torch.equal(y, again)
 
 
 @pytest.mark.parametrize("M,N,K", [(8, 64, 512), (300, 512, 1024), (600, 700, 2080)])
