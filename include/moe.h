@@ -468,7 +468,7 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
 /* moe_rmsnorm: the layer's input for the experts.  For every row of M rows
  * of H values
  *   h = bf16(x + residual)           (h = x without a residual)
- *   r = 1 / sqrt(mean(h^2) + eps)    (fp32)
+ *   r = 1 / sqrt(mean(h^2) + eps)    (fp32; 0 where the sum of squares overflows)
  *   y = bf16(h * r * weight)
  *   q, q_sf = the MX quantisation of that bf16 y, bit for bit what
  *             moe_quantize_mx(y, M, H, elem) gives
@@ -481,8 +481,9 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
  *   q    elem 0: E4M3 [M, H], elem 1: packed E2M1 [M, H/2]; q_sf E8M0
  *        [M, H/32]; both or neither; at least one of y and q
  *   rstd fp32 [M]             r, for moe_rmsnorm_backward; NULL: not stored
- * residual_out may be the (contiguous) residual itself or x, and y may be x;
- * other overlaps are not allowed.  h is rounded before it is normalised, so
+ * residual_out may be the residual itself or x, or y may be x, where those
+ * rows are contiguous (strided: MOE_ERR_INVALID_ARGUMENT); other overlaps are
+ * not allowed.  h is rounded before it is normalised, so
  * that the backward pass, which reads the stored h, differentiates what ran.
  * 0 <= eps < inf.  H a multiple of 8 (of 32 with q), at most 16384; row
  * strides multiples of 8; bf16 arrays, weight and q 16-byte aligned (else
@@ -582,8 +583,8 @@ moe_status_t moe_balance_loss(const void* logits, moe_dtype_t logits_dtype, int6
  *            s_e (1 - s_e) dw_e                   of a weight
  *   renormalize: w_j (dw_j - sum dw w) (SIGMOID: times 1 - s) on the chosen
  * topk_ids, token_mask, score and renormalize as in the forward calls; places
- * with an id outside [0, E) have no weight, and the ids of a token must
- * otherwise differ.  Tokens masked out get zeros.  MOE_ERR_INVALID_ARGUMENT:
+ * with an id outside [0, E) have no weight, equal ids of a token are places
+ * of their own, whose gradients add up.  Tokens masked out get zeros.  MOE_ERR_INVALID_ARGUMENT:
  * neither gradient given, d_loss without prob_grad. */
 moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
                                  const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score,

@@ -351,41 +351,57 @@ def moe_quantize_mx(x, rows: int, cols: int, elem: int, q, sf, stream=None):
 
 # ---- around the routed experts: norm, router, balance loss, linear ----------
 
-def _refuse(where, name, t, shape, size, dev, strided):
+# element types an argument of each kind may come in (filled in when first used,
+# so that this module imports without torch): bf16 also as its 16 bits
+_KINDS = {}
+
+
+def _kinds():
+    import torch
+    _KINDS.update(
+        bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,), i32=(torch.int32, torch.uint32),
+        byte=tuple(getattr(torch, n) for n in ("uint8", "int8", "bool", "float8_e4m3fn", "float8_e8m0fnu",
+                                               "float4_e2m1fn_x2") if hasattr(torch, n)))
+    return _KINDS
+
+
+def _refuse(where, name, t, shape, kind, strided):
     if t is None:
         what = "is required"
-    elif t.shape != shape or t.element_size() != size:
-        what = f"must be {shape} of {size}-byte elements, is {tuple(t.shape)} of {t.element_size()}"
-    elif not (t.is_contiguous() or strided and t.stride(-1) == 1):
-        what = "must be contiguous" + (" in a row" if strided else "")
+    elif t.shape != shape or t.dtype not in _KINDS[kind]:
+        what = f"must be {kind} {shape}, is {t.dtype} {tuple(t.shape)}"
+    elif not (t.is_contiguous() or strided and t.stride(-1) == 1 and t.stride(0) >= shape[1]):
+        what = "must be contiguous" + (" in a row, and its rows apart" if strided else "")
     else:
         what = "must be on the GPU, with the call's other tensors"
     raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} {what}")
 
 
-def _arg(where: str, name: str, t, shape, size: int, dev: int):
+def _arg(where: str, name: str, t, shape, kind: str, dev: int):
     """The device address of tensor `t`, checked against the shape, the element
-    size and the device that the call takes it with."""
-    if t is None or t.shape != shape or t.element_size() != size or t.get_device() != dev or dev < 0 \
+    type and the device that the call takes it with."""
+    if t is None or t.shape != shape or t.dtype not in (_KINDS or _kinds())[kind] or t.get_device() != dev or dev < 0 \
             or not t.is_contiguous():
-        _refuse(where, name, t, shape, size, dev, False)
+        _refuse(where, name, t, shape, kind, False)
     return t.data_ptr()
 
 
-def _opt(where, name, t, shape, size, dev):
+def _opt(where, name, t, shape, kind, dev):
     """The same of a tensor that may be None."""
-    return None if t is None else _arg(where, name, t, shape, size, dev)
+    return None if t is None else _arg(where, name, t, shape, kind, dev)
 
 
-def _rows(where, name, t, shape, size, dev):
+def _rows(where, name, t, shape, kind, dev):
     """(address, row stride in elements; 0: contiguous) of a [rows, columns]
     tensor whose rows may be apart."""
-    if t is not None and t.shape == shape and t.element_size() == size and t.get_device() == dev and dev >= 0:
+    if t is not None and t.shape == shape and t.dtype in (_KINDS or _kinds())[kind] and t.get_device() == dev \
+            and dev >= 0:
         if t.is_contiguous():
             return t.data_ptr(), 0
-        if t.stride(1) == 1 or shape[1] == 1:
+        # (rows of an expanded tensor are not apart: their stride is 0)
+        if (t.stride(1) == 1 or shape[1] == 1) and t.stride(0) >= shape[1]:
             return t.data_ptr(), t.stride(0)
-    _refuse(where, name, t, shape, size, dev, True)
+    _refuse(where, name, t, shape, kind, True)
 
 
 def _dtype(where: str, name: str, t) -> int:
@@ -407,14 +423,18 @@ def _raw_stream(where, dev, stream):
 
 
 def _workspace(where, nbytes: int, given, t, stream):
-    """(tensor, bytes): the caller's workspace, or one from torch's allocator,
-    which is told of a stream other than the one it allocates for."""
+    """(tensor, bytes): the caller's workspace, or one from torch's allocator:
+    from the memory of the call's stream, whose blocks other work on that
+    stream alone has used and will use."""
     if given is None:
-        given = _alloc(nbytes, t.device)
-        if stream is not None:
-            given.record_stream(stream)
+        if stream is None:
+            given = _alloc(nbytes, t.device)
+        else:
+            import torch
+            with torch.cuda.stream(stream):
+                given = _alloc(nbytes, t.device)
     elif given.get_device() != t.get_device() or not given.is_contiguous():
-        _refuse(where, "workspace", given, given.shape, given.element_size(), t.get_device(), False)
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: workspace must be contiguous, with the call's other tensors")
     return given, given.numel() * given.element_size()
 
 
@@ -427,13 +447,13 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
     M, H = shape = x.shape
     dev = x.get_device()
     wd = _dtype(w, "weight", weight)
-    xp, xs = _rows(w, "x", x, shape, 2, dev)
-    rp, rs = (None, 0) if residual is None else _rows(w, "residual", residual, shape, 2, dev)
+    xp, xs = _rows(w, "x", x, shape, "bf16", dev)
+    rp, rs = (None, 0) if residual is None else _rows(w, "residual", residual, shape, "bf16", dev)
     _check(lib().moe_rmsnorm(
-        xp, xs, rp, rs, _arg(w, "weight", weight, (H,), 4 if wd else 2, dev), wd, eps, M, H,
-        _opt(w, "residual_out", residual_out, shape, 2, dev), _opt(w, "y", y, shape, 2, dev), elem,
-        _opt(w, "q", q, (M, H if elem == 0 else H // 2), 1, dev), _opt(w, "q_sf", q_sf, (M, H // 32), 1, dev),
-        _opt(w, "rstd", rstd, (M,), 4, dev), _raw_stream(w, dev, stream)), w)
+        xp, xs, rp, rs, _arg(w, "weight", weight, (H,), "f32" if wd else "bf16", dev), wd, eps, M, H,
+        _opt(w, "residual_out", residual_out, shape, "bf16", dev), _opt(w, "y", y, shape, "bf16", dev), elem,
+        _opt(w, "q", q, (M, H if elem == 0 else H // 2), "byte", dev), _opt(w, "q_sf", q_sf, (M, H // 32), "byte", dev),
+        _opt(w, "rstd", rstd, (M,), "f32", dev), _raw_stream(w, dev, stream)), w)
 
 
 def rmsnorm_backward_workspace_size(M: int, H: int) -> int:
@@ -447,10 +467,10 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     M, H = shape = dy.shape
     dev = dy.get_device()
     wd = _dtype(w, "weight", weight)
-    args = (_arg(w, "dy", dy, shape, 2, dev), _arg(w, "h", h, shape, 2, dev),
-            _arg(w, "weight", weight, (H,), 4 if wd else 2, dev), wd, _arg(w, "rstd", rstd, (M,), 4, dev),
-            _opt(w, "dh", dh, shape, 2, dev), M, H, _arg(w, "dx", dx, shape, 2, dev),
-            _opt(w, "dweight", dweight, (H,), 4, dev))
+    args = (_arg(w, "dy", dy, shape, "bf16", dev), _arg(w, "h", h, shape, "bf16", dev),
+            _arg(w, "weight", weight, (H,), "f32" if wd else "bf16", dev), wd, _arg(w, "rstd", rstd, (M,), "f32", dev),
+            _opt(w, "dh", dh, shape, "bf16", dev), M, H, _arg(w, "dx", dx, shape, "bf16", dev),
+            _opt(w, "dweight", dweight, (H,), "f32", dev))
     st = _raw_stream(w, dev, stream)
     wp, nbytes = None, 0
     if dweight is not None:
@@ -464,8 +484,8 @@ def balance_workspace_size(M: int, E: int) -> int:
 
 
 def _balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss):
-    return (_arg(w, "expert_counts", expert_counts, (E,), 4, dev), _arg(w, "mean_probs", mean_probs, (E,), 4, dev),
-            _arg(w, "prob_grad", prob_grad, (E,), 4, dev), _arg(w, "loss", loss, (1,), 4, dev))
+    return (_arg(w, "expert_counts", expert_counts, (E,), "i32", dev),
+            _arg(w, "mean_probs", mean_probs, (E,), "f32", dev), _arg(w, "prob_grad", prob_grad, (E,), "f32", dev), _arg(w, "loss", loss, (1,), "f32", dev))
 
 
 def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renormalize=True, select_bias=None,
@@ -480,10 +500,10 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
     k = topk_ids.shape[-1]
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
-    lp, ls = _rows(w, "logits", logits, (M, E), 4 if d else 2, dev)
-    args = (lp, d, ls, _opt(w, "select_bias", select_bias, (E,), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev),
-            score, 1 if renormalize else 0, M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev),
-            _arg(w, "topk_weights", topk_weights, (M, k), 4, dev), coef)
+    lp, ls = _rows(w, "logits", logits, (M, E), "f32" if d else "bf16", dev)
+    args = (lp, d, ls, _opt(w, "select_bias", select_bias, (E,), "f32", dev),
+            _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, 1 if renormalize else 0, M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
+            _arg(w, "topk_weights", topk_weights, (M, k), "f32", dev), coef)
     st = _raw_stream(w, dev, stream)
     if expert_counts is None and mean_probs is None and prob_grad is None and loss is None:
         _check(lib().moe_router_topk(*args, None, None, None, None, None, 0, st), w)
@@ -502,9 +522,9 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     k = topk_ids.shape[-1]
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
-    lp, ls = _rows(w, "logits", logits, (M, E), 4 if d else 2, dev)
-    args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev),
-            score, M, E, k, coef, *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
+    lp, ls = _rows(w, "logits", logits, (M, E), "f32" if d else "bf16", dev)
+    args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
+            _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, M, E, k, coef, *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
     st = _raw_stream(w, dev, stream)
     workspace, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
     _check(lib().moe_balance_loss(*args, workspace.data_ptr(), nbytes, st), w)
@@ -521,13 +541,13 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
     d = _dtype(w, "logits", logits)
     if _dtype(w, "d_logits", d_logits) != d:
         raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: d_logits must have the type of logits")
-    size = 4 if d else 2
-    lp, ls = _rows(w, "logits", logits, (M, E), size, dev)
+    kind = "f32" if d else "bf16"
+    lp, ls = _rows(w, "logits", logits, (M, E), kind, dev)
     _check(lib().moe_router_backward(
-        lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), 4, dev), _opt(w, "token_mask", token_mask, (M,), 1, dev), score,
-        1 if renormalize else 0, M, E, k, _opt(w, "d_topk_weights", d_topk_weights, (M, k), 4, dev),
-        _opt(w, "prob_grad", prob_grad, (E,), 4, dev), _opt(w, "d_loss", d_loss, (1,), 4, dev),
-        _arg(w, "d_logits", d_logits, (M, E), size, dev), _raw_stream(w, dev, stream)), w)
+        lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
+        _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, 1 if renormalize else 0, M, E, k, _opt(w, "d_topk_weights", d_topk_weights, (M, k), "f32", dev),
+        _opt(w, "prob_grad", prob_grad, (E,), "f32", dev), _opt(w, "d_loss", d_loss, (1,), "f32", dev),
+        _arg(w, "d_logits", d_logits, (M, E), kind, dev), _raw_stream(w, dev, stream)), w)
 
 
 def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumulate=False, stream=None):
@@ -539,7 +559,8 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_mx(
-        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), 1, dev), _arg(f, "x_sf", x_sf, (M, K // 32), 1, dev), x_elem,
-        _arg(f, "w", w, (N, K // 2), 1, dev), _arg(f, "w_sf", w_sf, (N, K // 32), 1, dev),
-        _opt(f, "alpha", alpha, (1,), 4, dev), _opt(f, "bias", bias, (N,), 4, dev), M, N, K,
-        1 if accumulate else 0, _arg(f, "y", y, (M, N), 4 if d else 2, dev), d, _raw_stream(f, dev, stream)), f)
+        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), "byte", dev),
+        _arg(f, "x_sf", x_sf, (M, K // 32), "byte", dev), x_elem, _arg(f, "w", w, (N, K // 2), "byte", dev), _arg(f, "w_sf", w_sf, (N, K // 32), "byte", dev),
+        _opt(f, "alpha", alpha, (1,), "f32", dev), _opt(f, "bias", bias, (N,), "f32", dev), M, N, K,
+        1 if accumulate else 0, _arg(f, "y", y, (M, N), "f32" if d else "bf16", dev), d,
+        _raw_stream(f, dev, stream)), f)

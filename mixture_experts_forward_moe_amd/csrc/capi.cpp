@@ -638,6 +638,11 @@ moe_status_t moe_rmsnorm(const uint16_t* x, int64_t x_row_stride, const uint16_t
   if (unaligned16(x) || unaligned16(residual) || unaligned16(weight) || unaligned16(residual_out) || unaligned16(y) ||
       unaligned16(q) || unaligned4(rstd))
     return MOE_ERR_UNSUPPORTED;
+  // in place over strided rows: a row's output would be another row's input
+  const bool x_apart = M > 1 && x_row_stride != 0 && x_row_stride != H;
+  const bool res_apart = M > 1 && residual_row_stride != 0 && residual_row_stride != H;
+  if ((x && x_apart && (y == x || residual_out == x)) || (residual_out && res_apart && residual_out == residual))
+    return MOE_ERR_INVALID_ARGUMENT;
   if (M == 0) return MOE_OK;
   NormParams p = {};
   p.x = x;
@@ -703,7 +708,9 @@ moe_status_t moe_router_topk(const void* logits, moe_dtype_t logits_dtype, int64
   if (M > 0 && (!topk_ids || !topk_weights)) return MOE_ERR_INVALID_ARGUMENT;
   const int given = !!expert_counts + !!mean_probs + !!prob_grad + !!loss;
   if ((given != 0 && given != 4) || (given && !std::isfinite(coef))) return MOE_ERR_INVALID_ARGUMENT;
-  if (unaligned4(select_bias) || unaligned4(topk_ids) || unaligned4(topk_weights)) return MOE_ERR_UNSUPPORTED;
+  if (unaligned4(select_bias) || unaligned4(topk_ids) || unaligned4(topk_weights) || unaligned4(expert_counts) ||
+      unaligned4(mean_probs) || unaligned4(prob_grad) || unaligned4(loss))
+    return MOE_ERR_UNSUPPORTED;
   RouterParams p = {};
   p.logits = logits;
   p.logits_f32 = logits_dtype == MOE_DTYPE_F32;
@@ -735,7 +742,9 @@ moe_status_t moe_balance_loss(const void* logits, moe_dtype_t logits_dtype, int6
   if (s != MOE_OK) return s;
   if ((M > 0 && !topk_ids) || !expert_counts || !mean_probs || !prob_grad || !loss || !std::isfinite(coef))
     return MOE_ERR_INVALID_ARGUMENT;
-  if (unaligned4(topk_ids)) return MOE_ERR_UNSUPPORTED;
+  if (unaligned4(topk_ids) || unaligned4(expert_counts) || unaligned4(mean_probs) || unaligned4(prob_grad) ||
+      unaligned4(loss))
+    return MOE_ERR_UNSUPPORTED;
   RouterParams p = {};
   p.logits = logits;
   p.logits_f32 = logits_dtype == MOE_DTYPE_F32;

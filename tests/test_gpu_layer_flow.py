@@ -191,6 +191,25 @@ def test_stream_argument():
     assert same(L.results(), want)
 
 
+def test_own_workspace_is_of_the_calls_stream(monkeypatch):
+    """A workspace that a call allocates comes from the memory of the stream it
+    runs on: a block of another stream's may still be in use there."""
+    say("own workspace")
+    L = Layer(64, seed=5)
+    L.forward()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    seen = []
+    alloc = moe._alloc
+    monkeypatch.setattr(moe, "_alloc", lambda *a: seen.append(torch.cuda.current_stream()) or alloc(*a))
+    moe.moe_balance_loss(L.logits, L.ids, 0.1, L.counts, L.mean, L.grad, L.loss, stream=s)
+    moe.moe_rmsnorm_backward(L.dy, L.h, L.weight, L.rstd, L.dx, L.dweight, stream=s)
+    moe.moe_rmsnorm_backward(L.dy, L.h, L.weight, L.rstd, L.dx, L.dweight)
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert seen == [s, s, torch.cuda.current_stream()]
+
+
 def test_padded_tokens_do_not_reach_the_experts():
     """Masked tokens get no route: the forward leaves their rows zero."""
     say("padded tokens")

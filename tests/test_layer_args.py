@@ -35,6 +35,9 @@ NORM = dict(x=F, xs=0, residual=F, rs=0, weight=F, wd=0, eps=1e-6, M=4, H=64, h=
     (dict(rs=68), UNSUPPORTED), (dict(x=ODD), UNSUPPORTED), (dict(residual=ODD), UNSUPPORTED),
     (dict(weight=ODD), UNSUPPORTED), (dict(h=ODD), UNSUPPORTED), (dict(y=ODD), UNSUPPORTED),
     (dict(q=ODD), UNSUPPORTED), (dict(rstd=ODD), UNSUPPORTED), (dict(M=0), OK), (dict(M=0, x=None), OK),
+    # written rows over strided ones that other workgroups still read
+    (dict(h=F, xs=128, x=F, residual=2 * F, y=None), INVALID), (dict(y=F, x=F, xs=128, h=None), INVALID),
+    (dict(h=F, residual=F, rs=128, x=2 * F, y=None), INVALID),
 ])
 def test_norm(change, status):
     assert call("moe_rmsnorm", NORM, **change) == status
@@ -75,7 +78,8 @@ ALL = dict(counts=F, probs=F, grad=F, loss=F, ws=F, n=1 << 20)
     (dict(M=1 << 30), UNSUPPORTED), (dict(logits=ODD), UNSUPPORTED), (dict(logits=F + 2), UNSUPPORTED),
     (dict(d=0, logits=ODD), UNSUPPORTED), (dict(ids=F + 2), UNSUPPORTED), (dict(w=F + 2), UNSUPPORTED),
     (dict(bias=F + 2), UNSUPPORTED), (dict(ALL, ws=None), WORKSPACE), (dict(ALL, ws=F + 64), WORKSPACE),
-    (dict(ALL, n=256), WORKSPACE), (dict(M=0), OK), (dict(M=0, logits=None, ids=None, w=None), OK),
+    (dict(ALL, counts=F + 2), UNSUPPORTED), (dict(ALL, probs=F + 2), UNSUPPORTED), (dict(ALL, grad=ODD), UNSUPPORTED),
+    (dict(ALL, loss=ODD), UNSUPPORTED), (dict(ALL, n=256), WORKSPACE), (dict(M=0), OK), (dict(M=0, logits=None, ids=None, w=None), OK),
 ])
 def test_router_topk(change, status):
     assert call("moe_router_topk", TOPK, **change) == status
@@ -89,6 +93,7 @@ LOSS = dict(logits=F, d=1, stride=0, ids=F, mask=None, score=0, M=4, E=16, k=2, 
     (dict(logits=None), INVALID), (dict(ids=None), INVALID), (dict(counts=None), INVALID), (dict(probs=None), INVALID),
     (dict(grad=None), INVALID), (dict(loss=None), INVALID), (dict(coef=float("inf")), INVALID), (dict(k=17), INVALID),
     (dict(E=1025), UNSUPPORTED), (dict(ids=ODD), UNSUPPORTED), (dict(ws=None), WORKSPACE), (dict(n=511), WORKSPACE),
+    (dict(counts=F + 2), UNSUPPORTED), (dict(loss=ODD), UNSUPPORTED),
 ])
 def test_balance_loss(change, status):
     assert call("moe_balance_loss", LOSS, **change) == status
@@ -148,6 +153,39 @@ def test_binding_refuses_what_does_not_fit():
         moe.moe_router_topk(torch.zeros(4, 16), ids, torch.zeros(4, 3))
     with pytest.raises(moe.MoeError, match="type of logits"):
         moe.moe_router_backward(torch.zeros(4, 16), ids, x, prob_grad=w)
+
+
+def test_binding_refuses_other_element_types():
+    """Types of the right size but another meaning."""
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    w = torch.zeros(64)
+    f = torch.zeros(4, 16)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for call_, what in [
+        (lambda: moe.moe_rmsnorm(x.half(), w, y=x), "x must be bf16"),
+        (lambda: moe.moe_rmsnorm(x, w, y=x.half()), "weight|y must be bf16|on the GPU"),
+        (lambda: moe.moe_rmsnorm_backward(x.half(), x, w, w[:4], x), "dy must be bf16"),
+        (lambda: moe.moe_linear_mx(x.to(torch.float8_e5m2), w, w, w, x), "x must be byte|w"),
+    ]:
+        with pytest.raises(moe.MoeError, match=what):
+            call_()
+    with pytest.raises(moe.MoeError):
+        moe.moe_router_topk(f.half(), ids, f[:, :2])
+    # (past the device check the rest is the same function: by itself)
+    for t, kind in [(ids, "f32"), (f, "i32"), (x.half(), "bf16"), (f.to(torch.float8_e5m2), "byte"),
+                    (f.to(torch.float8_e4m3fnuz), "byte"), (ids.to(torch.int64), "i32")]:
+        with pytest.raises(moe.MoeError, match=f"must be {kind}"):
+            moe._arg("call", "t", t, tuple(t.shape), kind, 0)
+
+
+def test_binding_refuses_rows_that_are_not_apart():
+    """An expanded row has stride 0, which the library takes for contiguous."""
+    row = torch.zeros(1, 64, dtype=torch.bfloat16)
+    with pytest.raises(moe.MoeError, match="rows apart"):
+        moe._rows("call", "x", row.expand(4, 64), (4, 64), "bf16", -1)
+    over = torch.zeros(4 * 32 + 32).as_strided((4, 64), (32, 1))
+    with pytest.raises(moe.MoeError, match="rows apart"):
+        moe._rows("call", "x", over, (4, 64), "f32", -1)
 
 
 def test_constants_match_header():
