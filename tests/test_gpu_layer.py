@@ -354,6 +354,30 @@ def test_router_close_scores(E, k):
             assert torch.equal(ids.cpu(), ref.router_topk(l.to(dtype), k, 0, True)[0]), close
 
 
+def test_router_of_many_tokens():
+    """Elements past 2^31: the last tokens choose as they do alone, and their
+    gradients are the same."""
+    say("router of many tokens")
+    M, E, k, tail = 8_400_000, 256, 8, 3000
+    l = torch.randn(M, E, device="cuda", dtype=BF16)
+    ids, w = torch.empty(M, k, dtype=torch.int32, device="cuda"), torch.empty(M, k, device="cuda")
+    counts, mean = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda")
+    grad, loss = torch.empty(E, device="cuda"), torch.empty(1, device="cuda")
+    moe.moe_router_topk(l, ids, w, coef=1.0, expert_counts=counts, mean_probs=mean, prob_grad=grad, loss=loss)
+    assert int(counts.sum()) == M * k
+    assert torch.equal(counts.long(), torch.bincount(ids.flatten(), minlength=E))
+    # (a workgroup's lanes add M / 8192 probabilities, so a step of those each)
+    assert abs(float(mean.double().sum()) - 1) < (M / 8192 + 64) * U24
+    d = torch.empty_like(l)
+    moe.moe_router_backward(l, ids, d, d_topk_weights=w, prob_grad=grad)
+    end = l[-tail:].clone()
+    ids1, w1, d1 = torch.empty_like(ids[:tail]), torch.empty_like(w[:tail]), torch.empty_like(end)
+    moe.moe_router_topk(end, ids1, w1)
+    assert torch.equal(ids1, ids[-tail:]) and torch.equal(w1, w[-tail:])
+    moe.moe_router_backward(end, ids1, d1, d_topk_weights=w1, prob_grad=grad)
+    assert torch.equal(d1, d[-tail:])
+
+
 @pytest.mark.parametrize("M,E,k", SIZES + [(0, 7, 2), (20000, 64, 6), (9001, 256, 8)])
 @pytest.mark.parametrize("sigmoid", [0, 1])
 def test_balance_and_gradient(M, E, k, sigmoid):
@@ -535,6 +559,28 @@ def test_linear_many_tiles(M, N, K, elem):
         again = torch.empty_like(y)
         moe.moe_linear_mx(*args, again, x_elem=elem, alpha=al, bias=b)
         assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("M,N,K,elem", [(1_060_000, 256, 2080, 0), (8, 2_100_000, 4128, 1), (70_000, 32_776, 64, 1),
+                                         (66_000, 33_001, 32, 0)])
+def test_linear_past_32_bits(M, N, K, elem):
+    """x, w or y of more than 2^31 bytes or elements: the last rows and columns."""
+    say(f"linear past 32 bits M={M} N={N} K={K} elem={elem}")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    byte = lambda n, k, lo, hi: torch.randint(lo, hi, (n, k), generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    xq = byte(M, K, 0, 120) if elem == 0 else byte(M, K // 2, 0, 256)
+    wq = byte(N, K // 2, 0, 256)
+    xs, ws = byte(M, K // 32, 120, 130), byte(N, K // 32, 120, 130)
+    y, check = guarded((M, N), BF16)
+    moe.moe_linear_mx(xq, xs, wq, ws, y, x_elem=elem)
+    torch.cuda.synchronize()
+    check()
+    for m, n in [(slice(-200, None), slice(-300, None)), (slice(0, 200), slice(-300, None)),
+                 (slice(-200, None), slice(0, 300))]:
+        xv = ref.mx_values(xq[m].cpu(), xs[m].cpu(), elem)
+        wv = ref.mx_values(wq[n].cpu(), ws[n].cpu(), 1)
+        want = xv @ wv.t()
+        near(y[m, n], want, want.abs() * U8 + linear_tol(xv, wv, K, elem), "y")
 
 
 @pytest.mark.parametrize("M,N,K", [(8, 64, 512), (300, 512, 1024), (600, 700, 2080)])
