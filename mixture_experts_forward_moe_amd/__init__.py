@@ -8,6 +8,7 @@ built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -354,10 +355,13 @@ def moe_quantize_mx(x, rows: int, cols: int, elem: int, q, sf, stream=None):
 # element types an argument of each kind may come in (filled in when first used,
 # so that this module imports without torch): bf16 also as its 16 bits
 _KINDS = {}
+_cuda = None  # torch._C
 
 
 def _kinds():
+    global _cuda
     import torch
+    _cuda = torch._C
     _KINDS.update(
         bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,), i32=(torch.int32, torch.uint32),
         byte=tuple(getattr(torch, n) for n in ("uint8", "int8", "bool", "float8_e4m3fn", "float8_e8m0fnu",
@@ -415,27 +419,28 @@ def _dtype(where: str, name: str, t) -> int:
 
 
 def _raw_stream(where, dev, stream):
-    """The stream of a call on device `dev`, which must be the current one."""
-    import torch
-    if torch.cuda.current_device() != dev:
+    """The stream of a call on device `dev`, which must be the current one.
+    (After the arguments' checks: they are on a GPU, so torch has set it up.)"""
+    if _cuda._cuda_getDevice() != dev:
         raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: the tensors are on cuda:{dev}, which is not the current device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _cuda._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _workspace(where, nbytes: int, given, t, stream):
-    """(tensor, bytes): the caller's workspace, or one from torch's allocator:
-    from the memory of the call's stream, whose blocks other work on that
-    stream alone has used and will use."""
-    if given is None:
-        if stream is None:
+    """(tensor, address, bytes): the caller's workspace, or one from torch's
+    allocator: from the memory of the call's stream, whose blocks other work on
+    that stream alone has used and will use."""
+    if given is not None:
+        if given.get_device() != t.get_device() or not given.is_contiguous():
+            raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: workspace must be contiguous, with the call's other tensors")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if stream is None:
+        given = _alloc(nbytes, t.device)
+    else:
+        import torch
+        with torch.cuda.stream(stream):
             given = _alloc(nbytes, t.device)
-        else:
-            import torch
-            with torch.cuda.stream(stream):
-                given = _alloc(nbytes, t.device)
-    elif given.get_device() != t.get_device() or not given.is_contiguous():
-        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: workspace must be contiguous, with the call's other tensors")
-    return given, given.numel() * given.element_size()
+    return given, given.data_ptr(), nbytes
 
 
 def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_sf=None, elem=0, rstd=None, eps=1e-6,
@@ -456,6 +461,7 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
         _opt(w, "rstd", rstd, (M,), "f32", dev), _raw_stream(w, dev, stream)), w)
 
 
+@functools.lru_cache
 def rmsnorm_backward_workspace_size(M: int, H: int) -> int:
     return lib().moe_rmsnorm_backward_workspace_size(M, H)
 
@@ -474,11 +480,11 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     st = _raw_stream(w, dev, stream)
     wp, nbytes = None, 0
     if dweight is not None:
-        workspace, nbytes = _workspace(w, rmsnorm_backward_workspace_size(M, H), workspace, dy, stream)
-        wp = workspace.data_ptr()
+        workspace, wp, nbytes = _workspace(w, rmsnorm_backward_workspace_size(M, H), workspace, dy, stream)
     _check(lib().moe_rmsnorm_backward(*args, wp, nbytes, st), w)
 
 
+@functools.lru_cache
 def balance_workspace_size(M: int, E: int) -> int:
     return lib().moe_balance_workspace_size(M, E)
 
@@ -509,8 +515,8 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
         _check(lib().moe_router_topk(*args, None, None, None, None, None, 0, st), w)
         return
     balance = _balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss)
-    workspace, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
-    _check(lib().moe_router_topk(*args, *balance, workspace.data_ptr(), nbytes, st), w)
+    workspace, wp, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_router_topk(*args, *balance, wp, nbytes, st), w)
 
 
 def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_grad, loss, score=SCORE_SOFTMAX,
@@ -526,8 +532,8 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
             _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, M, E, k, coef, *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
     st = _raw_stream(w, dev, stream)
-    workspace, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
-    _check(lib().moe_balance_loss(*args, workspace.data_ptr(), nbytes, st), w)
+    workspace, wp, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
+    _check(lib().moe_balance_loss(*args, wp, nbytes, st), w)
 
 
 def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_grad=None, d_loss=None,
