@@ -100,7 +100,8 @@ DEV int expert_of(int i, int j) {
 }
 
 // e^x for x <= 0 to about one step: the product with log2(e) is carried in two
-// parts into the hardware's exp2; below the normal range 0
+// parts into the hardware's exp2; below the normal range, and for the NaN of
+// -inf - -inf, 0
 DEV float exp_neg(float x) {
   x = fmaxf(x, -200.0f);
   const float t = x * 1.44269502f;
@@ -146,7 +147,15 @@ DEV void load_row_as(const void* logits, int64_t at, int E, int j, bool vec, flo
     }
   }
 #pragma unroll
-  for (int i = 0; i < V; i++) l[i] = expert_of<V>(i, j) < E ? clean(l[i]) : -INFINITY;
+  for (int c = 0; c < G; c++) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) l[4 * c + i] = clean(l[4 * c + i]);
+    if (64 * (c + 1) > E) {
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        if (expert_of<V>(4 * c + i, j) >= E) l[4 * c + i] = -INFINITY;
+    }
+  }
 }
 template <int V>
 DEV void load_row(const void* logits, int f32, int64_t at, int E, int j, bool vec, float (&l)[V]) {
@@ -164,13 +173,14 @@ DEV float sigmoid_f32(float l) {
 // Both are taken relative to the largest logit, so that a row of very
 // negative logits does not become 0 / 0: s = exp(min(l, 0)) / (1 + exp(-|l|)),
 // and the factor exp(-min(max, 0)) cancels in the quotient (it is 1 unless
-// every logit of the row is negative).
+// every logit of the row is negative).  Returns the reciprocal of the sum, the
+// softmax's largest probability.
 template <int V>
-DEV void probabilities(const float (&l)[V], float top, int sigmoid, float (&p)[V]) {
+DEV float probabilities(const float (&l)[V], float top, int sigmoid, float (&p)[V]) {
   float sum = 0.0f;
   if (!sigmoid) {
 #pragma unroll
-    for (int i = 0; i < V; i++) p[i] = l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
+    for (int i = 0; i < V; i++) p[i] = exp_neg(l[i] - top);
   } else if (__all(top >= 0.0f)) {
 #pragma unroll
     for (int i = 0; i < V; i++) p[i] = sigmoid_f32(l[i]);
@@ -188,6 +198,7 @@ DEV void probabilities(const float (&l)[V], float top, int sigmoid, float (&p)[V
   const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
 #pragma unroll
   for (int i = 0; i < V; i++) p[i] *= inv;
+  return inv;
 }
 
 // Score of a chosen logit before the division by the sum over the chosen
@@ -413,9 +424,9 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
     for (int i = 0; i < V; i++) top = fmaxf(top, l[i]);
     top = row_max(top);
 
-    float p[STATS ? V : 1];
+    float p[STATS ? V : 1], most = 0.0f;  // (the softmax's largest probability)
     if constexpr (STATS) {
-      probabilities<V>(l, top, a.sigmoid, p);
+      most = probabilities<V>(l, top, a.sigmoid, p);
       if (on) {
 #pragma unroll
         for (int i = 0; i < V; i++) psum[i] += p[i];
@@ -429,14 +440,18 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
       float sum = 0.0f;  // of the scores' numerators: over all experts, or over the chosen ones
       if (!a.renormalize && !a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
+        for (int i = 0; i < V; i++) sum += exp_neg(l[i] - top);
       }
       int used = (a.top_k + 15) / 16;
       bool read_logits = true;
       uint2* own_cand = cand[threadIdx.x >> 4];
       if constexpr (BIAS) {
-        // a sigmoid is off by a few steps of 1, a softmax by its sum's V + 4
-        // roundings and those too; the addition rounds relative to the key
+        // Off by, in steps of 2^-24: a sigmoid, 8 of the row's largest (exp2 and
+        // rcp one of 2^-23 each, 1 + z and the product a half).  A softmax
+        // V + 24 of its largest: V + 4 additions, 4 for exp, quotient and
+        // product, and what the rounding of d = l - top does to the exp, |d| each,
+        // of which a probability's |d| e^d is less than one and the sum's mean
+        // at most ln E < 7.  The addition rounds relative to the key.
         float big = 0.0f;
         if (!a.sigmoid) {
           if constexpr (STATS) {
@@ -446,7 +461,7 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
             for (int i = 0; i < V; i++) l[i] = p[i];
           } else {
             float q[V];
-            probabilities<V>(l, top, 0, q);
+            most = probabilities<V>(l, top, 0, q);
 #pragma unroll
             for (int i = 0; i < V; i++) l[i] = l[i] == -INFINITY ? -INFINITY : q[i];
           }
@@ -458,7 +473,7 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
           l[i] = l[i] != -INFINITY && v == v ? v : -INFINITY;
           big = fmaxf(big, l[i] == -INFINITY ? 0.0f : fabsf(l[i]));
         }
-        const float err = (a.sigmoid ? 0x1p-20f : (V + 16) * 0x1p-24f) + 0x1p-22f * row_max(big);
+        const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f + 0x1p-23f * row_max(big);
         const int n = __all(err < INFINITY) ? choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c) : 0;
         if (n) used = n;
         else choose_rounds<true>(a, at_row, top, j, c);
@@ -740,15 +755,19 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
       f32x4_t* mine = reinterpret_cast<f32x4_t*>(row_of + 4 * j);  // (all lanes clear the row)
 #pragma unroll
       for (int i = 0; i < V / 4; i++) mine[16 * i] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+      // places j, j + 16, .. of which the first `slots` can be taken
+      const int slots = (a.top_k + 15) / 16;
       int id[SLOTS];
-      float w[SLOTS], dw[SLOTS], keep[SLOTS], ctop = -INFINITY, sum = 0.0f, dot = 0.0f;
+      float w[SLOTS], dw[SLOTS], ctop = -INFINITY, sum = 0.0f, dot = 0.0f;
 #pragma unroll
       for (int q = 0; q < SLOTS; q++) {
-        const int s = j + 16 * q;
-        id[q] = on && s < a.top_k ? a.ids[t * a.top_k + s] : -1;
-        if (id[q] >= a.E) id[q] = -1;
+        id[q] = -1;
         w[q] = -INFINITY;
         dw[q] = 0.0f;
+        if (q >= slots) continue;
+        const int s = j + 16 * q;
+        if (on && s < a.top_k) id[q] = a.ids[t * a.top_k + s];
+        if (id[q] >= a.E) id[q] = -1;
         if (id[q] >= 0) {
           const int64_t at = row * a.row_stride + id[q];
           w[q] = clean(a.logits_f32 ? reinterpret_cast<const float*>(a.logits)[at]
@@ -756,16 +775,19 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
           dw[q] = a.d_weights[t * a.top_k + s];
         }
         ctop = fmaxf(ctop, w[q]);
-        keep[q] = a.sigmoid ? sigmoid_f32(-w[q]) : 1.0f;  // 1 - s
       }
       ctop = row_max(ctop);
       if (!a.renormalize && !a.sigmoid) {
 #pragma unroll
-        for (int i = 0; i < V; i++) sum += l[i] == -INFINITY ? 0.0f : exp_neg(l[i] - top);
+        for (int i = 0; i < V; i++) sum += exp_neg(l[i] - top);
         ctop = top;
       }
+      float keep[SLOTS];
 #pragma unroll
       for (int q = 0; q < SLOTS; q++) {
+        keep[q] = 1.0f;
+        if (q >= slots) continue;
+        if (a.sigmoid) keep[q] = sigmoid_f32(-w[q]);  // 1 - s
         if (a.sigmoid && !a.renormalize) w[q] = w[q] == -INFINITY ? 0.0f : sigmoid_f32(w[q]);
         else w[q] = chosen_score(w[q], ctop, a.sigmoid);
         if (a.renormalize) sum += w[q];
@@ -773,10 +795,12 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
       if (a.renormalize || !a.sigmoid) {
         sum = row_add(sum);
 #pragma unroll
-        for (int q = 0; q < SLOTS; q++) w[q] = sum > 0.0f ? w[q] / sum : 0.0f;
+        for (int q = 0; q < SLOTS; q++)
+          if (q < slots) w[q] = sum > 0.0f ? w[q] / sum : 0.0f;
       }
 #pragma unroll
-      for (int q = 0; q < SLOTS; q++) dot += dw[q] * w[q];
+      for (int q = 0; q < SLOTS; q++)
+        if (q < slots) dot += dw[q] * w[q];
       dot = row_add(dot);
       if (!a.renormalize) {
         if (!a.sigmoid) all = dot;
@@ -806,17 +830,20 @@ __global__ __launch_bounds__(RT) void router_backward_kernel(const RouterBackwar
 #pragma unroll
       for (int i = 0; i < V; i++) dot = fmaf(u[i], p[i], dot);  // (p is 0 past the last expert)
       dot = row_add(dot);
+      if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < V; i++) {
-        float g = p[i] * (u[i] - dot);
-        if (a.sigmoid) g = g * sigmoid_f32(-l[i]);
-        else g -= p[i] * all;
-        d[i] += g;
+        for (int i = 0; i < V; i++) d[i] += p[i] * (u[i] - dot) * sigmoid_f32(-l[i]);
+      } else {
+        dot += all;
+#pragma unroll
+        for (int i = 0; i < V; i++) d[i] = fmaf(p[i], u[i] - dot, d[i]);
       }
     }
-    if (in) {
+    if (a.token_mask) {
 #pragma unroll
       for (int i = 0; i < V; i++) d[i] = on ? d[i] : 0.0f;
+    }
+    if (in) {
       store_row<V>(a.d_logits, a.logits_f32, t * a.E, a.E, j, vec_out, d);
     }
   }
@@ -838,6 +865,16 @@ hipError_t launch_v(const RouterParams& p, hipStream_t s) {
   const bool stats = p.prob_partial != nullptr;
   const unsigned grid = stats ? (unsigned)router_partials(p.M) : token_blocks(p.M);
   const int threads = threads_of(stats);
+  if constexpr (V == 64) {
+    if (p.select && stats) {
+      RouterParams q = p;
+      q.prob_partial = nullptr;
+      const hipError_t e = launch_v<V>(q, s);
+      if (e != hipSuccess) return e;
+      router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
+      return hipGetLastError();
+    }
+  }
   if (!p.select) router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
   else if (p.select_bias && stats) router_kernel<V, true, true, true><<<grid, threads, 0, s>>>(p, vec);
   else if (p.select_bias) router_kernel<V, true, true, false><<<grid, threads, 0, s>>>(p, vec);

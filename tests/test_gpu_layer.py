@@ -301,6 +301,28 @@ def test_router_ties_and_extremes():
     assert torch.equal(ids.cpu(), ref.router_topk(l, k, 1, True, bias)[0])
 
 
+def test_router_nan_bits():
+    """Every kind of NaN takes its expert out, quiet or signalling, either sign."""
+    say("router NaN bits")
+    for dtype, bits in ((F32, [0x7F800001, 0x7FC00000, 0x7FFFFFFF, -0x7FFFFF, -0x400000, -1]),
+                        (BF16, [0x7F81, 0x7FC0, 0x7FFF, -0x7F, -0x40, -1])):
+        l = torch.linspace(-1, 1, 70).repeat(len(bits), 1).to(dtype)
+        b = l.view(torch.int32 if dtype == F32 else torch.int16)
+        for i, v in enumerate(bits):
+            b[i, 60 + i] = v
+            b[i, 3] = v
+        assert bool(torch.isnan(l).sum(-1).eq(2).all())
+        for E in (70, 64, 66):
+            ids, w = torch.empty(len(bits), 6, dtype=torch.int32, device="cuda"), torch.empty(len(bits), 6, device="cuda")
+            moe.moe_router_topk(l[:, :E].cuda(), ids, w)
+            ids64, w64 = ref.router_topk(l[:, :E], 6, 0, True)
+            assert torch.equal(ids.cpu(), ids64)
+            near(w, w64, w64 * weight_tol(l[:, :E], E), "weights")
+            d = torch.empty(len(bits), E, dtype=dtype, device="cuda")
+            moe.moe_router_backward(l[:, :E].cuda(), ids, d, prob_grad=torch.ones(E, device="cuda"))
+            assert bool(torch.isfinite(d).all())
+
+
 def test_router_strided_rows():
     say("router strided rows")
     g = gen(9)
