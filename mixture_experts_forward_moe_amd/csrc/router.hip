@@ -38,7 +38,7 @@ namespace {
 // threads each would leave two wavefronts a SIMD.
 constexpr int threads_of(bool stats) { return stats ? 512 : 256; }
 constexpr int RT = 256, TOKENS = RT / 16;  // of the backward pass
-constexpr int STAT_TOKENS = threads_of(true) / 16;
+constexpr int STAT_TOKENS = threads_of(true) / 16, STAT_BLOCKS = 512;  // of the statistics
 
 template <int CTRL>
 DEV int dpp(int v) {
@@ -599,10 +599,11 @@ __global__ __launch_bounds__(FT) void balance_finish_kernel(const BalanceParams 
   __syncthreads();
   double s = 0.0;
   int n = 0, t = 0;
-  if (e < a.E) {
-    add_partials<FT / FE>(a, r, e, s, n);
-  }
-  for (int p = threadIdx.x; p < a.partials; p += FT) t += a.token_partial[p];
+  static_assert(STAT_BLOCKS <= 2 * FT, "two token counts a thread");
+  const int q = threadIdx.x;
+  const int t0 = a.token_partial[min(q, a.partials - 1)], t1 = a.token_partial[min(q + FT, a.partials - 1)];
+  if (e < a.E) add_partials<FT / FE>(a, r, e, s, n);
+  t = (q < a.partials ? t0 : 0) + (q + FT < a.partials ? t1 : 0);
   psum[r][c] = s;
   count[r][c] = n;
   if (t) atomicAdd(&total, t);
@@ -661,11 +662,11 @@ __global__ __launch_bounds__(OT) void balance_small_kernel(const BalanceParams a
   if (threadIdx.x == 0) total = 0;
   __syncthreads();
   double s = 0.0;
-  int n = 0, t = 0;
-  if (c < a.E) {
-    add_partials<R>(a, r, c, s, n);
-  }
-  for (int p = threadIdx.x; p < a.partials; p += OT) t += a.token_partial[p];
+  int n = 0;
+  static_assert(STAT_BLOCKS <= OT, "a token count a thread");
+  int t = a.token_partial[min((int)threadIdx.x, a.partials - 1)];
+  if (c < a.E) add_partials<R>(a, r, c, s, n);
+  t = (int)threadIdx.x < a.partials ? t : 0;
   psum[r][c] = s;
   count[r][c] = n;
   if (t) atomicAdd(&total, t);
@@ -895,7 +896,7 @@ hipError_t launch_back(const RouterBackwardParams& p, hipStream_t s) {
 
 int router_partials(int64_t M) {
   const int64_t b = (M + STAT_TOKENS - 1) / STAT_TOKENS;
-  return (int)(b < 1 ? 1 : b > 512 ? 512 : b);
+  return (int)(b < 1 ? 1 : b > STAT_BLOCKS ? STAT_BLOCKS : b);
 }
 
 int balance_finish_blocks(int E) { return (E + FE - 1) / FE; }
