@@ -22,6 +22,13 @@
 // keys pass (many equal ones).  score + bias is compared in fp32 first, and in
 // fp64 for a token any two of whose candidates are closer than the error of
 // that.
+//
+// Bound: up to some thousand tokens by latency (8 tokens of 256 experts: 4.9 us,
+// a kernel of that length has a launch, one trip to memory and the chain of
+// the choice); from there on by instructions, about 700 a wavefront of four
+// tokens.  65536 x 256 fp32: choice 23 us (71 MB, 3.1 TB/s), gradient 40 us
+// (138 MB, 3.5 TB/s).  16384 x 256: choice 8.5 us, with the loss 20 us, of which
+// the join is 7; gradient 14 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
