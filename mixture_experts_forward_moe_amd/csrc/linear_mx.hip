@@ -613,7 +613,8 @@ hipError_t launch_tile(const LinearParams& p, hipStream_t s) {
 // for memory.  A stage of 256 K is 2048 cycles of matrix cores for E2M1, and
 // 196 KiB of fragment reads and 64 KiB of loads in LDS, another 2048 cycles if
 // nothing overlapped.  16384 x 6144 x 4096: E2M1 203 - 222 us (3.7 - 4.1
-// PFLOP/s, the matrix cores 47% busy at 2.0 GHz), E4M3 321 us (2.6).  At 8192 x
+// PFLOP/s, the matrix cores 47% busy at 2.0 GHz), E4M3 320 - 360 us (2.3 - 2.6,
+// by the card).  Wave priorities and other orders of the reads: the same.  At 8192 x
 // 8192 x 8192 E2M1, 264 us: without the loads 221, without the fragment reads
 // 223, the instructions alone 176.
 template <int XE>

@@ -178,6 +178,16 @@ def test_binding_refuses_other_element_types():
             moe._arg("call", "t", t, tuple(t.shape), kind, 0)
 
 
+def test_binding_refuses_another_device_than_the_current_one(monkeypatch):
+    class OnOne:
+        _cuda_getDevice = staticmethod(lambda: 1)
+        _cuda_getCurrentRawStream = staticmethod(lambda dev: 7)
+    monkeypatch.setattr(moe, "_cuda", OnOne)
+    assert moe._raw_stream("call", 1, None) == 7
+    with pytest.raises(moe.MoeError, match="not the current device"):
+        moe._raw_stream("call", 0, None)
+
+
 def test_binding_refuses_rows_that_are_not_apart():
     """An expanded row has stride 0, which the library takes for contiguous."""
     row = torch.zeros(1, 64, dtype=torch.bfloat16)
