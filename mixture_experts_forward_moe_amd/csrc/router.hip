@@ -14,7 +14,7 @@
 // registers and four DPP steps, and a wavefront serves four tokens with each
 // instruction.
 //
-// The choice: the k-th largest of the half lanes' maxima bounds the k-th key
+// The choice: the k-th largest of the (half) lanes' maxima bounds the k-th key
 // from below, and only keys above the bound (about nine of 256 for k = 8) go
 // on, one to a lane, where each lane counts the ones before its own.  The
 // k rounds of maximum and removal that this replaces cost five instructions a
@@ -263,31 +263,47 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
                            uint2* cand, Chosen& c) {
   const int k = a.top_k;
   if (k > 16) return 0;
-  // the k-th largest of the maxima of half lanes, the least of those with
-  // fewer than k above them (of whole lanes: more than 16 keys would pass for
-  // 0.7% of the rows at 8 of 256, a quarter at 10 of 512)
+  // A lower bound of the k-th key: the k-th largest of the maxima of half lanes
+  // (the least of those with fewer than k above them; of 256 random keys 9 pass
+  // for k = 8), or of whole lanes, for which a third of the instructions do, where
+  // k is below 8: 8.7 keys pass for k = 7, more than 16 for 0.05% of the rows,
+  // but 10.4 and 0.9% for k = 8, a quarter of the rows for k = 10 (65536 x 60, k
+  // = 4: 11.4 us against 14.0 with half lanes; 4096 x 256, k = 8: 6.4 against
+  // 5.1).  Up to 128 experts only: with both in one kernel the larger ones lose 4%
+  // for k = 8 (65536 x 256: 23.7 us against 22.6).
   float ma = key[0], mb = key[V / 2];
 #pragma unroll
   for (int i = 1; i < V / 2; i++) {
     ma = fmaxf(ma, key[i]);
     mb = fmaxf(mb, key[V / 2 + i]);
   }
-  int na = mb > ma, nb = ma > mb;
+  float bound;
+  if (V <= 8 && k <= 7) {
+    ma = fmaxf(ma, mb);
+    int na = 0;
+#define ROTATE(R) na += dpp<0x120 + R>(ma) > ma;
+    ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
+    ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)
+#undef ROTATE
+    bound = na < k ? ma : INFINITY;
+  } else {
+    int na = mb > ma, nb = ma > mb;
 #define ROTATE(R)                                                     \
   {                                                                   \
     const float oa = dpp<0x120 + R>(ma), ob = dpp<0x120 + R>(mb);     \
     na += (oa > ma) + (ob > ma);                                      \
     nb += (oa > mb) + (ob > mb);                                      \
   }
-  ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
-  ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)
+    ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
+    ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)
 #undef ROTATE
-  float bound = fminf(na < k ? ma : INFINITY, nb < k ? mb : INFINITY);
-  bound = row_min(bound) - 2.0f * err;
+    bound = fminf(na < k ? ma : INFINITY, nb < k ? mb : INFINITY);
+  }
+  bound = fmaxf(row_min(bound) - 2.0f * err, -FLT_MAX);  // (-inf is no candidate)
   // candidates of this lane, and of the lanes before it
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < V; i++) n += key[i] >= bound && key[i] > -INFINITY;
+  for (int i = 0; i < V; i++) n += key[i] >= bound;
   int at = n;
   at += dpp_zero<0x111>(at);
   at += dpp_zero<0x112>(at);
@@ -298,7 +314,7 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
   at -= n;
 #pragma unroll
   for (int i = 0; i < V; i++) {
-    if (key[i] >= bound && key[i] > -INFINITY) {
+    if (key[i] >= bound) {
       cand[at] = make_uint2(__float_as_uint(key[i]), (uint32_t)expert_of<V>(i, j));
       at++;
     }
