@@ -86,8 +86,8 @@ DEV void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
 }
 
 // T threads a row (64: four rows a workgroup), up to VPT vectors a thread.
-// 65536 x 6144 with the residual and E4M3 codes: 3.64 GB in 623 us, 5.8 TB/s (a
-// large copy reaches 4.7).
+// 65536 x 6144 with the residual and E4M3 codes: 3.64 GB in 580 - 623 us, 5.8 - 6.2
+// TB/s (a large copy reaches 4.7).
 template <int T, int VPT, bool PAST>
 __global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormParams a) {
   constexpr int ROWS = T < 128 ? 256 / T : 1;

@@ -25,8 +25,8 @@
 //
 // Bound: up to some thousand tokens by latency (8 tokens of 256 experts: 4.9 us,
 // a kernel of that length has a launch, one trip to memory and the chain of
-// the choice); from there on by instructions, about 700 a wavefront of four
-// tokens.  65536 x 256 fp32: choice 23 us (71 MB, 3.1 TB/s), gradient 40 us
+// the choice); from there on by instructions, 680 a wavefront of four
+// tokens.  65536 x 256 fp32: choice 22.5 us (71 MB, 3.1 TB/s), gradient 40 us
 // (138 MB, 3.5 TB/s).  16384 x 256: choice 8.5 us, with the loss 20 us, of which
 // the join is 7; gradient 14 us.
 #include <algorithm>
