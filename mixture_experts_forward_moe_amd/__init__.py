@@ -352,9 +352,18 @@ def moe_quantize_mx(x, rows: int, cols: int, elem: int, q, sf, stream=None):
 
 # ---- around the routed experts: norm, router, balance loss, linear ----------
 
-# element types an argument of each kind may come in (filled in when first used,
-# so that this module imports without torch): bf16 also as its 16 bits
-_KINDS = {}
+class _Kind(list):
+    """The element types an argument may come in: filled in when first used, so
+    that this module imports without torch."""
+
+    def __init__(self, name, *types):
+        self.name, self.types = name, types
+
+
+_BF16 = _Kind("bf16", "bfloat16", "int16", "uint16")  # also as its 16 bits
+_F32 = _Kind("fp32", "float32")
+_I32 = _Kind("int32", "int32", "uint32")
+_BYTE = _Kind("bytes", "uint8", "int8", "bool", "float8_e4m3fn", "float8_e8m0fnu", "float4_e2m1fn_x2")
 _cuda = None  # torch._C
 
 
@@ -362,18 +371,15 @@ def _kinds():
     global _cuda
     import torch
     _cuda = torch._C
-    _KINDS.update(
-        bf16=(torch.bfloat16, torch.int16, torch.uint16), f32=(torch.float32,), i32=(torch.int32, torch.uint32),
-        byte=tuple(getattr(torch, n) for n in ("uint8", "int8", "bool", "float8_e4m3fn", "float8_e8m0fnu",
-                                               "float4_e2m1fn_x2") if hasattr(torch, n)))
-    return _KINDS
+    for kind in (_BF16, _F32, _I32, _BYTE):
+        kind[:] = [getattr(torch, n) for n in kind.types if hasattr(torch, n)]
 
 
 def _refuse(where, name, t, shape, kind, strided):
     if t is None:
         what = "is required"
-    elif t.shape != shape or t.dtype not in _KINDS[kind]:
-        what = f"must be {kind} {shape}, is {t.dtype} {tuple(t.shape)}"
+    elif t.shape != shape or t.dtype not in kind:
+        what = f"must be {kind.name} {shape}, is {t.dtype} {tuple(t.shape)}"
     elif not (t.is_contiguous() or strided and t.stride(-1) == 1 and t.stride(0) >= shape[1]):
         what = "must be contiguous" + (" in a row, and its rows apart" if strided else "")
     else:
@@ -381,10 +387,12 @@ def _refuse(where, name, t, shape, kind, strided):
     raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} {what}")
 
 
-def _arg(where: str, name: str, t, shape, kind: str, dev: int):
+def _arg(where: str, name: str, t, shape, kind: _Kind, dev: int):
     """The device address of tensor `t`, checked against the shape, the element
     type and the device that the call takes it with."""
-    if t is None or t.shape != shape or t.dtype not in (_KINDS or _kinds())[kind] or t.get_device() != dev or dev < 0 \
+    if not kind:
+        _kinds()
+    if t is None or t.shape != shape or t.dtype not in kind or t.get_device() != dev or dev < 0 \
             or not t.is_contiguous():
         _refuse(where, name, t, shape, kind, False)
     return t.data_ptr()
@@ -392,14 +400,21 @@ def _arg(where: str, name: str, t, shape, kind: str, dev: int):
 
 def _opt(where, name, t, shape, kind, dev):
     """The same of a tensor that may be None."""
-    return None if t is None else _arg(where, name, t, shape, kind, dev)
+    if t is None:
+        return None
+    if not kind:
+        _kinds()
+    if t.shape != shape or t.dtype not in kind or t.get_device() != dev or dev < 0 or not t.is_contiguous():
+        _refuse(where, name, t, shape, kind, False)
+    return t.data_ptr()
 
 
 def _rows(where, name, t, shape, kind, dev):
     """(address, row stride in elements; 0: contiguous) of a [rows, columns]
     tensor whose rows may be apart."""
-    if t is not None and t.shape == shape and t.dtype in (_KINDS or _kinds())[kind] and t.get_device() == dev \
-            and dev >= 0:
+    if not kind:
+        _kinds()
+    if t is not None and t.shape == shape and t.dtype in kind and t.get_device() == dev and dev >= 0:
         if t.is_contiguous():
             return t.data_ptr(), 0
         # (rows of an expanded tensor are not apart: their stride is 0)
@@ -410,10 +425,11 @@ def _rows(where, name, t, shape, kind, dev):
 
 def _dtype(where: str, name: str, t) -> int:
     """moe_dtype_t of a floating tensor (bf16 also as 16-bit integers)."""
-    d = t.dtype
-    if d.itemsize == 4 and d.is_floating_point:
+    if not _F32:
+        _kinds()
+    if t.dtype in _F32:
         return DTYPE_F32
-    if d.itemsize == 2 and str(d) != "torch.float16":
+    if t.dtype in _BF16:
         return DTYPE_BF16
     raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} must be bf16 or fp32, is {t.dtype}")
 
@@ -432,7 +448,8 @@ def _workspace(where, nbytes: int, given, t, stream):
     that stream alone has used and will use."""
     if given is not None:
         if given.get_device() != t.get_device() or not given.is_contiguous():
-            raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: workspace must be contiguous, with the call's other tensors")
+            raise MoeError(ERR_INVALID_ARGUMENT,
+                           f"{where}: workspace must be contiguous, with the call's other tensors")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if stream is None:
         given = _alloc(nbytes, t.device)
@@ -452,13 +469,13 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
     M, H = shape = x.shape
     dev = x.get_device()
     wd = _dtype(w, "weight", weight)
-    xp, xs = _rows(w, "x", x, shape, "bf16", dev)
-    rp, rs = (None, 0) if residual is None else _rows(w, "residual", residual, shape, "bf16", dev)
+    xp, xs = _rows(w, "x", x, shape, _BF16, dev)
+    rp, rs = (None, 0) if residual is None else _rows(w, "residual", residual, shape, _BF16, dev)
     _check(lib().moe_rmsnorm(
-        xp, xs, rp, rs, _arg(w, "weight", weight, (H,), "f32" if wd else "bf16", dev), wd, eps, M, H,
-        _opt(w, "residual_out", residual_out, shape, "bf16", dev), _opt(w, "y", y, shape, "bf16", dev), elem,
-        _opt(w, "q", q, (M, H if elem == 0 else H // 2), "byte", dev), _opt(w, "q_sf", q_sf, (M, H // 32), "byte", dev),
-        _opt(w, "rstd", rstd, (M,), "f32", dev), _raw_stream(w, dev, stream)), w)
+        xp, xs, rp, rs, _arg(w, "weight", weight, (H,), _F32 if wd else _BF16, dev), wd, eps, M, H,
+        _opt(w, "residual_out", residual_out, shape, _BF16, dev), _opt(w, "y", y, shape, _BF16, dev), elem,
+        _opt(w, "q", q, (M, H if elem == 0 else H // 2), _BYTE, dev), _opt(w, "q_sf", q_sf, (M, H // 32), _BYTE, dev),
+        _opt(w, "rstd", rstd, (M,), _F32, dev), _raw_stream(w, dev, stream)), w)
 
 
 @functools.lru_cache
@@ -473,10 +490,10 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     M, H = shape = dy.shape
     dev = dy.get_device()
     wd = _dtype(w, "weight", weight)
-    args = (_arg(w, "dy", dy, shape, "bf16", dev), _arg(w, "h", h, shape, "bf16", dev),
-            _arg(w, "weight", weight, (H,), "f32" if wd else "bf16", dev), wd, _arg(w, "rstd", rstd, (M,), "f32", dev),
-            _opt(w, "dh", dh, shape, "bf16", dev), M, H, _arg(w, "dx", dx, shape, "bf16", dev),
-            _opt(w, "dweight", dweight, (H,), "f32", dev))
+    args = (_arg(w, "dy", dy, shape, _BF16, dev), _arg(w, "h", h, shape, _BF16, dev),
+            _arg(w, "weight", weight, (H,), _F32 if wd else _BF16, dev), wd, _arg(w, "rstd", rstd, (M,), _F32, dev),
+            _opt(w, "dh", dh, shape, _BF16, dev), M, H, _arg(w, "dx", dx, shape, _BF16, dev),
+            _opt(w, "dweight", dweight, (H,), _F32, dev))
     st = _raw_stream(w, dev, stream)
     wp, nbytes = None, 0
     if dweight is not None:
@@ -490,8 +507,9 @@ def balance_workspace_size(M: int, E: int) -> int:
 
 
 def _balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss):
-    return (_arg(w, "expert_counts", expert_counts, (E,), "i32", dev),
-            _arg(w, "mean_probs", mean_probs, (E,), "f32", dev), _arg(w, "prob_grad", prob_grad, (E,), "f32", dev), _arg(w, "loss", loss, (1,), "f32", dev))
+    return (_arg(w, "expert_counts", expert_counts, (E,), _I32, dev),
+            _arg(w, "mean_probs", mean_probs, (E,), _F32, dev), _arg(w, "prob_grad", prob_grad, (E,), _F32, dev),
+            _arg(w, "loss", loss, (1,), _F32, dev))
 
 
 def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renormalize=True, select_bias=None,
@@ -506,10 +524,11 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
     k = topk_ids.shape[-1]
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
-    lp, ls = _rows(w, "logits", logits, (M, E), "f32" if d else "bf16", dev)
-    args = (lp, d, ls, _opt(w, "select_bias", select_bias, (E,), "f32", dev),
-            _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, 1 if renormalize else 0, M, E, k, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
-            _arg(w, "topk_weights", topk_weights, (M, k), "f32", dev), coef)
+    lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
+    args = (lp, d, ls, _opt(w, "select_bias", select_bias, (E,), _F32, dev),
+            _opt(w, "token_mask", token_mask, (M,), _BYTE, dev), score, 1 if renormalize else 0, M, E, k,
+            _arg(w, "topk_ids", topk_ids, (M, k), _I32, dev),
+            _arg(w, "topk_weights", topk_weights, (M, k), _F32, dev), coef)
     st = _raw_stream(w, dev, stream)
     if expert_counts is None and mean_probs is None and prob_grad is None and loss is None:
         _check(lib().moe_router_topk(*args, None, None, None, None, None, 0, st), w)
@@ -528,9 +547,10 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     k = topk_ids.shape[-1]
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
-    lp, ls = _rows(w, "logits", logits, (M, E), "f32" if d else "bf16", dev)
-    args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
-            _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, M, E, k, coef, *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
+    lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
+    args = (lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), _I32, dev),
+            _opt(w, "token_mask", token_mask, (M,), _BYTE, dev), score, M, E, k, coef,
+            *_balance_args(w, E, dev, expert_counts, mean_probs, prob_grad, loss))
     st = _raw_stream(w, dev, stream)
     workspace, wp, nbytes = _workspace(w, balance_workspace_size(M, E), workspace, logits, stream)
     _check(lib().moe_balance_loss(*args, wp, nbytes, st), w)
@@ -547,12 +567,13 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
     d = _dtype(w, "logits", logits)
     if _dtype(w, "d_logits", d_logits) != d:
         raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: d_logits must have the type of logits")
-    kind = "f32" if d else "bf16"
+    kind = _F32 if d else _BF16
     lp, ls = _rows(w, "logits", logits, (M, E), kind, dev)
     _check(lib().moe_router_backward(
-        lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), "i32", dev),
-        _opt(w, "token_mask", token_mask, (M,), "byte", dev), score, 1 if renormalize else 0, M, E, k, _opt(w, "d_topk_weights", d_topk_weights, (M, k), "f32", dev),
-        _opt(w, "prob_grad", prob_grad, (E,), "f32", dev), _opt(w, "d_loss", d_loss, (1,), "f32", dev),
+        lp, d, ls, _arg(w, "topk_ids", topk_ids, (M, k), _I32, dev),
+        _opt(w, "token_mask", token_mask, (M,), _BYTE, dev), score, 1 if renormalize else 0, M, E, k,
+        _opt(w, "d_topk_weights", d_topk_weights, (M, k), _F32, dev),
+        _opt(w, "prob_grad", prob_grad, (E,), _F32, dev), _opt(w, "d_loss", d_loss, (1,), _F32, dev),
         _arg(w, "d_logits", d_logits, (M, E), kind, dev), _raw_stream(w, dev, stream)), w)
 
 
@@ -565,8 +586,9 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_mx(
-        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), "byte", dev),
-        _arg(f, "x_sf", x_sf, (M, K // 32), "byte", dev), x_elem, _arg(f, "w", w, (N, K // 2), "byte", dev), _arg(f, "w_sf", w_sf, (N, K // 32), "byte", dev),
-        _opt(f, "alpha", alpha, (1,), "f32", dev), _opt(f, "bias", bias, (N,), "f32", dev), M, N, K,
-        1 if accumulate else 0, _arg(f, "y", y, (M, N), "f32" if d else "bf16", dev), d,
+        _arg(f, "x", x, (M, K if x_elem == 0 else K // 2), _BYTE, dev),
+        _arg(f, "x_sf", x_sf, (M, K // 32), _BYTE, dev), x_elem, _arg(f, "w", w, (N, K // 2), _BYTE, dev),
+        _arg(f, "w_sf", w_sf, (N, K // 32), _BYTE, dev),
+        _opt(f, "alpha", alpha, (1,), _F32, dev), _opt(f, "bias", bias, (N,), _F32, dev), M, N, K,
+        1 if accumulate else 0, _arg(f, "y", y, (M, N), _F32 if d else _BF16, dev), d,
         _raw_stream(f, dev, stream)), f)

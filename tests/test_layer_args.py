@@ -165,17 +165,18 @@ def test_binding_refuses_other_element_types():
         (lambda: moe.moe_rmsnorm(x.half(), w, y=x), "x must be bf16"),
         (lambda: moe.moe_rmsnorm(x, w, y=x.half()), "weight|y must be bf16|on the GPU"),
         (lambda: moe.moe_rmsnorm_backward(x.half(), x, w, w[:4], x), "dy must be bf16"),
-        (lambda: moe.moe_linear_mx(x.to(torch.float8_e5m2), w, w, w, x), "x must be byte|w"),
+        (lambda: moe.moe_linear_mx(x.to(torch.float8_e5m2), w, w, w, x), "x must be bytes|w"),
     ]:
         with pytest.raises(moe.MoeError, match=what):
             call_()
     with pytest.raises(moe.MoeError):
         moe.moe_router_topk(f.half(), ids, f[:, :2])
     # (past the device check the rest is the same function: by itself)
-    for t, kind in [(ids, "f32"), (f, "i32"), (x.half(), "bf16"), (f.to(torch.float8_e5m2), "byte"),
-                    (f.to(torch.float8_e4m3fnuz), "byte"), (ids.to(torch.int64), "i32")]:
-        with pytest.raises(moe.MoeError, match=f"must be {kind}"):
-            moe._arg("call", "t", t, tuple(t.shape), kind, 0)
+    for t, kind in [(ids, moe._F32), (f, moe._I32), (x.half(), moe._BF16), (f.to(torch.float8_e5m2), moe._BYTE),
+                    (f.to(torch.float8_e4m3fnuz), moe._BYTE), (ids.to(torch.int64), moe._I32)]:
+        for check in (moe._arg, moe._opt, moe._rows):
+            with pytest.raises(moe.MoeError, match=f"must be {kind.name}"):
+                check("call", "t", t, tuple(t.shape), kind, 0)
 
 
 def test_binding_refuses_another_device_than_the_current_one(monkeypatch):
@@ -192,10 +193,10 @@ def test_binding_refuses_rows_that_are_not_apart():
     """An expanded row has stride 0, which the library takes for contiguous."""
     row = torch.zeros(1, 64, dtype=torch.bfloat16)
     with pytest.raises(moe.MoeError, match="rows apart"):
-        moe._rows("call", "x", row.expand(4, 64), (4, 64), "bf16", -1)
+        moe._rows("call", "x", row.expand(4, 64), (4, 64), moe._BF16, -1)
     over = torch.zeros(4 * 32 + 32).as_strided((4, 64), (32, 1))
     with pytest.raises(moe.MoeError, match="rows apart"):
-        moe._rows("call", "x", over, (4, 64), "f32", -1)
+        moe._rows("call", "x", over, (4, 64), moe._F32, -1)
 
 
 def test_constants_match_header():
