@@ -26,6 +26,11 @@ DEV T ld_uniform(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;
 }
 
+// Between the lanes of a wavefront that hand values to each other through LDS:
+// the LDS keeps a wavefront's accesses in order, this keeps the compiler, which
+// sees one lane at a time, from moving one lane's read above another's write.
+DEV void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 DEV float bf16_to_f32(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 
 // fp32 -> bf16, round to nearest even (v_cvt_pk_bf16_f32 on gfx950)

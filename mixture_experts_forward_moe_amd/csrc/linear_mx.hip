@@ -285,6 +285,7 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
           for (int c = 0; c < 2; c++)
             *reinterpret_cast<u32x4_t*>(out + 64 * (r % ROWS) + 16 * ((2 * h + c) ^ ((r >> 2) & 3))) = o[c];
         }
+        wave_fence();  // the rows are read by other lanes
         const int64_t row0 = m0 + 32 * m + ROWS * part;
         auto rows_of = [&](auto w_) {  // in pieces of W columns, 32 / W lanes a row
           constexpr int W = decltype(w_)::value, LR = 32 / W;
@@ -304,6 +305,7 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
         else if (width == 4) rows_of(std::integral_constant<int, 4>{});
         else if (width == 2) rows_of(std::integral_constant<int, 2>{});
         else rows_of(std::integral_constant<int, 1>{});
+        wave_fence();  // and written again once they have been
       }
       __builtin_amdgcn_sched_barrier(0);
     }

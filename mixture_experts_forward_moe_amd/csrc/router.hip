@@ -319,11 +319,11 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
       at++;
     }
   }
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  wave_fence();
   const bool two = __any(total > 16);
   const bool have = j < total, have2 = j + 16 < total;
   const uint2 own = have ? cand[j] : make_uint2(0u, 0u), own2 = have2 ? cand[j + 16] : make_uint2(0u, 0u);
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  wave_fence();
   const float v = __uint_as_float(own.x), v2 = __uint_as_float(own2.x);
   const int e = have ? (int)own.y : INT32_MAX, e2 = have2 ? (int)own2.y : INT32_MAX;
   // places by descending key, then ascending expert
@@ -742,8 +742,6 @@ DEV void store_row(void* out, int f32, int64_t at, int E, int j, bool vec, const
     }
   }
 }
-
-DEV void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // The chosen experts' own terms are scattered through an LDS row of the token.
 template <int V>

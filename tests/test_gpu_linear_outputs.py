@@ -1,0 +1,74 @@
+"""The ways out of moe_linear_mx: every width of the stored pieces, at every
+alignment of y, in every kernel."""
+import pytest
+import torch
+
+import mixture_experts_forward_moe_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+GUARD = 173
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def whole_operands(M, N, K, elem, seed=1):
+    """x, w and their scales whose products are multiples of 1/4 up to 36 and
+    whose sums stay below 2^22: every order of the sums gives the same fp32."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    byte = lambda *s: torch.randint(0, 256, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    t = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device="cuda")
+    t = torch.cat((t, -t))
+    val = lambda q: t[torch.stack((q & 15, q >> 4), -1).flatten(-2).long()]  # noqa: E731
+    xq, wq = byte(M, K // 2), byte(N, K // 2)
+    prod = val(xq) @ val(wq).t()
+    if elem == 0:
+        xq = val(xq).to(torch.float8_e4m3fn).view(torch.uint8)
+    one = lambda n: torch.full((n, K // 32), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    return (xq, one(M), wq, one(N)), prod
+
+
+def placed(M, N, dtype, offset):
+    """y at `offset` elements behind an aligned address, and a check of what
+    lies around it."""
+    size = torch.empty(0, dtype=dtype).element_size()
+    room = torch.full(((M * N + offset) * size + 512,), GUARD, dtype=torch.uint8, device="cuda")
+    at, end = offset * size, (offset + M * N) * size
+
+    def check():
+        assert bool((room[:at] == GUARD).all()) and bool((room[end:] == GUARD).all()), "written outside of y"
+    return room[at:end].view(dtype).view(M, N), check
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (7, 515, 1536), (70, 200, 160),                                     # 16 x 16 tiles
+    (300, 512, 1536), (300, 515, 1536), (300, 516, 2048), (300, 514, 1024),
+    (1100, 1252, 160), (1237, 2056, 1568), (1237, 2055, 1568), (2111, 1110, 736), (600, 4100, 2080),
+    (2500, 2576, 544), (4096, 4096, 1024), (3900, 4090, 1120),
+])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_ways_out(M, N, K, elem):
+    say(f"ways out M={M} N={N} K={K} elem={elem}")
+    args, prod = whole_operands(M, N, K, elem)
+    for offset in (0, 1, 2, 4):
+        y, check = placed(M, N, BF16, offset)
+        moe.moe_linear_mx(*args, y, x_elem=elem)
+        torch.cuda.synchronize()
+        check()
+        assert torch.equal(y, prod.to(BF16)), offset
+        y32, check = placed(M, N, F32, offset)
+        moe.moe_linear_mx(*args, y32, x_elem=elem)
+        torch.cuda.synchronize()
+        check()
+        assert torch.equal(y32, prod), offset
+        # (fp32: a sum of two multiples of 1/4 below 2^22; bf16: rounded once)
+        moe.moe_linear_mx(*args, y32, x_elem=elem, accumulate=True)
+        assert torch.equal(y32, 2 * prod), offset
+        y.fill_(3)
+        moe.moe_linear_mx(*args, y, x_elem=elem, accumulate=True)
+        torch.cuda.synchronize()
+        check()
+        assert torch.equal(y, (prod + 3).to(BF16)), offset
