@@ -533,6 +533,8 @@ typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_t;
  * than top_k choosable experts gets id -1 and weight 0 in the places left,
  * and so does every place of a token with token_mask[t] == 0 (uint8 [M], NULL: all
  * tokens count): moe_sort drops those routes.
+ * What a token gets depends on its own logits alone, bit for bit, whatever
+ * the batch holds beside it.
  * E at most 1024 and top_k at most 64 (else MOE_ERR_UNSUPPORTED); top_k <= E.
  *
  * expert_counts, mean_probs, prob_grad and loss: all NULL, or all given; then
@@ -584,8 +586,9 @@ moe_status_t moe_balance_loss(const void* logits, moe_dtype_t logits_dtype, int6
  *   renormalize: w_j (dw_j - sum dw w) (SIGMOID: times 1 - s) on the chosen
  * topk_ids, token_mask, score and renormalize as in the forward calls; places
  * with an id outside [0, E) have no weight, equal ids of a token are places
- * of their own, whose gradients add up.  Tokens masked out get zeros.  MOE_ERR_INVALID_ARGUMENT:
- * neither gradient given, d_loss without prob_grad. */
+ * of their own, whose gradients add up.  Tokens masked out get zeros; a
+ * token's gradients depend on its own row alone, bit for bit.
+ * MOE_ERR_INVALID_ARGUMENT: neither gradient given, d_loss without prob_grad. */
 moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, int64_t logits_row_stride,
                                  const int32_t* topk_ids, const uint8_t* token_mask, moe_score_t score,
                                  int renormalize, int M, int E, int top_k, const float* d_topk_weights,

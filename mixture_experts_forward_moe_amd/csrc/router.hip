@@ -253,16 +253,17 @@ DEV double sum_f64(const RouterParams& a, int64_t at, float top, int j) {
   return row_add(sum);
 }
 
-// The choice by candidates (see above) of the wavefront's four tokens: the
-// number of slots used, one candidate a lane or two (17 to 32 of them).  key:
-// the logits, or with BIAS fp32 forms of the keys, each off by at most err;
-// where two candidates are closer than that the candidates' keys are compared
-// in fp64.  0, and nothing chosen, if any of the tokens needs the other way.
+// The choice by candidates (see above) of the wavefront's four tokens, up to 16
+// experts each: the number of slots used, one candidate a lane or two (17 to 32
+// of them).  key: the logits, or with BIAS fp32 forms of the keys, each off by
+// at most err; where two candidates are closer than that the candidates' keys
+// are compared in fp64.  rounds: in, the token counts (nothing is chosen for
+// one that does not); out, it has more candidates and goes the other way.  Each
+// token by itself, so that what it gets does not hang on its neighbours.
 template <int V, bool BIAS>
 DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, const float (&key)[V], float err, int j,
-                           uint2* cand, Chosen& c) {
+                           uint2* cand, Chosen& c, bool& rounds) {
   const int k = a.top_k;
-  if (k > 16) return 0;
   // A lower bound of the k-th key: the k-th largest of the maxima of half lanes
   // (the least of those with fewer than k above them; of 256 random keys 9 pass
   // for k = 8), or of whole lanes, for which a third of the instructions do, where
@@ -309,8 +310,13 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
   at += dpp_zero<0x112>(at);
   at += dpp_zero<0x114>(at);
   at += dpp_zero<0x118>(at);
-  const int total = __shfl(at, 15, 16);
-  if (__any(total > 32)) return 0;
+  int total = __shfl(at, 15, 16);
+  const bool counts = rounds;
+  rounds = counts && (total > 32 || !(err < INFINITY));
+  if (!counts || rounds) {  // (no key passes)
+    total = 0;
+    bound = INFINITY;
+  }
   at -= n;
 #pragma unroll
   for (int i = 0; i < V; i++) {
@@ -378,16 +384,12 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
 
 // The choice by k rounds of maximum and removal, the row read again in each
 // (it is in the first-level cache; registers for it would halve the wavefronts
-// of the other way).  Lane j looks at the experts j, j + 16, ..
+// of the other way).  Lane j looks at the experts j, j + 16, .. and gets places
+// j, j + 16, .., which c holds with no expert before.
 template <bool BIAS>
 DEV void choose_rounds(const RouterParams& a, int64_t at_row, float top, int j, Chosen& c) {
   uint64_t taken = 0;
   const double sum = BIAS ? sum_f64(a, at_row, top, j) : 1.0;
-#pragma unroll
-  for (int q = 0; q < SLOTS; q++) {
-    c.id[q] = -1;
-    c.place[q] = j + 16 * q;
-  }
 #pragma unroll 1
   for (int s = 0; s < a.top_k; s++) {
     // the largest key; of equal ones the lowest expert
@@ -466,7 +468,12 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
         for (int i = 0; i < V; i++) sum += exp_neg(l[i] - top);
       }
       int used = (a.top_k + 15) / 16;
-      bool read_logits = true;
+      bool rounds = on;  // this token's choice goes by rounds
+#pragma unroll
+      for (int q = 0; q < SLOTS; q++) {
+        c.id[q] = -1;
+        c.place[q] = j + 16 * q;
+      }
       uint2* own_cand = cand[threadIdx.x >> 4];
       if constexpr (BIAS) {
         // Off by, in steps of 2^-24: a sigmoid, 8 of the row's largest (exp2 and
@@ -497,15 +504,12 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
           big = fmaxf(big, l[i] == -INFINITY ? 0.0f : fabsf(l[i]));
         }
         const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f + 0x1p-23f * row_max(big);
-        const int n = __all(err < INFINITY) ? choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c) : 0;
-        if (n) used = n;
-        else choose_rounds<true>(a, at_row, top, j, c);
+        if (a.top_k <= 16) used = choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c, rounds);
       } else {
-        const int n = choose_candidates<V, false>(a, at_row, top, l, 0.0f, j, own_cand, c);
-        read_logits = n == 0;
-        if (n) used = n;
-        else choose_rounds<false>(a, at_row, top, j, c);
+        if (a.top_k <= 16) used = choose_candidates<V, false>(a, at_row, top, l, 0.0f, j, own_cand, c, rounds);
       }
+      if (rounds) choose_rounds<BIAS>(a, at_row, top, j, c);
+      const bool read_logits = BIAS || rounds;
 #pragma unroll
       for (int q = 0; q < SLOTS; q++) {
         if (q >= used) c.id[q] = -1;

@@ -1,0 +1,112 @@
+"""A token's experts, weights and gradients hang on its own logits alone,
+and tokens that are hard to choose for cost the others nothing."""
+import pytest
+import torch
+
+import layer_ref as ref
+import mixture_experts_forward_moe_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+INF, NAN = float("inf"), float("nan")
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def topk(l, k, **kw):
+    ids = torch.empty(l.shape[0], k, dtype=torch.int32, device="cuda")
+    w = torch.empty(l.shape[0], k, device="cuda")
+    moe.moe_router_topk(l, ids, w, **kw)
+    return ids, w
+
+
+def gradient(l, ids, dw, grad, **kw):
+    d = torch.empty_like(l)
+    moe.moe_router_backward(l, ids, d, d_topk_weights=dw, prob_grad=grad, **kw)
+    return d
+
+
+def median_us(f, n=20):
+    """Median time of a call in a replayed graph of n."""
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        f()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(n):
+            f()
+    times = []
+    for _ in range(9):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        times.append(a.elapsed_time(b) * 1e3 / n)
+    return sorted(times)[4]
+
+
+# what stands beside the tokens looked at: rows that choose by another way
+BESIDE = {
+    "equal": lambda l: torch.zeros_like(l),
+    "negative": lambda l: -5 - l.abs(),
+    "nothing": lambda l: torch.full_like(l, -INF),
+    "nan": lambda l: torch.full_like(l, NAN),
+    "two slots": lambda l: torch.where(torch.arange(l.shape[1], device="cuda") % (l.shape[1] // 20 + 1) == 0, 9.0, l),
+}
+
+
+@pytest.mark.parametrize("E,k", [(40, 4), (100, 7), (159, 6), (256, 8), (500, 16), (128, 20), (1000, 8)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_rows_do_not_hang_on_their_neighbours(E, k, dtype):
+    g = torch.Generator(device="cuda").manual_seed(E + k)
+    M = 203
+    l = torch.randn(M, E, generator=g, device="cuda").to(dtype)
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1
+    dw, grad = torch.randn(M, k, generator=g, device="cuda"), torch.randn(E, generator=g, device="cuda")
+    out = [torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E, device="cuda"),
+           torch.empty(E, device="cuda"), torch.empty(1, device="cuda")]
+    names = ("expert_counts", "mean_probs", "prob_grad", "loss")
+    for score in (0, 1):
+        for renorm in (True, False):
+            for b in (None, bias):
+                kw = dict(score=score, renormalize=renorm, select_bias=b)
+                ids, w = topk(l, k, **kw)
+                d = gradient(l, ids, dw, grad, score=score, renormalize=renorm)
+                fused = topk(l, k, coef=0.1, **dict(zip(names, out)), **kw)
+                assert torch.equal(fused[0], ids) and torch.equal(fused[1], w)
+                for what, change in BESIDE.items():
+                    say(f"rows E={E} k={k} {dtype} score={score} renorm={renorm} bias={b is not None} {what}")
+                    for first in (0, 2):
+                        at = torch.arange(M, device="cuda") % 4 != first
+                        other = torch.where(at[:, None], l, change(l).to(dtype))
+                        ids2, w2 = topk(other, k, **kw)
+                        assert torch.equal(ids2[at], ids[at]) and torch.equal(w2[at], w[at])
+                        d2 = gradient(other, ids2, dw, grad, score=score, renormalize=renorm)
+                        assert torch.equal(d2[at], d[at])
+                        ids64, w64 = ref.router_topk(other.cpu(), k, score, renorm, None if b is None else b.cpu())
+                        assert torch.equal(ids2.cpu(), ids64)
+                        on = at.to(torch.uint8)
+                        ids2, w2 = topk(other, k, token_mask=on, **kw)
+                        assert torch.equal(ids2[at], ids[at]) and torch.equal(w2[at], w[at])
+                        assert bool((ids2[~at] == -1).all()) and bool((w2[~at] == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_padding_rows_cost_no_more_than_others(dtype):
+    """A masked row's choice is thrown away, whatever it holds: a batch whose
+    padding has equal logits (every key a candidate) takes the time of one
+    whose padding is random.  (Chosen by rounds, those rows made it 4.7 times.)"""
+    say(f"padding {dtype}")
+    M, E, k = 65536, 256, 8
+    l = torch.randn(M, E, device="cuda").to(dtype)
+    mask = (torch.arange(M, device="cuda") % 5 != 4).to(torch.uint8)
+    same = torch.where(mask.bool()[:, None], l, torch.zeros_like(l))
+    t = [median_us(lambda: topk(x, k, token_mask=mask)) for x in (l, same)]
+    say(t)
+    assert t[1] <= 2 * t[0]
