@@ -337,12 +337,17 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
   bool exactly = BIAS && two;
   if (!two) {
     const uint32_t hi = have ? ordered(v) : 0u, lo = ~(uint32_t)e;
+    // (all lanes take part in each rotation: one that a condition had switched
+    // off would be read as 0)
     bool close = false;
 #define ROTATE(R)                                                                                        \
   {                                                                                                      \
     const uint32_t h2 = (uint32_t)dpp<0x120 + R>((int)hi), l2 = (uint32_t)dpp<0x120 + R>((int)lo);        \
     rank += (((uint64_t)h2 << 32) | l2) > (((uint64_t)hi << 32) | lo);                                   \
-    if (BIAS) close |= have && h2 != 0u && fabsf(dpp<0x120 + R>(v) - v) <= 2.0f * err;                   \
+    if (BIAS) {                                                                                          \
+      const float o = dpp<0x120 + R>(v);                                                                 \
+      close |= have && h2 != 0u && fabsf(o - v) <= 2.0f * err;                                           \
+    }                                                                                                    \
   }
     ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
     ROTATE(12) ROTATE(13) ROTATE(14) ROTATE(15)

@@ -110,3 +110,31 @@ def test_padding_rows_cost_no_more_than_others(dtype):
     t = [median_us(lambda: topk(x, k, token_mask=mask)) for x in (l, same)]
     say(t)
     assert t[1] <= 2 * t[0]
+
+
+@pytest.mark.parametrize("E,k", [(16, 4), (40, 4), (64, 8), (128, 6), (159, 6), (256, 8), (256, 3), (500, 10), (1000, 8)])
+@pytest.mark.parametrize("score", [0, 1])
+def test_one_pair_closer_than_fp32_resolves(E, k, score):
+    """Two experts whose scores plus bias agree to fp32's last bits, among
+    others that are far apart: the fp64 order, wherever the pair lies."""
+    say(f"one close pair E={E} k={k} score={score}")
+    for seed in range(12):
+        g = torch.Generator().manual_seed(seed)
+        M = 64
+        b = torch.randn(E, generator=g) * 0.1
+        i, j = torch.randperm(E, generator=g)[:2].tolist()
+        if score:  # the others differ from token to token
+            l = torch.randn(M, E, generator=g)
+            l[:, i], l[:, j] = 2.5, 1.0
+        else:      # the same logits in another order, so that the pair's softmax stays
+            others = torch.tensor([e for e in range(E) if e not in (i, j)])
+            row = torch.randn(E, generator=g)
+            row[i], row[j] = 1.5, 0.75
+            l = row.repeat(M, 1)
+            for m in range(M):
+                l[m, others] = row[others[torch.randperm(E - 2, generator=g)]]
+        s = ref.scores(l[:1], score)[0][0]
+        b[i] = 0.5
+        b[j] = (s[i] + 0.5 - s[j]).float()
+        ids, _ = topk(l.cuda(), k, score=score, select_bias=b.cuda())
+        assert torch.equal(ids.cpu(), ref.router_topk(l, k, score, True, b)[0]), seed
