@@ -313,9 +313,9 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
   int total = __shfl(at, 15, 16);
   const bool counts = rounds;
   rounds = counts && (total > 32 || !(err < INFINITY));
-  if (!counts || rounds) {  // (no key passes)
+  if (!counts || rounds) {  // (nothing is >= NaN: no key passes, not +inf either)
     total = 0;
-    bound = INFINITY;
+    bound = __builtin_nanf("");
   }
   at -= n;
 #pragma unroll

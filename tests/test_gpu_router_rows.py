@@ -138,3 +138,26 @@ def test_one_pair_closer_than_fp32_resolves(E, k, score):
         b[j] = (s[i] + 0.5 - s[j]).float()
         ids, _ = topk(l.cuda(), k, score=score, select_bias=b.cuda())
         assert torch.equal(ids.cpu(), ref.router_topk(l, k, score, True, b)[0]), seed
+
+
+@pytest.mark.parametrize("E,k", [(40, 4), (128, 7), (300, 16), (1000, 9)])
+def test_infinite_keys_beside_other_tokens(E, k):
+    """A bias of +inf, in tokens with few candidates and with many (which go by
+    rounds and must leave the candidates of the others alone)."""
+    g = torch.Generator().manual_seed(E)
+    M = 70
+    l = torch.randn(M, E, generator=g)
+    l[1::4] = 0.5
+    mask = torch.ones(M, dtype=torch.uint8)
+    mask[2::4] = 0
+    for count in (1, 2, k, k + 2, E):
+        bias = torch.randn(E, generator=g) * 0.1
+        bias[torch.randperm(E, generator=g)[:count]] = INF
+        for score in (0, 1):
+            for m in (None, mask):
+                say(f"infinite E={E} k={k} count={count} score={score} mask={m is not None}")
+                ids, w = topk(l.cuda(), k, score=score, select_bias=bias.cuda(),
+                              token_mask=None if m is None else m.cuda())
+                ids64, w64 = ref.router_topk(l, k, score, True, bias, m)
+                assert torch.equal(ids.cpu(), ids64)
+                assert bool(((w.cpu().double() - w64).abs() <= w64 * (k + 40) * ref.U24).all())
