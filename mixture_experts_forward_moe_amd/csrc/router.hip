@@ -256,10 +256,11 @@ DEV double sum_f64(const RouterParams& a, int64_t at, float top, int j) {
 // The choice by candidates (see above) of the wavefront's four tokens, up to 16
 // experts each: the number of slots used, one candidate a lane or two (17 to 32
 // of them).  key: the logits, or with BIAS fp32 forms of the keys, each off by
-// at most err; where two candidates are closer than that the candidates' keys
-// are compared in fp64.  rounds: in, the token counts (nothing is chosen for
-// one that does not); out, it has more candidates and goes the other way.  Each
-// token by itself, so that what it gets does not hang on its neighbours.
+// at most err + 2^-23 |key|; where two candidates are closer than that the
+// candidates' keys are compared in fp64.  rounds: in, the token counts (nothing
+// is chosen for one that does not); out, it has more candidates and goes the
+// other way.  Each token by itself, so that what it gets does not hang on its
+// neighbours.
 template <int V, bool BIAS>
 DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, const float (&key)[V], float err, int j,
                            uint2* cand, Chosen& c, bool& rounds) {
@@ -300,7 +301,14 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
 #undef ROTATE
     bound = fminf(na < k ? ma : INFINITY, nb < k ? mb : INFINITY);
   }
-  bound = fmaxf(row_min(bound) - 2.0f * err, -FLT_MAX);  // (-inf is no candidate)
+  // What the errors can hide below it: k keys are at least `bound`, so the k-th
+  // true one is at least bound - err - 2^-24 |bound| (the error that the addition
+  // makes, half of what is allowed for), and a key that reaches that is at least
+  // bound - 2 err - 2^-22 |bound|.  Keys far below, such as those of a bias that
+  // takes an expert out, have no part in it, whatever their own error.
+  bound = row_min(bound);
+  if (BIAS) bound -= 2.0f * (err + 0x1p-23f * fabsf(bound));
+  bound = fmaxf(bound, -FLT_MAX);  // (-inf is no candidate)
   // candidates of this lane, and of the lanes before it
   int n = 0;
 #pragma unroll
@@ -312,7 +320,7 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
   at += dpp_zero<0x118>(at);
   int total = __shfl(at, 15, 16);
   const bool counts = rounds;
-  rounds = counts && (total > 32 || !(err < INFINITY));
+  rounds = counts && total > 32;
   if (!counts || rounds) {  // (nothing is >= NaN: no key passes, not +inf either)
     total = 0;
     bound = __builtin_nanf("");
@@ -340,13 +348,14 @@ DEV int choose_candidates(const RouterParams& a, int64_t at_row, float top, cons
     // (all lanes take part in each rotation: one that a condition had switched
     // off would be read as 0)
     bool close = false;
+    const float apart = 2.0f * (err + 0x1p-23f * fabsf(v));  // (each of a pair looks: the larger error counts)
 #define ROTATE(R)                                                                                        \
   {                                                                                                      \
     const uint32_t h2 = (uint32_t)dpp<0x120 + R>((int)hi), l2 = (uint32_t)dpp<0x120 + R>((int)lo);        \
     rank += (((uint64_t)h2 << 32) | l2) > (((uint64_t)hi << 32) | lo);                                   \
     if (BIAS) {                                                                                          \
       const float o = dpp<0x120 + R>(v);                                                                 \
-      close |= have && h2 != 0u && fabsf(o - v) <= 2.0f * err;                                           \
+      close |= have && h2 != 0u && fabsf(o - v) <= apart;                                                \
     }                                                                                                    \
   }
     ROTATE(1) ROTATE(2) ROTATE(3) ROTATE(4) ROTATE(5) ROTATE(6) ROTATE(7) ROTATE(8) ROTATE(9) ROTATE(10) ROTATE(11)
@@ -481,13 +490,12 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
       }
       uint2* own_cand = cand[threadIdx.x >> 4];
       if constexpr (BIAS) {
-        // Off by, in steps of 2^-24: a sigmoid, 8 of the row's largest (exp2 and
-        // rcp one of 2^-23 each, 1 + z and the product a half).  A softmax
+        // Scores are off by, in steps of 2^-24: a sigmoid, 8 of the row's largest
+        // (exp2 and rcp one of 2^-23 each, 1 + z and the product a half).  A softmax
         // V + 24 of its largest: V + 4 additions, 4 for exp, quotient and
         // product, and what the rounding of d = l - top does to the exp, |d| each,
         // of which a probability's |d| e^d is less than one and the sum's mean
         // at most ln E < 7.  The addition rounds relative to the key.
-        float big = 0.0f;
         if (!a.sigmoid) {
           if constexpr (STATS) {
 #pragma unroll
@@ -506,9 +514,8 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
           const int e = expert_of<V>(i, j);
           const float v = (a.sigmoid ? sigmoid_f32(l[i]) : l[i]) + a.select_bias[min(e, a.E - 1)];
           l[i] = l[i] != -INFINITY && v == v ? v : -INFINITY;
-          big = fmaxf(big, l[i] == -INFINITY ? 0.0f : fabsf(l[i]));
         }
-        const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f + 0x1p-23f * row_max(big);
+        const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f;
         if (a.top_k <= 16) used = choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c, rounds);
       } else {
         if (a.top_k <= 16) used = choose_candidates<V, false>(a, at_row, top, l, 0.0f, j, own_cand, c, rounds);

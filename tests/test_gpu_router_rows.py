@@ -161,3 +161,50 @@ def test_infinite_keys_beside_other_tokens(E, k):
                 ids64, w64 = ref.router_topk(l, k, score, True, bias, m)
                 assert torch.equal(ids.cpu(), ids64)
                 assert bool(((w.cpu().double() - w64).abs() <= w64 * (k + 40) * ref.U24).all())
+
+
+@pytest.mark.parametrize("E,k", [(40, 4), (60, 6), (256, 8), (300, 16), (1000, 9)])
+def test_bias_that_takes_experts_out_or_puts_them_first(E, k):
+    """Biases far from the scores: their own rounding errors are larger than
+    any difference of scores, which the other experts must not feel."""
+    g = torch.Generator().manual_seed(E)
+    M = 61
+    l = torch.randn(M, E, generator=g)
+    l[7] = 0.25
+    base = torch.randn(E, generator=g) * 0.1
+    at = torch.randperm(E, generator=g)
+    big = torch.finfo(F32).max
+    cases = {"one out": {-1e9: 1}, "lowest": {-big: 2}, "three out": {-1e9: 1, -999999936.0: 1, -3e4: 1},
+             "all but three out": {-1e9: E - 3}, "one first": {1e9: 1}, "many first": {1e9: k + 3},
+             "first and out": {1e9: 2, -1e9: 2, -big: 1}, "infinite": {INF: 1, -INF: 1}, "infinite first": {INF: k + 2},
+             "largest": {big: 3}}
+    for what, values in cases.items():
+        bias, n = base.clone(), 0
+        for v, count in values.items():
+            bias[at[n:n + count]] = v
+            n += count
+        for score in (0, 1):
+            for b in (bias, torch.where(bias == base, 0.0, bias)):
+                say(f"bias E={E} k={k} {what} score={score}")
+                for dtype in (F32, BF16):
+                    x = l.to(dtype)
+                    ids, w = topk(x.cuda(), k, score=score, select_bias=b.cuda())
+                    ids64, w64 = ref.router_topk(x, k, score, True, b)
+                    assert torch.equal(ids.cpu(), ids64)
+                    # half a dozen steps of |l| <= 6 and of the sum of k scores
+                    assert bool(((w.cpu().double() - w64).abs() <= w64 * (k + 40) * ref.U24).all())
+
+
+@pytest.mark.parametrize("score", [0, 1])
+def test_expert_taken_out_costs_the_others_nothing(score):
+    """One expert at -1e9: the others keep the time of an ordinary bias (8 times
+    that, when the errors of its key counted for all)."""
+    say(f"expert out score={score}")
+    M, E, k = 65536, 256, 8
+    l = torch.randn(M, E, device="cuda")
+    bias = torch.randn(E, device="cuda") * 0.1
+    out = bias.clone()
+    out[3] = -1e9
+    t = [median_us(lambda: topk(l, k, score=score, select_bias=b)) for b in (bias, out)]
+    say(t)
+    assert t[1] <= 2 * t[0]
