@@ -495,7 +495,8 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
         // V + 24 of its largest: V + 4 additions, 4 for exp, quotient and
         // product, and what the rounding of d = l - top does to the exp, |d| each,
         // of which a probability's |d| e^d is less than one and the sum's mean
-        // at most ln E < 7.  The addition rounds relative to the key.
+        // at most ln E < 7.  The addition rounds relative to the key.  Scores below
+        // fp32's normal range are 0: 2^-126 more.
         if (!a.sigmoid) {
           if constexpr (STATS) {
 #pragma unroll
@@ -515,7 +516,7 @@ __global__ __launch_bounds__(threads_of(STATS)) void router_kernel(const RouterP
           const float v = (a.sigmoid ? sigmoid_f32(l[i]) : l[i]) + a.select_bias[min(e, a.E - 1)];
           l[i] = l[i] != -INFINITY && v == v ? v : -INFINITY;
         }
-        const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f;
+        const float err = (a.sigmoid ? 8.0f * sigmoid_f32(top) : (V + 24) * most) * 0x1p-24f + 0x1p-125f;
         if (a.top_k <= 16) used = choose_candidates<V, true>(a, at_row, top, l, err, j, own_cand, c, rounds);
       } else {
         if (a.top_k <= 16) used = choose_candidates<V, false>(a, at_row, top, l, 0.0f, j, own_cand, c, rounds);

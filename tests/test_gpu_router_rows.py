@@ -208,3 +208,14 @@ def test_expert_taken_out_costs_the_others_nothing(score):
     t = [median_us(lambda: topk(l, k, score=score, select_bias=b)) for b in (bias, out)]
     say(t)
     assert t[1] <= 2 * t[0]
+
+
+def test_scores_below_the_normal_range():
+    """Scores that fp32 does not hold, beside biases of their size."""
+    say("tiny scores")
+    for l, bias in [([-87.5, -200.0], [0.0, 7e-39]), ([-88.0, -200.0], [1.2e-38, 1.5e-38]),
+                    ([-90.0, -89.0], [1.2e-38, 1.2e-38]), ([-200.0, -87.5, -100.0], [8e-39, 0.0, 3e-39])]:
+        l, bias = torch.tensor([l] * 5), torch.tensor(bias)
+        for k in (1, 2):
+            ids, _ = topk(l.cuda(), k, score=1, select_bias=bias.cuda())
+            assert torch.equal(ids.cpu(), ref.router_topk(l, k, 1, True, bias)[0])
