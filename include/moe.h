@@ -601,12 +601,14 @@ moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, i
  * outputs of moe_rmsnorm or moe_quantize_mx); w packed E2M1 [N, K/2], w_sf
  * E8M0 [N, K/32], laid out as an expert's w1 or w2; alpha a device fp32
  * scalar (NULL: 1); bias device fp32 [N] (NULL: none); y bf16 or fp32
- * [M, N] by y_dtype.  The products accumulate in fp32; alpha, bias and the
- * accumulation onto y are fp32 steps, and y is rounded once.  M, N >= 0; K a
+ * [M, N] by y_dtype.  The products accumulate in fp32; alpha * sum + bias is
+ * one fp32 step (a fused multiply-add), the accumulation onto y another, and y
+ * is rounded once.  M, N >= 0; K a
  * positive multiple of 32 (else MOE_ERR_INVALID_ARGUMENT).  x and w 16-byte
  * aligned, y aligned to its elements, K at most 2^20, M and N at most 2^26, M * N
  * at most 2^36 (else MOE_ERR_UNSUPPORTED).  Each output is one sum in an order that
- * depends on the shape alone: reproducible bit for bit. */
+ * depends on x_elem, M, N and K alone: reproducible bit for bit, also in a y of
+ * another type (rounded) or alignment. */
 moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, const uint8_t* w, const uint8_t* w_sf,
                            const float* alpha, const float* bias, int M, int N, int K, int accumulate, void* y,
                            moe_dtype_t y_dtype, moe_stream_t stream);

@@ -179,16 +179,16 @@ DEV void mfma_one(f32x16_t& acc, const u32x4_t& w, const XFrag<XE>& x, int ws, i
   acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, acc, 4, XE == 1 ? 4 : 0, 2 * U, ws, 2 * U, xs);
 }
 
+// alpha * sum + bias, one step with one rounding: written out, so that every
+// way out makes the same one
+DEV float scaled(float sum, float alpha, float bias) { return fmaf(sum, alpha, bias); }
+
 // y[m, n .. n + 15] of a lane: fp32, or onto what y holds
 DEV void store16(const LinearParams& a, const f32x16_t& acc, int64_t m, int n, float alpha) {
   float v[16];
 #pragma unroll
-  for (int j = 0; j < 16; j++) v[j] = acc[j] * alpha;
+  for (int j = 0; j < 16; j++) v[j] = scaled(acc[j], alpha, a.bias && n + j < a.N ? a.bias[n + j] : 0.0f);
   const int64_t at = m * a.N + n;
-  if (a.bias) {
-#pragma unroll
-    for (int j = 0; j < 16; j++) v[j] += n + j < a.N ? a.bias[n + j] : 0.0f;
-  }
   if (a.y_f32) {
     float* y = reinterpret_cast<float*>(a.y) + at;
     if (n + 16 <= a.N && a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0) {
@@ -270,10 +270,11 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
       for (int c = 0; c < 2; c++) {
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-          float lo = acc[n][m][8 * c + 2 * i] * alpha, hi = acc[n][m][8 * c + 2 * i + 1] * alpha;
+          const int k = 8 * c + 2 * i;
+          float lo = acc[n][m][k] * alpha, hi = acc[n][m][k + 1] * alpha;
           if (a.bias) {
-            lo += bias[8 * c + 2 * i];
-            hi += bias[8 * c + 2 * i + 1];
+            lo = scaled(acc[n][m][k], alpha, bias[k]);
+            hi = scaled(acc[n][m][k + 1], alpha, bias[k + 1]);
           }
           o[c][i] = pack_bf16x2(lo, hi);
         }
@@ -1014,7 +1015,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void linear_stream_kernel(const 
   for (int i = 0; i < 4; i++) {
     const int64_t row = m0 + 4 * q + i;
     if (row >= a.M) continue;
-    const float o = v[i] * alpha + bias;
+    const float o = scaled(v[i], alpha, bias);
     const int64_t at = row * a.N + n;
     if (a.y_f32) {
       float* y = reinterpret_cast<float*>(a.y) + at;
@@ -1042,12 +1043,20 @@ hipError_t launch(const LinearParams& p, hipStream_t s) {
   // x 4096 7.4 us against 8.2; 64 x 8192 x 1024 4.5 against 4.3).
   if (tiles(64, 64) <= CUS)
     return p.K >= 2048 ? launch_tile<XE, 1, 1, 128, 4, 2, 1>(p, s) : launch_tile<XE, 1, 1, 256, 2, 1, 2>(p, s);
-  if (!wide_rows(p)) return launch_tile_as<XE, false, 1, 2, 256, XE == 1 ? 3 : 2, 1, 2>(p, s);
+  const int64_t t128 = tiles(128, 128);
+  // K split in two goes by the shape alone, whatever becomes of the sums: its
+  // split is in their order.
+  const bool halves = XE == 0 && t128 <= CUS / 2 && p.K >= 2048;
+  if (!wide_rows(p)) {
+    if constexpr (XE == 0)
+      if (halves) return launch_tile_as<0, false, 1, 2, 256, 2, 2, 1>(p, s);
+    return launch_tile_as<XE, false, 1, 2, 256, XE == 1 ? 3 : 2, 1, 2>(p, s);
+  }
   // 256 x 256 tiles in whole rounds of the CUs, three quarters full at least
   // (2048 x 6144 x 4096, 0.75: 34.7 us against 44.5 in 128 x 128 tiles; 4096 x
   // 5120 x 2048, 0.63: 37.1 against 37.2, E4M3 53.9 against 47.0), and with
   // enough stages to fill its pipeline (8192 x 8192 x 512: 53.0 against 39.9).
-  const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS, t128 = tiles(128, 128);
+  const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS;
   if (p.K >= 1024 && 4 * big >= 3 * CUS * rounds) return launch_big<XE>(p, s);
   // Between, stages of 256 K load whole lines of W (64 x 128 x 128 stages reach
   // 14 TB/s from L2 into LDS and are bound by it).  E2M1: 64 x 64 tiles, from
@@ -1061,7 +1070,7 @@ hipError_t launch(const LinearParams& p, hipStream_t s) {
     if (t128 <= CUS * 3 / 4) return launch_tile_as<1, true, 1, 1, 256, 2, 1, 2>(p, s);
     return launch_tile_as<1, true, 2, 2, 256, 2, 1, 2>(p, s);
   } else {
-    if (t128 <= CUS / 2 && p.K >= 2048) return launch_tile_as<0, true, 1, 2, 256, 2, 2, 1>(p, s);
+    if (halves) return launch_tile_as<0, true, 1, 2, 256, 2, 2, 1>(p, s);
     if (t128 <= CUS) return launch_tile_as<0, true, 1, 2, 256, 2, 1, 2>(p, s);
     return launch_tile_as<0, true, 2, 2, 128, 3, 1, 2>(p, s);
   }

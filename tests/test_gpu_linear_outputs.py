@@ -72,3 +72,41 @@ def test_ways_out(M, N, K, elem):
         torch.cuda.synchronize()
         check()
         assert torch.equal(y, (prod + 3).to(BF16)), offset
+
+
+def mixed_operands(M, N, K, elem, seed=2):
+    """Random codes and scales of 2^-10 .. 2^10: sums that round at every step."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    byte = lambda lo, hi, *s: torch.randint(lo, hi, s, generator=g, device="cuda", dtype=torch.uint8)  # noqa: E731
+    xq = byte(0, 256, M, K // 2)
+    if elem == 0:  # E4M3 codes of both signs, without NaN
+        xq = byte(0, 126, M, K) | (byte(0, 2, M, K) << 7)
+    return xq, byte(117, 138, M, K // 32), byte(0, 256, N, K // 2), byte(117, 138, N, K // 32)
+
+
+@pytest.mark.parametrize("M,N,K", [
+    (8, 520, 1536), (70, 200, 1120),                                    # 16 x 16 tiles
+    (300, 512, 1536), (300, 512, 2048), (300, 520, 4096),               # 64 x 64, K split in two from 2048 on
+    (512, 4096, 4096), (1024, 1032, 2080), (520, 4104, 2048),           # E4M3: K split in two
+    (1237, 2056, 1568), (1100, 4096, 2048), (2500, 2576, 544), (4096, 4096, 1024), (3900, 4096, 1120),
+])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_one_sum_whatever_becomes_of_it(M, N, K, elem):
+    """y's type, alignment and the accumulation change no bit of the sums."""
+    say(f"one sum M={M} N={N} K={K} elem={elem}")
+    args = mixed_operands(M, N, K, elem)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    alpha, bias = torch.tensor([0.7], device="cuda"), torch.randn(N, generator=g, device="cuda") * 1e4
+    for kw in (dict(), dict(alpha=alpha), dict(bias=bias), dict(alpha=alpha, bias=bias)):
+        y32, _ = placed(M, N, F32, 0)
+        moe.moe_linear_mx(*args, y32, x_elem=elem, **kw)
+        assert bool(torch.isfinite(y32).all())
+        for dtype, offset, acc in ((F32, 1, False), (F32, 0, True), (F32, 3, True), (BF16, 0, False), (BF16, 1, False),
+                                   (BF16, 2, False), (BF16, 4, False), (BF16, 0, True), (BF16, 1, True)):
+            y, check = placed(M, N, dtype, offset)
+            if acc:
+                y.zero_()
+            moe.moe_linear_mx(*args, y, x_elem=elem, accumulate=acc, **kw)
+            torch.cuda.synchronize()
+            check()
+            assert torch.equal(y, y32.to(dtype)), (list(kw), dtype, offset, acc)
