@@ -580,7 +580,8 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
 def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumulate=False, stream=None):
     """y = alpha * x w^T + bias (+ y) of MX operands: x E4M3 [M, K] (x_elem 0)
     or packed E2M1 [M, K/2] (1) with E8M0 x_sf [M, K/32]; w packed E2M1
-    [N, K/2] with w_sf [N, K/32]; y bf16 or fp32 [M, N]."""
+    [N, K/2] with w_sf [N, K/32]; y bf16 or fp32 [M, N].  Sums are fp32; E4M3
+    products keep 13 bits below the largest of 8 neighbours (see moe.h)."""
     f = "moe_linear_mx"
     M, N, K = x.shape[0], w.shape[0], 2 * w.shape[-1]
     dev = x.get_device()

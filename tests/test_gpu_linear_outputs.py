@@ -110,3 +110,30 @@ def test_one_sum_whatever_becomes_of_it(M, N, K, elem):
             torch.cuda.synchronize()
             check()
             assert torch.equal(y, y32.to(dtype)), (list(kw), dtype, offset, acc)
+
+
+@pytest.mark.parametrize("M", [16, 300, 3000])
+@pytest.mark.parametrize("elem", [0, 1])
+def test_bits_of_a_product_that_count(M, elem):
+    """What the header says of the products beside a large one: E4M3 ones count
+    down to 2^-13 of it in its group of 8 consecutive k, and to fp32's last bit
+    in others; E2M1 ones all."""
+    say(f"product bits M={M} elem={elem}")
+    N, K = 1024, 1056
+    code = {0: {256.0: 0x78, 2.0 ** -5: 0x10, 2.0 ** -9: 0x01}, 1: {4.0: 6, 0.5: 1}}[elem]
+    big, small, least = (256.0, 2.0 ** -5, 2.0 ** -9) if elem == 0 else (4.0, 0.5, 0.5)
+    x = torch.zeros(M, K, dtype=torch.uint8)
+    want = torch.zeros(M)
+    for m in range(M):
+        i = (37 * m) % K                       # the large one
+        j = i - i % 8 + (i + 1 + m % 7) % 8    # in its group
+        far = (i + 8 * (1 + m // 8 % 100)) % K # in another
+        x[m, i], x[m, j], x[m, far] = code[big], code[small], code[least]
+        want[m] = big + small + least
+    if elem == 1:
+        x = x[:, 0::2] | (x[:, 1::2] << 4)
+    w = torch.full((N, K // 2), 0x22, dtype=torch.uint8, device="cuda")  # 1 everywhere
+    one = lambda n: torch.full((n, K // 32), 127, dtype=torch.uint8, device="cuda")  # noqa: E731
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear_mx(x.cuda(), one(M), w, one(N), y, x_elem=elem)
+    assert torch.equal(y, want.cuda()[:, None].expand(M, N))
