@@ -250,9 +250,9 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
     }
     return;
   }
-  // columns of a piece that the rows of y are aligned to
+  // columns of a piece that the rows of y are aligned to, of less than 16 bytes
   const int align = (int)(((uint32_t)a.N * 2u) | (uint32_t)(uintptr_t)a.y);
-  const int width = (align & 15) == 0 ? 8 : (align & 7) == 0 ? 4 : (align & 3) == 0 ? 2 : 1;
+  const int width = (align & 7) == 0 ? 4 : (align & 3) == 0 ? 2 : 1;
   constexpr int ROWS = OUT / 64;
   uint16_t* y = reinterpret_cast<uint16_t*>(a.y);
 #pragma unroll
@@ -302,7 +302,7 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
             if (row0 + rr < a.M && col < a.N) *reinterpret_cast<Piece*>(y + (row0 + rr) * a.N + col) = v;
           }
         };
-        if (WIDE || width == 8) rows_of(std::integral_constant<int, 8>{});
+        if constexpr (WIDE) rows_of(std::integral_constant<int, 8>{});
         else if (width == 4) rows_of(std::integral_constant<int, 4>{});
         else if (width == 2) rows_of(std::integral_constant<int, 2>{});
         else rows_of(std::integral_constant<int, 1>{});

@@ -160,12 +160,13 @@ __global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormPa
   }
 }
 
-template <int T, int VPT>
+// MANY: rows past the caches' size can come here
+template <int T, int VPT, bool MANY = true>
 hipError_t launch_norm(const NormParams& p, hipStream_t s) {
   constexpr int ROWS = T < 128 ? 256 / T : 1;
   const int64_t blocks = (p.M + ROWS - 1) / ROWS;
   const unsigned grid = (unsigned)(blocks < 1 << 20 ? blocks : 1 << 20);
-  if (p.past_caches) rmsnorm_kernel<T, VPT, true><<<grid, T < 128 ? 256 : T, 0, s>>>(p);
+  if (MANY && p.past_caches) rmsnorm_kernel<T, VPT, MANY><<<grid, T < 128 ? 256 : T, 0, s>>>(p);
   else rmsnorm_kernel<T, VPT, false><<<grid, T < 128 ? 256 : T, 0, s>>>(p);
   return hipGetLastError();
 }
@@ -309,7 +310,7 @@ hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
     if (nv <= 768) return launch_norm<256, 3>(p, s);
     if (nv <= 1024) return launch_norm<256, 4>(p, s);
   }
-  if (nv <= 1024) return launch_norm<1024, 1>(p, s);
+  if (nv <= 1024) return launch_norm<1024, 1, false>(p, s);  // (fewer than 1024 rows of at most 8192 values)
   return launch_norm<1024, 2>(p, s);
 }
 

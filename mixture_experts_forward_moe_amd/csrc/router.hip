@@ -904,21 +904,27 @@ hipError_t launch_v(const RouterParams& p, hipStream_t s) {
   const bool stats = p.prob_partial != nullptr;
   const unsigned grid = stats ? (unsigned)router_partials(p.M) : token_blocks(p.M);
   const int threads = threads_of(stats);
-  if constexpr (V == 64) {
-    if (p.select && stats) {
+  if (p.select && stats) {
+    if constexpr (V == 64) {  // (both at once do not fit the registers: one after the other)
       RouterParams q = p;
       q.prob_partial = nullptr;
       const hipError_t e = launch_v<V>(q, s);
       if (e != hipSuccess) return e;
-      router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
-      return hipGetLastError();
+      q = p;
+      q.select = 0;
+      return launch_v<V>(q, s);
+    } else if (p.select_bias) {
+      router_kernel<V, true, true, true><<<grid, threads, 0, s>>>(p, vec);
+    } else {
+      router_kernel<V, true, false, true><<<grid, threads, 0, s>>>(p, vec);
     }
+  } else if (stats) {
+    router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
+  } else if (p.select_bias) {
+    router_kernel<V, true, true, false><<<grid, threads, 0, s>>>(p, vec);
+  } else {
+    router_kernel<V, true, false, false><<<grid, threads, 0, s>>>(p, vec);
   }
-  if (!p.select) router_kernel<V, false, false, true><<<grid, threads, 0, s>>>(p, vec);
-  else if (p.select_bias && stats) router_kernel<V, true, true, true><<<grid, threads, 0, s>>>(p, vec);
-  else if (p.select_bias) router_kernel<V, true, true, false><<<grid, threads, 0, s>>>(p, vec);
-  else if (stats) router_kernel<V, true, false, true><<<grid, threads, 0, s>>>(p, vec);
-  else router_kernel<V, true, false, false><<<grid, threads, 0, s>>>(p, vec);
   return hipGetLastError();
 }
 
