@@ -17,6 +17,7 @@
 // workgroup: it is bound by what L2 gives to LDS) and a persistent one (whole
 // rounds of large tiles: it is bound by the matrix cores, whose operands'
 // reads and loads share the LDS).  Figures stand at launch().
+#include <atomic>
 #include <type_traits>
 
 #include "device_common.h"
@@ -55,28 +56,22 @@ DEV void dma16(const uint8_t* g, uint8_t* base) {
 }
 
 // Allows a kernel more than the default dynamic LDS, once per device, and
-// gives the device's number of compute units.
+// gives the device's number of compute units.  Calls of several threads may
+// come here at once: one word says that it has been done, and is the number.
 template <auto KERN>
 hipError_t allow_lds(int bytes, int* cus) {
-  static bool attr[64] = {};
-  static int count[64] = {};
+  static std::atomic<int> count[64] = {};  // 0: not yet
   int dev = 0;
   hipError_t err = hipGetDevice(&dev);
   if (err != hipSuccess) return err;
   const bool known = dev >= 0 && dev < 64;
-  if (!known || !attr[dev]) {
-    err = hipFuncSetAttribute((const void*)KERN, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (err != hipSuccess) return err;
-    err = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
-    if (err != hipSuccess) return err;
-    if (known) {
-      count[dev] = *cus;
-      attr[dev] = true;
-    }
-    return hipSuccess;
-  }
-  *cus = count[dev];
-  return hipSuccess;
+  *cus = known ? count[dev].load(std::memory_order_acquire) : 0;
+  if (*cus > 0) return hipSuccess;
+  err = hipFuncSetAttribute((const void*)KERN, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err != hipSuccess) return err;
+  err = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (err == hipSuccess && known) count[dev].store(*cus, std::memory_order_release);
+  return err;
 }
 
 // ------------------------------------------------------------- tiled kernel
