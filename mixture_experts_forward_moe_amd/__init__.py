@@ -423,10 +423,20 @@ def _rows(where, name, t, shape, kind, dev):
     _refuse(where, name, t, shape, kind, True)
 
 
+def _shapes(where, **given):
+    """What a call says whose sizes could not be taken from these tensors."""
+    for name, t in given.items():
+        if t is None or t.dim() != 2:
+            what = "is required" if t is None else f"must have two dimensions, has {t.dim()}"
+            raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} {what}")
+
+
 def _dtype(where: str, name: str, t) -> int:
     """moe_dtype_t of a floating tensor (bf16 also as 16-bit integers)."""
     if not _F32:
         _kinds()
+    if t is None:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} is required")
     if t.dtype in _F32:
         return DTYPE_F32
     if t.dtype in _BF16:
@@ -466,7 +476,11 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
     and y's MX codes, in one pass (see moe_rmsnorm in moe.h).  x, residual
     bf16 [M, H], rows may be strided; weight bf16 or fp32 [H]."""
     w = "moe_rmsnorm"
-    M, H = shape = x.shape
+    try:
+        M, H = shape = x.shape
+    except (AttributeError, ValueError):
+        _shapes(w, x=x)
+        raise
     dev = x.get_device()
     wd = _dtype(w, "weight", weight)
     xp, xs = _rows(w, "x", x, shape, _BF16, dev)
@@ -487,7 +501,11 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     """Gradients of moe_rmsnorm's rows and weight.  A workspace (only with
     dweight) is taken from `workspace`, or allocated here when None."""
     w = "moe_rmsnorm_backward"
-    M, H = shape = dy.shape
+    try:
+        M, H = shape = dy.shape
+    except (AttributeError, ValueError):
+        _shapes(w, dy=dy)
+        raise
     dev = dy.get_device()
     wd = _dtype(w, "weight", weight)
     args = (_arg(w, "dy", dy, shape, _BF16, dev), _arg(w, "h", h, shape, _BF16, dev),
@@ -520,8 +538,11 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
     mean_probs, prob_grad and loss (all four) also the balance loss of that
     choice, from the same reading of the logits."""
     w = "moe_router_topk"
-    M, E = logits.shape
-    k = topk_ids.shape[-1]
+    try:
+        (M, E), (_, k) = logits.shape, topk_ids.shape
+    except (AttributeError, ValueError):
+        _shapes(w, logits=logits, topk_ids=topk_ids)
+        raise
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
@@ -543,8 +564,11 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     """Per-expert counts, mean probabilities and the load-balancing loss of
     given expert ids, and the loss's gradient in the probabilities."""
     w = "moe_balance_loss"
-    M, E = logits.shape
-    k = topk_ids.shape[-1]
+    try:
+        (M, E), (_, k) = logits.shape, topk_ids.shape
+    except (AttributeError, ValueError):
+        _shapes(w, logits=logits, topk_ids=topk_ids)
+        raise
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
@@ -561,8 +585,11 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
     """The gradient of the logits, in their type, from that of the routing
     weights and / or of the balance loss (a device scalar; None: 1)."""
     w = "moe_router_backward"
-    M, E = logits.shape
-    k = topk_ids.shape[-1]
+    try:
+        (M, E), (_, k) = logits.shape, topk_ids.shape
+    except (AttributeError, ValueError):
+        _shapes(w, logits=logits, topk_ids=topk_ids)
+        raise
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     if _dtype(w, "d_logits", d_logits) != d:
@@ -583,7 +610,12 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
     [N, K/2] with w_sf [N, K/32]; y bf16 or fp32 [M, N].  Sums are fp32; E4M3
     products keep 13 bits below the largest of 8 neighbours (see moe.h)."""
     f = "moe_linear_mx"
-    M, N, K = x.shape[0], w.shape[0], 2 * w.shape[-1]
+    try:
+        (M, _), (N, K) = x.shape, w.shape
+    except (AttributeError, ValueError):
+        _shapes(f, x=x, w=w)
+        raise
+    K *= 2
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_mx(
