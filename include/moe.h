@@ -468,7 +468,8 @@ typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F32 = 1 } moe_dtype_t;
 /* moe_rmsnorm: the layer's input for the experts.  For every row of M rows
  * of H values
  *   h = bf16(x + residual)           (h = x without a residual)
- *   r = 1 / sqrt(mean(h^2) + eps)    (fp32; 0 where the sum of squares overflows)
+ *   r = 1 / sqrt(mean(h^2) + eps)    (fp32; 0, and y 0, where the sum of squares
+ *                                     overflows; inf for a row of zeros with eps 0)
  *   y = bf16(h * r * weight)
  *   q, q_sf = the MX quantisation of that bf16 y, bit for bit what
  *             moe_quantize_mx(y, M, H, elem) gives

@@ -144,7 +144,8 @@ __global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormPa
       unpack8(h[i], f);
       load_weight8(a.weight, a.weight_f32, 8 * v, w);
 #pragma unroll
-      for (int j = 0; j < 8; j++) f[j] = f[j] * w[j] * r;  // (h w is exact for a bf16 weight)
+      for (int j = 0; j < 8; j++)
+        f[j] = r > 0.0f ? f[j] * w[j] * r : f[j] * r;  // (h w is exact for a bf16 weight, or past fp32 where r is 0)
       const u32x4_t y = pack8(f);
       if (a.y) put16<PAST>(a.y + row * a.H + 8 * v, y);
       if (a.q) {
