@@ -596,7 +596,7 @@ moe_status_t moe_router_backward(const void* logits, moe_dtype_t logits_dtype, i
                                  const float* prob_grad, const float* d_loss, void* d_logits, moe_stream_t stream);
 
 /* moe_linear_mx: the product of the MX formats without a routing plan, for
- * the layers that every token takes (a shared expert, a dense layer):
+ * what every token takes (a projection of a shared expert or a dense layer):
  *   y[m, n] = alpha * sum_k x[m, k] w[n, k] + bias[n]   (+ y[m, n] when accumulating)
  * x_elem 0: x E4M3 [M, K]; 1: packed E2M1 [M, K/2]; x_sf E8M0 [M, K/32] (the
  * outputs of moe_rmsnorm or moe_quantize_mx); w packed E2M1 [N, K/2], w_sf

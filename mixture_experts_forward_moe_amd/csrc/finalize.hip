@@ -168,8 +168,9 @@ hipError_t launch_quantize_nvfp4(const uint16_t* x, int64_t batches, int64_t row
 }
 
 // Eight values a thread, a quad of lanes a 32-element block: neighbouring lanes
-// read and write neighbouring bytes (16384 x 4096 to E2M1: 30 us
-// against 52 with a whole block a thread, whose loads lie 64 bytes apart).
+// read and write neighbouring bytes (16384 x 4096 to E2M1: 33 us in a row of
+// launches, 48 on average between others, whose inputs the caches have dropped;
+// 52 in a row with a whole block a thread, whose loads lie 64 bytes apart).
 __global__ __launch_bounds__(256) void quantize_mx_kernel(const uint16_t* __restrict__ x, int elem,
                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ sf,
                                                           int64_t total) {

@@ -14,7 +14,8 @@
 //
 // Three kernels, in order of size: a streaming one (a row of 16 x 16 tiles: it
 // is bound by latency and by the bytes of W), a tiled one (one tile a
-// workgroup: it is bound by what L2 gives to LDS) and a persistent one (whole
+// workgroup: it is bound by its stages' trips from L2 to LDS, of which one or two
+// are under way at a time) and a persistent one (whole
 // rounds of large tiles: it is bound by the matrix cores, whose operands'
 // reads and loads share the LDS).  Figures stand at launch().
 #include <atomic>
@@ -314,8 +315,11 @@ DEV void store_tiles(const LinearParams& a, const f32x16_t (&acc)[TN][TM], int64
 // fragments of the next one are read, so a barrier a stage is all that the
 // ring costs.  KG groups of four wavefronts split K where there are few tiles,
 // each with a ring of its own; their sums meet in LDS in a fixed order.  Bound
-// by L2 -> LDS: 512 x 4096 x 4096 moves 134 MB, E4M3 in 13.4 us (1.28
-// PFLOP/s), E2M1 in 11.0 (1.56).
+// by the stages' trips: with two buffers one stage is on its way while the other
+// multiplies.  512 x 4096 x 4096 E4M3 in 14.1 us (1.22 PFLOP/s): eight steps of
+// 64 KiB a CU at 1.27 us (the slope up to K = 16384), 13 TB/s of the 27 above,
+// where the matrix cores need 0.5, and 4 us of start, join and way out.  E2M1 in
+// 11.8 us (1.46): 16 steps of 32 KiB at 0.57, 15 TB/s, and 2.7 us.
 template <int XE, bool WIDE, int TM, int TN, int KS, int NBUF, int KG, int PER_CU>
 __global__ __launch_bounds__(256 * KG, PER_CU * KG) void linear_tile_kernel(const LinearParams a, int tiles_m,
                                                                             int tiles_n) {
@@ -610,9 +614,9 @@ hipError_t launch_tile(const LinearParams& p, hipStream_t s) {
 // while the last ones of this tile multiply, so that only the first tile waits
 // for memory.  A stage of 256 K is 2048 cycles of matrix cores for E2M1, and
 // 196 KiB of fragment reads and 64 KiB of loads in LDS, another 2048 cycles if
-// nothing overlapped.  16384 x 6144 x 4096: E2M1 203 - 222 us (3.7 - 4.1
-// PFLOP/s, the matrix cores 47% busy at 2.0 GHz), E4M3 320 - 360 us (2.3 - 2.6,
-// by the card).  Wave priorities and other orders of the reads: the same.  At 8192 x
+// nothing overlapped.  16384 x 6144 x 4096: E2M1 207 us at best, 220 - 250 from
+// launch to launch (3.3 - 4.0 PFLOP/s, the matrix cores 47% busy at 2.0 GHz), E4M3
+// 333 - 374 us (2.2 - 2.5).  Wave priorities and other orders of the reads: the same.  At 8192 x
 // 8192 x 8192 E2M1, 264 us: without the loads 221, without the fragment reads
 // 223, the instructions alone 176.
 template <int XE>
@@ -935,10 +939,11 @@ hipError_t launch_big(const LinearParams& p, hipStream_t s) {
 
 // 16 rows of x a workgroup (decoding): it streams 16 rows of W once, its
 // wavefronts splitting K, straight into registers; their sums meet in LDS in
-// a fixed order.  8 x 4096 x 6144 E2M1: 7.0 us for 13.4 MB of W, of which a
-// kernel's start and end and two trips to memory are most; eight wavefronts
-// and six steps at a time have the whole of W in flight.  v_mfma_scale_f32_16x16x128_f8f6f4: lane (row or column r =
-// lane & 15, group q = lane >> 4) holds block q of each 128 values of an E2M1
+// a fixed order.  8 x 4096 x 6144 E2M1: 6.8 - 7.0 us for 13.4 MB of W, of which 2.1
+// are a kernel's start and end; the rest goes at the 2.8 TB/s (4.7 us) that one
+// workgroup a CU asks for, whose eight wavefronts have six steps each under way
+// (K = 24576: 21.0 us).  v_mfma_scale_f32_16x16x128_f8f6f4: lane (row or column r
+// = lane & 15, group q = lane >> 4) holds block q of each 128 values of an E2M1
 // row (16 bytes), or of an E4M3 row its halves 16 q .. and 64 + 16 q .., and
 // block q's scale.
 constexpr int STREAM_WAVES = 8;
@@ -1039,8 +1044,13 @@ hipError_t launch(const LinearParams& p, hipStream_t s) {
   if (tiles(64, 64) <= CUS)
     return p.K >= 2048 ? launch_tile<XE, 1, 1, 128, 4, 2, 1>(p, s) : launch_tile<XE, 1, 1, 256, 2, 1, 2>(p, s);
   const int64_t t128 = tiles(128, 128);
-  // K split in two goes by the shape alone, whatever becomes of the sums: its
-  // split is in their order.
+  // K split in two goes by the shape alone, whatever becomes of the sums: it is
+  // in their order.  Sums that leave as fp32, onto y or in narrower pieces have 64 x
+  // 128 tiles at every size, whose bound is the trips of the stages and, where rows
+  // are not whole 16 bytes, single elements (16384 x 6144 x 4096, E2M1 / E4M3: fp32
+  // 448 / 540 us, accumulated bf16 438 / 511, accumulated fp32 534 / 621, N = 6147
+  // 424 / 513 and accumulated 794 / 857, against 250 / 355 for aligned bf16 in
+  // the same run; 2048 x 4096 x 2048 fp32 27 / 31 against 16 / 22).
   const bool halves = XE == 0 && t128 <= CUS / 2 && p.K >= 2048;
   if (!wide_rows(p)) {
     if constexpr (XE == 0)

@@ -86,7 +86,7 @@ DEV void load_weight8(const void* w, int f32, int c, float (&f)[8]) {
 }
 
 // T threads a row (64: four rows a workgroup), up to VPT vectors a thread.
-// 65536 x 6144 with the residual and E4M3 codes: 3.64 GB in 580 - 623 us, 5.8 - 6.2
+// 65536 x 6144 with the residual and E4M3 codes: 3.64 GB in 594 - 630 us, 5.8 - 6.1
 // TB/s (a large copy reaches 4.7).
 template <int T, int VPT, bool PAST>
 __global__ __launch_bounds__(T < 128 ? 256 : T) void rmsnorm_kernel(const NormParams a) {
@@ -176,7 +176,7 @@ hipError_t launch_norm(const NormParams& p, hipStream_t s) {
 // keeping its columns' sums of dy h r in registers: the weight gradient costs
 // one [P, H] array of partial sums instead of a second pass over the rows.
 // The next row's loads go out before this row's sum is joined.  8191 x 4128 with
-// dh: 270 MB in 55 us, 4.9 TB/s; the join of the partials takes 4 us, a launch.
+// dh: 270 MB in 53 - 56 us, 4.8 - 5.1 TB/s; the join of the partials takes 4 us, a launch.
 template <int T, int VPT, bool PAST>
 __global__ __launch_bounds__(T) void rmsnorm_backward_kernel(const NormBackwardParams a) {
   __shared__ float red[2][T > 64 ? T / 64 : 1];
@@ -301,8 +301,13 @@ int norm_backward_partials(int64_t M, int H) {
 
 hipError_t launch_rmsnorm(const NormParams& p, hipStream_t s) {
   const int nv = p.H / 8;
-  // (H = 6144: 65536 rows take 637 us in 256 threads x 3 vectors, 976 us in a
-  // wavefront each with 12; 64 rows 4.0 us in 1024 threads, 4.8 us in 256)
+  // Many rows: 256 threads each, so that a CU has several rows under way; few: as
+  // many threads as vectors, for the shortest chain.  (256 threads against 1024,
+  // us.  H = 6144: 64 rows 4.5, 3.7; 512 7.9, 7.4; 1024 11.7, 12.5; 4096 47, 46.
+  // H = 8192: 512 10.0, 9.0; 1024 15.7, 15.2; 2048 32.5, 33.3.  Shorter rows, which
+  // leave half of the 1024 threads without work, meet earlier: H = 4096 256 rows
+  // 4.4, 4.2; 512 5.3, 6.4; 1024 9.3, 10.2; H = 2080 256 3.9, 3.9; 512 4.4, 5.6; 1024 6.5,
+  // 9.1.  65536 x 6144 in a wavefront a row with 12 vectors: 976, against 637.)
   if (nv <= 64) return launch_norm<64, 1>(p, s);
   if (nv <= 128) return launch_norm<128, 1>(p, s);
   if (nv <= 256) return launch_norm<256, 1>(p, s);

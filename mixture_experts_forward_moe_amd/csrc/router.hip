@@ -23,12 +23,21 @@
 // fp64 for a token any two of whose candidates are closer than the error of
 // that.
 //
-// Bound: up to some thousand tokens by latency (8 tokens of 256 experts: 4.9 us,
+// Bound: up to some thousand tokens by latency (8 tokens of 256 experts: 4.7 us,
 // a kernel of that length has a launch, one trip to memory and the chain of
-// the choice); from there on by instructions, 680 a wavefront of four
-// tokens.  65536 x 256 fp32: choice 22.5 us (71 MB, 3.1 TB/s), gradient 40 us
-// (138 MB, 3.5 TB/s).  16384 x 256: choice 8.5 us, with the loss 20 us, of which
-// the join is 7; gradient 14 us.
+// the choice).  From there on the choice without a bias by instructions, 640 a
+// wavefront of four tokens (65536 x 256: 22.3 us fp32, 71 MB, 3.2 TB/s; 21 - 22
+// bf16).  The others wait for memory as well:
+// - with a bias (38 - 41 us; 8 tokens 6.4 - 6.7) a lane's biases are asked for
+//   once the logits have come, and the chosen logits are read again;
+// - with the loss (39 us; 16384 x 256: 19.6, of which the join is 7) the join
+//   takes 16 bytes of each line, and reads every line eight times;
+// - the gradient (39 us fp32, 138 MB, 3.5 TB/s; 32 bf16; 16384 x 256: 14.2, of the
+//   weights alone 8.8) loads a lane's values of prob_grad one after another
+//   before its first token, and its ids before their logits;
+// - bf16 rows, and rows that are not whole groups of four, wait for each group
+//   of 64 logits before they ask for the next.
+// Equal logits, of which every one is a candidate, go by rounds: 111 us.
 #include <algorithm>
 #include <cfloat>
 #include <type_traits>
