@@ -219,3 +219,26 @@ def test_scores_below_the_normal_range():
         for k in (1, 2):
             ids, _ = topk(l.cuda(), k, score=1, select_bias=bias.cuda())
             assert torch.equal(ids.cpu(), ref.router_topk(l, k, 1, True, bias)[0])
+
+
+@pytest.mark.parametrize("E,k", [(5, 5), (60, 16), (300, 40), (1000, 64)])
+def test_equal_ids_add_up_in_one_order(E, k):
+    """Many places of a token with the same expert: the same bits wherever the
+    token stands and on every run."""
+    say(f"equal ids E={E} k={k}")
+    g = torch.Generator(device="cuda").manual_seed(E)
+    M = 1003
+    l = torch.randn(1, E, generator=g, device="cuda").expand(M, E).contiguous()
+    ids = torch.randint(0, 3, (1, k), generator=g, device="cuda", dtype=torch.int32).expand(M, k).contiguous()
+    dw = torch.randn(1, k, generator=g, device="cuda") * 10 ** torch.randn(1, k, generator=g, device="cuda")
+    dw = dw.expand(M, k).contiguous()
+    for score in (0, 1):
+        for renorm in (True, False):
+            kw = dict(score=score, renormalize=renorm)
+            d = gradient(l, ids, dw, None, **kw)
+            assert torch.equal(d, d[:1].expand(M, E))
+            for _ in range(5):
+                assert torch.equal(gradient(l, ids, dw, None, **kw), d)
+            want, size = ref.router_backward(l[:1].cpu(), ids[:1].cpu(), score, renorm, dw[:1].cpu())
+            # (a place more is a rounding more: k of them on top of the weights')
+            assert bool(((d[:1].cpu().double() - want).abs() <= size * (k + 100) * ref.U24 + 1e-37).all())
