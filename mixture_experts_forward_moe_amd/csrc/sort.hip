@@ -238,8 +238,12 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_single_kernel(SortArgs a) {
   int le[PER];
   int id[PER];
 #pragma unroll
-  for (int c = 0; c < PER; c++)  // all loads in flight at once (routes past R re-read route 0)
-    id[c] = a.ids[(c * SORT_THREADS + (int)threadIdx.x < a.R) ? c * SORT_THREADS + threadIdx.x : 0];
+  for (int c = 0; c < PER; c++) id[c] = -1;
+  if (a.R > 0) {  // (an empty batch has no ids to read)
+#pragma unroll
+    for (int c = 0; c < PER; c++)  // all loads in flight at once (routes past R re-read route 0)
+      id[c] = a.ids[(c * SORT_THREADS + (int)threadIdx.x < a.R) ? c * SORT_THREADS + threadIdx.x : 0];
+  }
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int c = 0; c < PER; c++) {
