@@ -619,6 +619,144 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
                            const float* alpha, const float* bias, int M, int N, int K, int accumulate, void* y,
                            moe_dtype_t y_dtype, moe_stream_t stream);
 
+/* ---- Rows in 8 bits: training and serving the experts in E4M3 --------- */
+
+/* The formats of the calls below.
+ *  rows    : E4M3 codes q [rows, cols] and q_sf E8M0 [rows, ceil(cols / 128)], a
+ *            power of two for each 128 values of a row (the last block may be
+ *            shorter): the least one, 2^-126 at least, that brings the block's
+ *            largest finite |value| to 448 or less.  codes = value / scale,
+ *            rounded to nearest even, from bf16.  An infinity or a NaN becomes a
+ *            NaN code.  (Values within 1/64 of the largest finite bf16 decode to
+ *            infinity.)
+ *  weights : E4M3 codes [N, K] and an fp32 scale for each block of 128 x 128,
+ *            [ceil(N / 128), ceil(K / 128)]; the scales may be any finite value.
+ * Rows in a plan's order are [route_slots, ..]; padding slots are neither read
+ * nor written by any of the calls. */
+
+/* Row quantisation of bf16 x [rows, cols], row stride in elements (0 =
+ * contiguous; shorter than cols: MOE_ERR_INVALID_ARGUMENT).  cols a multiple of
+ * 16, row strides of 8, x and q 16-byte aligned, rows * ceil(cols / 2048) at most
+ * 2^25 (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t x_row_stride, int64_t rows, int cols, uint8_t* q,
+                              uint8_t* q_sf, moe_stream_t stream);
+
+/* Weight quantisation of bf16 w [batches, N, K]: scale = (largest finite |value| of
+ * the block) / 448, 2^-126 at least, and codes E4M3(value / scale), each an fp32
+ * quotient; infinities and NaN become NaN codes.  q [batches, N, K], sf
+ * [batches, ceil(N / 128), ceil(K / 128)].  qt and sft (both or neither): the same
+ * codes and scales transposed, [batches, K, N] and [batches, ceil(K / 128),
+ * ceil(N / 128)], the weights of the gradient of a product's rows.  K a multiple of
+ * 8, with qt N too; w 16-byte, q and qt 8-byte aligned; blocks at most 2^23 (else
+ * MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_quantize_fp8_weight(const uint16_t* w, int batches, int N, int K, uint8_t* q, float* sf, uint8_t* qt,
+                                     float* sft, moe_stream_t stream);
+
+/* moe_dispatch: each token's row at the slots of its routes: for every local
+ * route r = t * top_k + j with slot s
+ *   rows[s] = x[t]  (bf16 [route_slots, H]; NULL: not stored)
+ *   q[s], q_sf[s] = the row quantisation of x[t]  (both or neither)
+ * At least one of rows and q.  x bf16 [M, H], row stride as in
+ * moe_quantize_fp8, a token's row read once.  H a multiple of 16, at most 16384;
+ * x, rows and q 16-byte aligned; M at most 2^22 (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_dispatch(const uint16_t* x, int64_t x_row_stride, const moe_plan_t* plan, int H, uint16_t* rows,
+                          uint8_t* q, uint8_t* q_sf, moe_stream_t stream);
+
+/* moe_dispatch_backward: the gradient of x from that of the dispatched rows:
+ *   dx[t] = bf16((accumulate ? dx[t] : 0) + sum of d_rows[s] over t's local routes)
+ * in fp32, in route order.  d_rows bf16 [route_slots, H], dx bf16 [M, H].  A token
+ * without a local route gets 0 (or keeps its value).  Limits as in moe_dispatch. */
+moe_status_t moe_dispatch_backward(const uint16_t* d_rows, const moe_plan_t* plan, int H, int accumulate, uint16_t* dx,
+                                   moe_stream_t stream);
+
+/* moe_finalize_backward: the gradients of moe_finalize's rows and routing weights
+ * from that of its output, dout bf16 [M, H].  For every local route r of token t
+ * with slot s
+ *   dy2[s] = bf16(fp32(topk_weights[r] * routed_scaling_factor) * dout[t])
+ *   q[s], q_sf[s] = the row quantisation of that bf16 row
+ *   d_topk_weights[r] = routed_scaling_factor * sum_h dout[t, h] y2[s, h]   (fp32)
+ * and d_topk_weights[r] = 0 for a route that is not local.  dy2 bf16
+ * [route_slots, H]; NULL: not stored; q and q_sf both or neither; y2 bf16
+ * [route_slots, H] only with d_topk_weights fp32 [M, top_k] (both or neither); at
+ * least one output.  dy2 may be y2.  The sums' order is fixed: reproducible bit for
+ * bit.  Limits as in moe_dispatch. */
+moe_status_t moe_finalize_backward(const uint16_t* dout, const uint16_t* y2, const moe_plan_t* plan,
+                                   const float* topk_weights, int H, float routed_scaling_factor, uint16_t* dy2,
+                                   uint8_t* q, uint8_t* q_sf, float* d_topk_weights, moe_stream_t stream);
+
+/* moe_linear_fp8: the product of quantised rows with quantised weights,
+ *   y[m, n] = sum_k x[m, k] w[n, k] + bias[n]   (+ y[m, n] when accumulating)
+ * x E4M3 [M, K] with x_sf, w E4M3 [N, K] with w_sf; bias fp32 [N] (NULL: none); y
+ * bf16 or fp32 [M, N] by y_dtype.  The gradient of the rows is the same call on the
+ * transposed weights of moe_quantize_fp8_weight.  Each 128 of K is one fp32 sum,
+ * which w's scale joins to the next in one fused multiply-add.  Inside it the matrix
+ * instruction adds up each group of 8 consecutive values first, and keeps of a
+ * product the bits down to 2^-13 of the power of two of the group's largest one:
+ * off by up to 8 * 2^-13 of that product, in an fp32 y too.  bias and accumulation
+ * are one fp32 addition each, y is rounded once.  M, N >= 0; K positive.
+ * K a multiple of 16, at most 2^20; x and w 16-byte aligned, y aligned to its
+ * elements; M and N at most 2^26, M * N at most 2^36 (else MOE_ERR_UNSUPPORTED).
+ * Each output is one sum in an order that depends on M, N and K alone: reproducible
+ * bit for bit. */
+moe_status_t moe_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const uint8_t* w, const float* w_sf,
+                            const float* bias, int M, int N, int K, int accumulate, void* y, moe_dtype_t y_dtype,
+                            moe_stream_t stream);
+
+/* moe_grouped_linear_fp8: the same of every expert: for every valid slot s of local
+ * expert e, y[s] = bf16(x[s] W_e^T).  x E4M3 [route_slots, K] with x_sf
+ * [route_slots, ceil(K / 128)], w E4M3 [E_l, N, K], w_sf fp32 [E_l, ceil(N / 128),
+ * ceil(K / 128)], y bf16 [route_slots, N], 16-byte aligned.  N a multiple of 8;
+ * otherwise the limits of moe_linear_fp8, with N and K at most 2^16.  The tile that
+ * moe_default_tile gives for MOE_QUANT_MXFP8_MXFP4 suits it.  The sums' order depends
+ * on the plan's tile, N and K alone. */
+moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const moe_plan_t* plan, const uint8_t* w,
+                                    const float* w_sf, int N, int K, uint16_t* y, moe_stream_t stream);
+
+/* moe_linear_fp8_wgrad: the gradient of a product's weights from its rows, kept in 8
+ * bits by the forward pass:
+ *   dw[n, k] = sum_m dy[m, n] x[m, k]   (+ dw[n, k] when accumulating)
+ * dy bf16 [M, N]; x E4M3 [M, K] with x_sf; dw fp32 [N, K].  x is decoded exactly, the
+ * products are exact and the sums fp32, in an order that depends on the shape alone.
+ * M = 0: zeros.  N a multiple of 8, K of 16; dy, x and dw 16-byte aligned; M at most
+ * 2^26, N and K at most 2^16 (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf, int M, int N, int K,
+                                  int accumulate, float* dw, moe_stream_t stream);
+
+/* moe_grouped_linear_fp8_wgrad: the same of every expert from the valid slots of its
+ * range: dy bf16 [route_slots, N], x E4M3 [route_slots, K] with x_sf, dw fp32
+ * [E_l, N, K].  An expert without a route gets zeros (or keeps its values). */
+moe_status_t moe_grouped_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf,
+                                          const moe_plan_t* plan, int N, int K, int accumulate, float* dw,
+                                          moe_stream_t stream);
+
+/* moe_gated_act_fp8: a gated activation of rows h = (gate, up), bf16 [rows, 2I], with
+ * its result quantised, and h itself kept in 8 bits for the backward pass:
+ *   y, y_sf = the row quantisation of bf16(f(g) * up(u))   [rows, I]
+ *   hq [rows, 2I], hq_sf [rows, 2 ceil(I / 128)] = that of g and of u, each half in
+ *     blocks of its own (both or neither)
+ * activation (moe_activation_t) as in moe_grouped_gemm1_act: MOE_ACT_SWIGLU,
+ *   f = min(g, limit) sigmoid(swiglu_alpha min(g, limit)), up = clamp(u, -limit, limit) + swiglu_beta
+ * or MOE_ACT_GEGLU_TANH (with the SwiGLU parameters 1, 0, FLT_MAX); the other one:
+ * MOE_ERR_UNSUPPORTED.  With a plan (else NULL) rows must be its route_slots, and its
+ * valid slots are the rows.  I a multiple of 16; h, y and hq 16-byte aligned; rows *
+ * ceil(I / 1024) at most 2^25 (else MOE_ERR_UNSUPPORTED). */
+moe_status_t moe_gated_act_fp8(const uint16_t* h, const moe_plan_t* plan, int64_t rows, int I, int activation,
+                               float swiglu_alpha, float swiglu_beta, float swiglu_limit, uint8_t* y, uint8_t* y_sf,
+                               uint8_t* hq, uint8_t* hq_sf, moe_stream_t stream);
+
+/* moe_gated_act_fp8_backward: the gradient of h, at the kept h, from that of y (the
+ * quantisations pass it straight through):
+ *   dh = bf16(dy * f'(g) * up(u)),  bf16(dy * f(g) * up'(u))   [rows, 2I]
+ *   dq, dq_sf = the row quantisation of those bf16 values, each half in blocks of its
+ *     own: with I a multiple of 128 rows of moe_linear_fp8 with K = 2I
+ * Past the limit f' and up' are 0.  dy bf16 [rows, I]; dh NULL: not stored; dq and
+ * dq_sf both or neither; at least one of dh and dq.  Otherwise as
+ * moe_gated_act_fp8. */
+moe_status_t moe_gated_act_fp8_backward(const uint8_t* hq, const uint8_t* hq_sf, const uint16_t* dy,
+                                        const moe_plan_t* plan, int64_t rows, int I, int activation,
+                                        float swiglu_alpha, float swiglu_beta, float swiglu_limit, uint16_t* dh,
+                                        uint8_t* dq, uint8_t* dq_sf, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -32,6 +32,9 @@ EXPORTS = [
     "moe_workspace_size", "moe_forward_plan", "moe_forward", "moe_forward_noalloc", "moe_fc2_input_scale", "moe_nvfp4_global_scale", "moe_quantize_nvfp4", "moe_quantize_mx",
     "moe_rmsnorm", "moe_rmsnorm_backward_workspace_size", "moe_rmsnorm_backward", "moe_router_topk",
     "moe_balance_workspace_size", "moe_balance_loss", "moe_router_backward", "moe_linear_mx",
+    "moe_quantize_fp8", "moe_quantize_fp8_weight", "moe_dispatch", "moe_dispatch_backward", "moe_finalize_backward",
+    "moe_linear_fp8", "moe_grouped_linear_fp8", "moe_linear_fp8_wgrad", "moe_grouped_linear_fp8_wgrad",
+    "moe_gated_act_fp8", "moe_gated_act_fp8_backward",
 ]
 
 
@@ -105,6 +108,17 @@ def lib() -> ctypes.CDLL:
             "moe_balance_loss": ([P, I, I64, P, P, I, I, I, I, F, P, P, P, P, P, SZ, P], I),
             "moe_router_backward": ([P, I, I64, P, P, I, I, I, I, I, P, P, P, P, P], I),
             "moe_linear_mx": ([P, P, I, P, P, P, P, I, I, I, I, P, I, P], I),
+            "moe_quantize_fp8": ([P, I64, I64, I, P, P, P], I),
+            "moe_quantize_fp8_weight": ([P, I, I, I, P, P, P, P, P], I),
+            "moe_dispatch": ([P, I64, P, I, P, P, P, P], I),
+            "moe_dispatch_backward": ([P, P, I, I, P, P], I),
+            "moe_finalize_backward": ([P, P, P, P, I, F, P, P, P, P, P], I),
+            "moe_linear_fp8": ([P, P, P, P, P, I, I, I, I, P, I, P], I),
+            "moe_grouped_linear_fp8": ([P, P, P, P, P, I, I, P, P], I),
+            "moe_linear_fp8_wgrad": ([P, P, P, I, I, I, I, P, P], I),
+            "moe_grouped_linear_fp8_wgrad": ([P, P, P, P, I, I, I, P, P], I),
+            "moe_gated_act_fp8": ([P, P, I64, I, I, F, F, F, P, P, P, P, P], I),
+            "moe_gated_act_fp8_backward": ([P, P, P, P, I64, I, I, F, F, F, P, P, P, P], I),
         }
         for name, (args, res) in sigs.items():
             fn = getattr(L, name)
@@ -625,3 +639,198 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
         _opt(f, "alpha", alpha, (1,), _F32, dev), _opt(f, "bias", bias, (N,), _F32, dev), M, N, K,
         1 if accumulate else 0, _arg(f, "y", y, (M, N), _F32 if d else _BF16, dev), d,
         _raw_stream(f, dev, stream)), f)
+
+
+# ---- rows in 8 bits: training and serving the experts in E4M3 ---------------
+
+def _nb(cols: int) -> int:
+    return (cols + 127) // 128
+
+
+def _sizes(where, **given):
+    """The two sizes of each tensor, one after another."""
+    try:
+        return [n for t in given.values() for n in _two(t.shape)]
+    except (AttributeError, ValueError):
+        _shapes(where, **given)
+        raise
+
+
+def _two(shape):
+    a, b = shape
+    return a, b
+
+
+def _plan_arg(where, plan, dev):
+    """The plan's C struct, checked to be on the call's device."""
+    if not isinstance(plan, MoePlan):
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: plan must be a MoePlan, is {type(plan).__name__}")
+    if plan.workspace.get_device() != dev:
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: plan must be on the GPU, with the call's other tensors")
+    return ctypes.byref(plan.c)
+
+
+def moe_quantize_fp8(x, q, q_sf, stream=None):
+    """E4M3 codes q [rows, cols] and E8M0 scales q_sf [rows, ceil(cols / 128)]
+    of bf16 rows x, which may be strided."""
+    w = "moe_quantize_fp8"
+    rows, cols = _sizes(w, x=x)
+    dev = x.get_device()
+    xp, xs = _rows(w, "x", x, (rows, cols), _BF16, dev)
+    _check(lib().moe_quantize_fp8(xp, xs, rows, cols, _arg(w, "q", q, (rows, cols), _BYTE, dev),
+                                  _arg(w, "q_sf", q_sf, (rows, _nb(cols)), _BYTE, dev),
+                                  _raw_stream(w, dev, stream)), w)
+
+
+def moe_quantize_fp8_weight(weight, q, sf, qt=None, sft=None, stream=None):
+    """E4M3 codes and fp32 scales for blocks of 128 x 128 of bf16 weights
+    [N, K] or [batches, N, K]; qt and sft the same transposed (for
+    the gradient of a product's rows)."""
+    w = "moe_quantize_fp8_weight"
+    if weight is None or weight.dim() not in (2, 3):
+        raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: weight must have two or three dimensions")
+    lead, (N, K) = tuple(weight.shape[:-2]), weight.shape[-2:]
+    dev = weight.get_device()
+    _check(lib().moe_quantize_fp8_weight(
+        _arg(w, "weight", weight, (*lead, N, K), _BF16, dev), lead[0] if lead else 1, N, K,
+        _arg(w, "q", q, (*lead, N, K), _BYTE, dev), _arg(w, "sf", sf, (*lead, _nb(N), _nb(K)), _F32, dev),
+        _opt(w, "qt", qt, (*lead, K, N), _BYTE, dev), _opt(w, "sft", sft, (*lead, _nb(K), _nb(N)), _F32, dev),
+        _raw_stream(w, dev, stream)), w)
+
+
+def moe_dispatch(x, plan: MoePlan, rows=None, q=None, q_sf=None, stream=None):
+    """Each token's bf16 row x [M, H] (rows may be strided) at the slots of its
+    routes: as bf16 rows [route_slots, H], and / or quantised, q [route_slots,
+    H] with q_sf [route_slots, ceil(H / 128)]."""
+    w = "moe_dispatch"
+    M, H = _sizes(w, x=x)
+    dev = x.get_device()
+    p = _plan_arg(w, plan, dev)
+    n = plan.route_slots
+    xp, xs = _rows(w, "x", x, (plan.M, H), _BF16, dev)
+    _check(lib().moe_dispatch(xp, xs, p, H, _opt(w, "rows", rows, (n, H), _BF16, dev),
+                              _opt(w, "q", q, (n, H), _BYTE, dev), _opt(w, "q_sf", q_sf, (n, _nb(H)), _BYTE, dev),
+                              _raw_stream(w, dev, stream)), w)
+
+
+def moe_dispatch_backward(d_rows, plan: MoePlan, dx, accumulate=False, stream=None):
+    """dx [M, H] = (dx +) the sum of d_rows [route_slots, H] over each token's
+    routes."""
+    w = "moe_dispatch_backward"
+    n, H = _sizes(w, d_rows=d_rows)
+    dev = d_rows.get_device()
+    p = _plan_arg(w, plan, dev)
+    _check(lib().moe_dispatch_backward(_arg(w, "d_rows", d_rows, (plan.route_slots, H), _BF16, dev), p, H,
+                                       1 if accumulate else 0, _arg(w, "dx", dx, (plan.M, H), _BF16, dev),
+                                       _raw_stream(w, dev, stream)), w)
+
+
+def moe_finalize_backward(dout, y2, plan: MoePlan, topk_weights, dy2=None, q=None, q_sf=None, d_topk_weights=None,
+                          routed_scaling_factor=1.0, stream=None):
+    """The gradients of moe_finalize: of its rows (dy2 bf16 [route_slots, H],
+    and / or quantised in q, q_sf) and, with y2, of the routing weights."""
+    w = "moe_finalize_backward"
+    M, H = _sizes(w, dout=dout)
+    dev = dout.get_device()
+    p = _plan_arg(w, plan, dev)
+    n = plan.route_slots
+    _check(lib().moe_finalize_backward(
+        _arg(w, "dout", dout, (plan.M, H), _BF16, dev), _opt(w, "y2", y2, (n, H), _BF16, dev), p,
+        _arg(w, "topk_weights", topk_weights, (plan.M, plan.top_k), _F32, dev), H, routed_scaling_factor,
+        _opt(w, "dy2", dy2, (n, H), _BF16, dev), _opt(w, "q", q, (n, H), _BYTE, dev),
+        _opt(w, "q_sf", q_sf, (n, _nb(H)), _BYTE, dev),
+        _opt(w, "d_topk_weights", d_topk_weights, (plan.M, plan.top_k), _F32, dev), _raw_stream(w, dev, stream)), w)
+
+
+def moe_linear_fp8(x, x_sf, w, w_sf, y, bias=None, accumulate=False, stream=None):
+    """y = x w^T + bias (+ y): x E4M3 [M, K] with E8M0 x_sf [M, ceil(K / 128)],
+    w E4M3 [N, K] with fp32 w_sf [ceil(N / 128), ceil(K / 128)], y bf16 or fp32
+    [M, N].  What the matrix instruction keeps of a product stands in moe.h."""
+    f = "moe_linear_fp8"
+    M, K, N, _ = _sizes(f, x=x, w=w)
+    dev = x.get_device()
+    d = _dtype(f, "y", y)
+    _check(lib().moe_linear_fp8(
+        _arg(f, "x", x, (M, K), _BYTE, dev), _arg(f, "x_sf", x_sf, (M, _nb(K)), _BYTE, dev),
+        _arg(f, "w", w, (N, K), _BYTE, dev), _arg(f, "w_sf", w_sf, (_nb(N), _nb(K)), _F32, dev),
+        _opt(f, "bias", bias, (N,), _F32, dev), M, N, K, 1 if accumulate else 0,
+        _arg(f, "y", y, (M, N), _F32 if d else _BF16, dev), d, _raw_stream(f, dev, stream)), f)
+
+
+def moe_grouped_linear_fp8(x, x_sf, plan: MoePlan, w, w_sf, y, stream=None):
+    """y[s] = bf16(x[s] w[e]^T) for every valid slot s of expert e: x E4M3
+    [route_slots, K], w E4M3 [E_l, N, K] with w_sf [E_l, ceil(N / 128),
+    ceil(K / 128)], y bf16 [route_slots, N]."""
+    f = "moe_grouped_linear_fp8"
+    n, K, _, N = _sizes(f, x=x, y=y)
+    dev = x.get_device()
+    p = _plan_arg(f, plan, dev)
+    n, E = plan.route_slots, plan.num_local_experts
+    _check(lib().moe_grouped_linear_fp8(
+        _arg(f, "x", x, (n, K), _BYTE, dev), _arg(f, "x_sf", x_sf, (n, _nb(K)), _BYTE, dev), p,
+        _arg(f, "w", w, (E, N, K), _BYTE, dev), _arg(f, "w_sf", w_sf, (E, _nb(N), _nb(K)), _F32, dev), N, K,
+        _arg(f, "y", y, (n, N), _BF16, dev), _raw_stream(f, dev, stream)), f)
+
+
+def moe_linear_fp8_wgrad(dy, x, x_sf, dw, accumulate=False, stream=None):
+    """dw [N, K] = dy^T x (+ dw) in fp32, from bf16 dy [M, N] and the product's
+    rows in 8 bits, x E4M3 [M, K] with x_sf."""
+    f = "moe_linear_fp8_wgrad"
+    M, N, _, K = _sizes(f, dy=dy, x=x)
+    dev = dy.get_device()
+    _check(lib().moe_linear_fp8_wgrad(
+        _arg(f, "dy", dy, (M, N), _BF16, dev), _arg(f, "x", x, (M, K), _BYTE, dev),
+        _arg(f, "x_sf", x_sf, (M, _nb(K)), _BYTE, dev), M, N, K, 1 if accumulate else 0,
+        _arg(f, "dw", dw, (N, K), _F32, dev), _raw_stream(f, dev, stream)), f)
+
+
+def moe_grouped_linear_fp8_wgrad(dy, x, x_sf, plan: MoePlan, dw, accumulate=False, stream=None):
+    """The same of every expert, dw [E_l, N, K], from the valid slots of its
+    range: dy bf16 [route_slots, N], x E4M3 [route_slots, K]."""
+    f = "moe_grouped_linear_fp8_wgrad"
+    n, N, _, K = _sizes(f, dy=dy, x=x)
+    dev = dy.get_device()
+    p = _plan_arg(f, plan, dev)
+    n, E = plan.route_slots, plan.num_local_experts
+    _check(lib().moe_grouped_linear_fp8_wgrad(
+        _arg(f, "dy", dy, (n, N), _BF16, dev), _arg(f, "x", x, (n, K), _BYTE, dev),
+        _arg(f, "x_sf", x_sf, (n, _nb(K)), _BYTE, dev), p, N, K, 1 if accumulate else 0,
+        _arg(f, "dw", dw, (E, N, K), _F32, dev), _raw_stream(f, dev, stream)), f)
+
+
+def moe_gated_act_fp8(h, y, y_sf, hq=None, hq_sf=None, plan: MoePlan | None = None, activation=ACT_SWIGLU,
+                      swiglu_alpha=1.0, swiglu_beta=0.0, swiglu_limit=FLT_MAX, stream=None):
+    """The gated activation of bf16 rows h = (gate, up) [rows, 2I], quantised (y
+    [rows, I], y_sf [rows, ceil(I / 128)]), and h kept in 8 bits for the
+    backward pass (hq [rows, 2I], hq_sf [rows, 2 ceil(I / 128)]).  With a plan
+    its valid slots are the rows."""
+    w = "moe_gated_act_fp8"
+    rows, I = _sizes(w, y=y)
+    dev = y.get_device()
+    p = None if plan is None else _plan_arg(w, plan, dev)
+    if plan is not None:
+        rows = plan.route_slots
+    _check(lib().moe_gated_act_fp8(
+        _arg(w, "h", h, (rows, 2 * I), _BF16, dev), p, rows, I, activation, swiglu_alpha, swiglu_beta, swiglu_limit,
+        _arg(w, "y", y, (rows, I), _BYTE, dev), _arg(w, "y_sf", y_sf, (rows, _nb(I)), _BYTE, dev),
+        _opt(w, "hq", hq, (rows, 2 * I), _BYTE, dev), _opt(w, "hq_sf", hq_sf, (rows, 2 * _nb(I)), _BYTE, dev),
+        _raw_stream(w, dev, stream)), w)
+
+
+def moe_gated_act_fp8_backward(hq, hq_sf, dy, dh=None, dq=None, dq_sf=None, plan: MoePlan | None = None,
+                               activation=ACT_SWIGLU, swiglu_alpha=1.0, swiglu_beta=0.0, swiglu_limit=FLT_MAX,
+                               stream=None):
+    """The gradient of moe_gated_act_fp8's h at the h it kept, from dy bf16
+    [rows, I]: dh bf16 [rows, 2I] and / or quantised, dq [rows, 2I] with dq_sf
+    [rows, 2 ceil(I / 128)]."""
+    w = "moe_gated_act_fp8_backward"
+    rows, I = _sizes(w, dy=dy)
+    dev = dy.get_device()
+    p = None if plan is None else _plan_arg(w, plan, dev)
+    if plan is not None:
+        rows = plan.route_slots
+    _check(lib().moe_gated_act_fp8_backward(
+        _arg(w, "hq", hq, (rows, 2 * I), _BYTE, dev), _arg(w, "hq_sf", hq_sf, (rows, 2 * _nb(I)), _BYTE, dev),
+        _arg(w, "dy", dy, (rows, I), _BF16, dev), p, rows, I, activation, swiglu_alpha, swiglu_beta, swiglu_limit,
+        _opt(w, "dh", dh, (rows, 2 * I), _BF16, dev), _opt(w, "dq", dq, (rows, 2 * I), _BYTE, dev),
+        _opt(w, "dq_sf", dq_sf, (rows, 2 * _nb(I)), _BYTE, dev), _raw_stream(w, dev, stream)), w)

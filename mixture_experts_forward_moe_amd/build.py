@@ -11,6 +11,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["sort.hip", "gemm.hip", "gemm_wide.hip", "gemm_mx.hip", "gemm_mxw.hip", "gemm_nvfp4.hip",
            "decode.hip", "finalize.hip", "norm.hip", "router.hip", "linear_mx.hip",
+           "fp8_rows.hip", "linear_fp8.hip", "wgrad_fp8.hip",
            "capi.cpp", "noalloc.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

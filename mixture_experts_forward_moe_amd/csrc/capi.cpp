@@ -819,3 +819,273 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
 }
 
 }  // extern "C"
+
+namespace {
+
+bool unaligned8(const void* p) { return ((uintptr_t)p & 7) != 0; }
+
+// Rows of the calls on rows in 8 bits: launches of one wavefront for each part
+// of `part` values of a row, whose threads must stay below 2^32.
+bool too_many_parts(int64_t rows, int cols, int part) {
+  return rows > (int64_t)1 << 25 || rows * ((cols + part - 1) / part) > (int64_t)1 << 25;
+}
+
+// what the calls between tokens and a plan's slots have in common
+moe_status_t slots_shape(const moe_plan_t* plan, int H) {
+  if (!plan_ok(plan) || H <= 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (H % 16 != 0 || H > FP8_MAX_H || plan->M > 1 << 22) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t act_shape(const moe_plan_t* plan, int64_t rows, int I, int activation, float alpha, float beta,
+                       float limit, GateAct* act) {
+  if ((plan && (!plan_ok(plan) || rows != plan->route_slots)) || rows < 0 || I <= 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (!std::isfinite(alpha) || !std::isfinite(beta)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status_t s = make_act(activation, alpha, beta, limit, 0.0f, 0.0f, act);
+  if (s != MOE_OK) return s;
+  if (activation == MOE_ACT_RELU2 || I % 16 != 0 || I > 1 << 29 || too_many_parts(rows, I, 1024))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t linear_fp8_shape(int64_t M, int N, int K, int most) {
+  if (M < 0 || N < 0 || K < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (K % 16 != 0 || K > (most < 1 << 20 ? most : 1 << 20) || M > 1 << 26 || N > most ||
+      M * N > (int64_t)1 << 36)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status_t wgrad_shape(int64_t M, int N, int K, const void* dy, const void* x, const void* dw) {
+  if (M < 0 || N < 0 || K < 1) return MOE_ERR_INVALID_ARGUMENT;
+  if (N % 8 != 0 || K % 16 != 0 || N > 1 << 16 || K > 1 << 16 || M > 1 << 26) return MOE_ERR_UNSUPPORTED;
+  if (unaligned16(dy) || unaligned16(x) || unaligned16(dw)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t x_row_stride, int64_t rows, int cols, uint8_t* q,
+                              uint8_t* q_sf, moe_stream_t stream) {
+  if (rows < 0 || cols <= 0 || (x_row_stride != 0 && x_row_stride < cols)) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows > 0 && (!x || !q || !q_sf)) return MOE_ERR_INVALID_ARGUMENT;
+  if (cols % 16 != 0 || x_row_stride % 8 != 0 || cols > 1 << 30 || too_many_parts(rows, cols, 2048))
+    return MOE_ERR_UNSUPPORTED;
+  if (unaligned16(x) || unaligned16(q)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  return dev(launch_quantize_fp8(x, x_row_stride ? x_row_stride : cols, rows, cols, q, q_sf, (hipStream_t)stream));
+}
+
+moe_status_t moe_quantize_fp8_weight(const uint16_t* w, int batches, int N, int K, uint8_t* q, float* sf, uint8_t* qt,
+                                     float* sft, moe_stream_t stream) {
+  if (batches < 0 || N < 0 || K < 1 || !qt != !sft) return MOE_ERR_INVALID_ARGUMENT;
+  if (batches > 0 && N > 0 && (!w || !q || !sf)) return MOE_ERR_INVALID_ARGUMENT;
+  if (K % 8 != 0 || (qt && N % 8 != 0)) return MOE_ERR_UNSUPPORTED;
+  const int64_t blocks = (((int64_t)N + 127) / 128) * (((int64_t)K + 127) / 128);
+  if (blocks > 1 << 23 || blocks * batches > 1 << 23) return MOE_ERR_UNSUPPORTED;
+  if (unaligned16(w) || unaligned8(q) || unaligned8(qt) || unaligned4(sf) || unaligned4(sft))
+    return MOE_ERR_UNSUPPORTED;
+  if (batches == 0 || N == 0) return MOE_OK;
+  return dev(launch_quantize_fp8_weight(w, batches, N, K, q, sf, qt, sft, (hipStream_t)stream));
+}
+
+moe_status_t moe_dispatch(const uint16_t* x, int64_t x_row_stride, const moe_plan_t* plan, int H, uint16_t* rows,
+                          uint8_t* q, uint8_t* q_sf, moe_stream_t stream) {
+  const moe_status_t s = slots_shape(plan, H);
+  if (s != MOE_OK) return s;
+  if ((x_row_stride != 0 && x_row_stride < H) || !q != !q_sf) return MOE_ERR_INVALID_ARGUMENT;
+  if (plan->M > 0 && (!x || (!rows && !q))) return MOE_ERR_INVALID_ARGUMENT;
+  if (x_row_stride % 8 != 0 || unaligned16(x) || unaligned16(rows) || unaligned16(q)) return MOE_ERR_UNSUPPORTED;
+  if (plan->M == 0) return MOE_OK;
+  DispatchParams p = {};
+  p.x = x;
+  p.x_row_stride = x_row_stride ? x_row_stride : H;
+  p.slots = plan->expanded_to_permuted;
+  p.M = plan->M;
+  p.top_k = plan->top_k;
+  p.H = H;
+  p.rows = rows;
+  p.q = q;
+  p.q_sf = q_sf;
+  return dev(launch_dispatch(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_dispatch_backward(const uint16_t* d_rows, const moe_plan_t* plan, int H, int accumulate, uint16_t* dx,
+                                   moe_stream_t stream) {
+  const moe_status_t s = slots_shape(plan, H);
+  if (s != MOE_OK) return s;
+  if (plan->M > 0 && (!d_rows || !dx)) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(d_rows) || unaligned16(dx)) return MOE_ERR_UNSUPPORTED;
+  if (plan->M == 0) return MOE_OK;
+  return dev(launch_dispatch_backward(d_rows, plan->expanded_to_permuted, plan->M, plan->top_k, H, accumulate ? 1 : 0,
+                                      dx, (hipStream_t)stream));
+}
+
+moe_status_t moe_finalize_backward(const uint16_t* dout, const uint16_t* y2, const moe_plan_t* plan,
+                                   const float* topk_weights, int H, float routed_scaling_factor, uint16_t* dy2,
+                                   uint8_t* q, uint8_t* q_sf, float* d_topk_weights, moe_stream_t stream) {
+  const moe_status_t s = slots_shape(plan, H);
+  if (s != MOE_OK) return s;
+  if (!q != !q_sf || !std::isfinite(routed_scaling_factor)) return MOE_ERR_INVALID_ARGUMENT;
+  if (plan->M > 0 && (!dout || !topk_weights || !y2 != !d_topk_weights || (!dy2 && !q && !d_topk_weights)))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(dout) || unaligned16(y2) || unaligned16(dy2) || unaligned16(q) || unaligned4(topk_weights) ||
+      unaligned4(d_topk_weights))
+    return MOE_ERR_UNSUPPORTED;
+  if (plan->M == 0) return MOE_OK;
+  FinalizeBackwardParams p = {};
+  p.dout = dout;
+  p.y2 = y2;
+  p.slots = plan->expanded_to_permuted;
+  p.weights = topk_weights;
+  p.M = plan->M;
+  p.top_k = plan->top_k;
+  p.H = H;
+  p.rsf = routed_scaling_factor;
+  p.dy2 = dy2;
+  p.q = q;
+  p.q_sf = q_sf;
+  p.dw = d_topk_weights;
+  return dev(launch_finalize_backward(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const uint8_t* w, const float* w_sf,
+                            const float* bias, int M, int N, int K, int accumulate, void* y, moe_dtype_t y_dtype,
+                            moe_stream_t stream) {
+  if (!dtype_ok(y_dtype)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status_t s = linear_fp8_shape(M, N, K, 1 << 26);
+  if (s != MOE_OK) return s;
+  if (M > 0 && N > 0 && (!x || !x_sf || !w || !w_sf || !y)) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(x) || unaligned16(w) || ((uintptr_t)y & (y_dtype == MOE_DTYPE_F32 ? 3 : 1)) != 0 ||
+      unaligned4(w_sf) || unaligned4(bias))
+    return MOE_ERR_UNSUPPORTED;
+  if (M == 0 || N == 0) return MOE_OK;
+  LinearFp8Params p = {};
+  p.x = x;
+  p.x_sf = x_sf;
+  p.w = w;
+  p.w_sf = w_sf;
+  p.bias = bias;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.accumulate = accumulate ? 1 : 0;
+  p.y = y;
+  p.y_f32 = y_dtype == MOE_DTYPE_F32;
+  return dev(launch_linear_fp8(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const moe_plan_t* plan, const uint8_t* w,
+                                    const float* w_sf, int N, int K, uint16_t* y, moe_stream_t stream) {
+  if (!plan_ok(plan)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status_t s = linear_fp8_shape(plan->route_slots, N, K, 1 << 16);
+  if (s != MOE_OK) return s;
+  if (N % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  if (plan->M > 0 && N > 0 && (!x || !x_sf || !w || !w_sf || !y)) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(x) || unaligned16(w) || unaligned16(y) || unaligned4(w_sf)) return MOE_ERR_UNSUPPORTED;
+  if (plan->M == 0 || N == 0) return MOE_OK;
+  LinearFp8Params p = {};
+  p.x = x;
+  p.x_sf = x_sf;
+  p.w = w;
+  p.w_sf = w_sf;
+  p.M = plan->route_slots;
+  p.N = N;
+  p.K = K;
+  p.y = y;
+  p.tile_expert = plan->tile_to_expert;
+  p.tile_limit = plan->tile_to_mn_limit;
+  p.tile = plan->tile;
+  p.tiles = plan->max_tiles;
+  return dev(launch_linear_fp8(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf, int M, int N, int K,
+                                  int accumulate, float* dw, moe_stream_t stream) {
+  const moe_status_t s = wgrad_shape(M, N, K, dy, x, dw);
+  if (s != MOE_OK) return s;
+  if (N > 0 && (!dw || (M > 0 && (!dy || !x || !x_sf)))) return MOE_ERR_INVALID_ARGUMENT;
+  if (N == 0) return MOE_OK;
+  WgradParams p = {};
+  p.dy = dy;
+  p.x = x;
+  p.x_sf = x_sf;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.accumulate = accumulate ? 1 : 0;
+  p.dw = dw;
+  p.experts = 1;
+  return dev(launch_wgrad_fp8(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_grouped_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf,
+                                          const moe_plan_t* plan, int N, int K, int accumulate, float* dw,
+                                          moe_stream_t stream) {
+  if (!plan_ok(plan)) return MOE_ERR_INVALID_ARGUMENT;
+  const moe_status_t s = wgrad_shape(plan->route_slots, N, K, dy, x, dw);
+  if (s != MOE_OK) return s;
+  if (N > 0 && (!dw || (plan->M > 0 && (!dy || !x || !x_sf)))) return MOE_ERR_INVALID_ARGUMENT;
+  if (N == 0) return MOE_OK;
+  WgradParams p = {};
+  p.dy = dy;
+  p.x = x;
+  p.x_sf = x_sf;
+  p.M = plan->M == 0 ? 0 : plan->route_slots;
+  p.N = N;
+  p.K = K;
+  p.accumulate = accumulate ? 1 : 0;
+  p.dw = dw;
+  p.offsets = plan->M == 0 ? NULL : plan->expert_offsets;
+  p.counts = plan->expert_counts;
+  p.experts = plan->num_local_experts;
+  return dev(launch_wgrad_fp8(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_gated_act_fp8(const uint16_t* h, const moe_plan_t* plan, int64_t rows, int I, int activation,
+                               float swiglu_alpha, float swiglu_beta, float swiglu_limit, uint8_t* y, uint8_t* y_sf,
+                               uint8_t* hq, uint8_t* hq_sf, moe_stream_t stream) {
+  ActParams p = {};
+  const moe_status_t s = act_shape(plan, rows, I, activation, swiglu_alpha, swiglu_beta, swiglu_limit, &p.act);
+  if (s != MOE_OK) return s;
+  if (!hq != !hq_sf) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows > 0 && (!h || !y || !y_sf)) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(h) || unaligned16(y) || unaligned16(hq)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || (plan && plan->M == 0)) return MOE_OK;
+  p.h = h;
+  p.routes = plan ? plan->permuted_to_expanded : NULL;
+  p.rows = rows;
+  p.I = I;
+  p.y = y;
+  p.y_sf = y_sf;
+  p.hq = hq;
+  p.hq_sf = hq_sf;
+  return dev(launch_act(p, (hipStream_t)stream));
+}
+
+moe_status_t moe_gated_act_fp8_backward(const uint8_t* hq, const uint8_t* hq_sf, const uint16_t* dy,
+                                        const moe_plan_t* plan, int64_t rows, int I, int activation,
+                                        float swiglu_alpha, float swiglu_beta, float swiglu_limit, uint16_t* dh,
+                                        uint8_t* dq, uint8_t* dq_sf, moe_stream_t stream) {
+  ActBackwardParams p = {};
+  const moe_status_t s = act_shape(plan, rows, I, activation, swiglu_alpha, swiglu_beta, swiglu_limit, &p.act);
+  if (s != MOE_OK) return s;
+  if (!dq != !dq_sf) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows > 0 && (!hq || !hq_sf || !dy || (!dh && !dq))) return MOE_ERR_INVALID_ARGUMENT;
+  if (unaligned16(hq) || unaligned16(dy) || unaligned16(dh) || unaligned16(dq)) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0 || (plan && plan->M == 0)) return MOE_OK;
+  p.hq = hq;
+  p.hq_sf = hq_sf;
+  p.dy = dy;
+  p.routes = plan ? plan->permuted_to_expanded : NULL;
+  p.rows = rows;
+  p.I = I;
+  p.dh = dh;
+  p.dq = dq;
+  p.dq_sf = dq_sf;
+  return dev(launch_act_backward(p, (hipStream_t)stream));
+}
+
+}  // extern "C"

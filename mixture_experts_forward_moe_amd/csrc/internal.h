@@ -244,4 +244,88 @@ struct LinearParams {
 };
 hipError_t launch_linear_mx(const LinearParams& p, hipStream_t stream);
 
+// rows in 8 bits (E4M3 codes, an E8M0 byte for each 128 values): quantisers,
+// the experts' rows and back, activations
+constexpr int FP8_MAX_H = 16384;
+struct DispatchParams {
+  const uint16_t* x;
+  int64_t x_row_stride;
+  const int32_t* slots;       // expanded_to_permuted
+  int64_t M;
+  int top_k, H;
+  uint16_t* rows;             // NULL: not stored
+  uint8_t *q, *q_sf;          // NULL: not stored
+};
+struct FinalizeBackwardParams {
+  const uint16_t *dout, *y2;  // y2 NULL: no dw
+  const int32_t* slots;
+  const float* weights;
+  int64_t M;
+  int top_k, H;
+  float rsf;
+  uint16_t* dy2;              // NULL: not stored (as q, dw)
+  uint8_t *q, *q_sf;
+  float* dw;
+};
+struct ActParams {
+  const uint16_t* h;
+  const int32_t* routes;      // permuted_to_expanded (rows without a route are passed over); NULL: every row
+  int64_t rows;
+  int I;
+  GateAct act;
+  uint8_t *y, *y_sf;
+  uint8_t *hq, *hq_sf;        // NULL: not kept
+};
+struct ActBackwardParams {
+  const uint8_t *hq, *hq_sf;
+  const uint16_t* dy;
+  const int32_t* routes;
+  int64_t rows;
+  int I;
+  GateAct act;
+  uint16_t* dh;               // NULL: not stored (as dq)
+  uint8_t *dq, *dq_sf;
+};
+hipError_t launch_quantize_fp8(const uint16_t* x, int64_t stride, int64_t rows, int cols, uint8_t* q, uint8_t* sf,
+                               hipStream_t stream);
+hipError_t launch_quantize_fp8_weight(const uint16_t* w, int batches, int N, int K, uint8_t* q, float* sf, uint8_t* qt,
+                                      float* sft, hipStream_t stream);
+hipError_t launch_dispatch(const DispatchParams& p, hipStream_t stream);
+hipError_t launch_dispatch_backward(const uint16_t* dxp, const int32_t* slots, int64_t M, int top_k, int H,
+                                    int accumulate, uint16_t* dx, hipStream_t stream);
+hipError_t launch_finalize_backward(const FinalizeBackwardParams& p, hipStream_t stream);
+hipError_t launch_act(const ActParams& p, hipStream_t stream);
+hipError_t launch_act_backward(const ActBackwardParams& p, hipStream_t stream);
+
+// products of rows in 8 bits, of one matrix or of every expert's
+struct LinearFp8Params {
+  const uint8_t *x, *x_sf;    // [rows, K], [rows, ceil(K / 128)]
+  const uint8_t* w;           // [N, K], or [experts, N, K]
+  const float* w_sf;          // [.., ceil(N / 128), ceil(K / 128)]
+  const float* bias;          // NULL: none
+  int64_t M;                  // rows; with a plan its slots
+  int N, K;
+  int accumulate;
+  void* y;
+  int y_f32;
+  const int32_t* tile_expert; // NULL: one matrix; else the plan's tiles
+  const int32_t* tile_limit;
+  int tile, tiles;
+};
+hipError_t launch_linear_fp8(const LinearFp8Params& p, hipStream_t stream);
+
+// gradients of their weights
+struct WgradParams {
+  const uint16_t* dy;         // bf16 [rows, N]
+  const uint8_t *x, *x_sf;
+  int64_t M;
+  int N, K;
+  int accumulate;
+  float* dw;                  // [N, K], or [experts, N, K]
+  const int32_t* offsets;     // NULL: one matrix; else the plan's first slots and counts
+  const int32_t* counts;
+  int experts;                // 1 without a plan
+};
+hipError_t launch_wgrad_fp8(const WgradParams& p, hipStream_t stream);
+
 }  // namespace moe
