@@ -997,6 +997,7 @@ moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const
   p.y = y;
   p.tile_expert = plan->tile_to_expert;
   p.tile_limit = plan->tile_to_mn_limit;
+  p.num_tiles = plan->num_tiles;
   p.tile = plan->tile;
   p.tiles = plan->max_tiles;
   return dev(launch_linear_fp8(p, (hipStream_t)stream));

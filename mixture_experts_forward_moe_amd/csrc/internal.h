@@ -310,6 +310,7 @@ struct LinearFp8Params {
   int y_f32;
   const int32_t* tile_expert; // NULL: one matrix; else the plan's tiles
   const int32_t* tile_limit;
+  const int32_t* num_tiles;
   int tile, tiles;
 };
 hipError_t launch_linear_fp8(const LinearFp8Params& p, hipStream_t stream);

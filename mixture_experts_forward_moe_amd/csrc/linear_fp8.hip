@@ -6,6 +6,8 @@
 // any fp32 value, which it does not take: the product of each 128 of K is a
 // sum of its own, from zero, that one fused multiply-add with W's scale adds to
 // the fp32 sum.
+#include <atomic>
+
 #include "device_common.h"
 #include "internal.h"
 
@@ -40,6 +42,72 @@ DEV bool group_of(const LinearFp8Params& a, int g, int height, Group& o) {
   o.w_sf = a.w_sf + (int64_t)e * ((a.N + 127) / 128) * ((a.K + 127) / 128);
   return o.first < o.end;
 }
+
+// ------------------------------------------------------------- way out
+
+DEV void store_one(const LinearFp8Params& a, int64_t row, int n, float v) {
+  const int64_t at = row * a.N + n;
+  if (a.y_f32) {
+    float* y = reinterpret_cast<float*>(a.y) + at;
+    *y = a.accumulate ? *y + v : v;
+  } else {
+    uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + at;
+    *y = f32_to_bf16(a.accumulate ? bf16_to_f32(*y) + v : v);
+  }
+}
+
+// A wavefront's 16 TM x 16 TN results, rows m0 .. end, columns from n0.  WIDE:
+// bf16 that is overwritten, its rows aligned to 16 bytes, leaves through the
+// wavefront's own part of LDS, 16 rows at a time (chunks swizzled by the row), in whole
+// lines.
+template <typename S, bool WIDE>
+DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM], int64_t m0, int64_t end, int n0,
+                    uint8_t* out, int lane) {
+  constexpr int TM = S::TM, TN = S::TN, W = 4 * TN;  // columns of a lane
+  constexpr int C = 2 * TN;                          // chunks of 16 bytes in a row
+  const int r = lane & 15, q = lane >> 4, n = n0 + W * q;
+#pragma unroll
+  for (int m = 0; m < TM; m++) {
+    const int64_t row0 = m0 + 16 * m;
+    if constexpr (WIDE) {
+      if (row0 >= end) break;
+#pragma unroll
+      for (int c = 0; c < TN / 2; c++) {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          v[i] = acc[2 * c + (i >> 2)][m][i & 3];
+          if (a.bias) v[i] += a.bias[min(n + 8 * c + i, a.N - 1)];
+        }
+        u32x4_t o;
+#pragma unroll
+        for (int i = 0; i < 4; i++) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+        *reinterpret_cast<u32x4_t*>(out + 16 * (C * r + ((TN / 2 * q + c) ^ (r & (C - 1))))) = o;
+      }
+      wave_fence();  // the rows are read by other lanes
+      constexpr int ROWS = 64 / C;  // rows a store
+#pragma unroll
+      for (int i = 0; i < 16 / ROWS; i++) {
+        const int rr = ROWS * i + lane / C, c = lane % C;
+        const u32x4_t o = *reinterpret_cast<const u32x4_t*>(out + 16 * (C * rr + (c ^ (rr & (C - 1)))));
+        if (row0 + rr < end && n0 + 8 * c < a.N)
+          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.y) + (row0 + rr) * a.N + n0 + 8 * c) = o;
+      }
+      wave_fence();  // and written again once they have been
+    } else {
+      if (row0 + r >= end) continue;
+#pragma unroll
+      for (int t = 0; t < TN; t++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          const int col = n + 4 * t + i;
+          if (col < a.N) store_one(a, row0 + r, col, a.bias ? acc[t][m][i] + a.bias[col] : acc[t][m][i]);
+        }
+    }
+  }
+}
+
+// ------------------------------------------------------------- streaming kernel
 
 constexpr int STREAM_WAVES = 8;
 
@@ -102,15 +170,7 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void fp8_stream_kernel(const Lin
   for (int i = 0; i < 4; i++) {
     const int64_t row = o.first + 16 * wave + 4 * q + i;
     if (row >= o.end) continue;
-    const float out = v[i] + bias;
-    const int64_t at = row * a.N + n;
-    if (a.y_f32) {
-      float* y = reinterpret_cast<float*>(a.y) + at;
-      *y = a.accumulate ? *y + out : out;
-    } else {
-      uint16_t* y = reinterpret_cast<uint16_t*>(a.y) + at;
-      *y = f32_to_bf16(a.accumulate ? bf16_to_f32(*y) + out : out);
-    }
+    store_one(a, row, n, v[i] + bias);
   }
 }
 
@@ -123,13 +183,325 @@ hipError_t launch_stream(const LinearFp8Params& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ------------------------------------------------------------- tiled kernel
+
+typedef __attribute__((address_space(3))) void lds_void_t;
+
+// Workgroup barrier: this wavefront's LDS accesses and its loads are done
+// (written out: a release fence would not say which loads).
+DEV void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+template <int WM_, int WN_, int TM_, int TN_>
+struct Tile {
+  static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // wavefronts, 16 x 16 results of each
+  static constexpr int NT = 64 * WM * WN;
+  static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
+  static constexpr int X_BYTES = BM * 128;
+  static constexpr int STAGE = (BM + BN) * 128;
+  static constexpr int OUT = 16 * 16 * TN * 2;                  // a wavefront's way out: 16 rows
+  static constexpr int T_OFF = 2 * STAGE;
+  static constexpr int LDS = T_OFF + WM * WN * OUT;
+  static constexpr int NX = BM * 8 / NT, NW = BN * 8 / NT;      // LDS-DMA loads a wavefront and stage
+};
+
+// The four E8M0 bytes from block 4 g of a row of kb blocks, the first one lowest.
+// A word that reaches past the row's end is read from its last four bytes.
+DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
+  if (kb >= 4) {
+    const int at = min(4 * g, kb - 4);
+    uint32_t v;
+    __builtin_memcpy(&v, row + at, 4);
+    return v >> (8 * min(3, 4 * g - at));
+  }
+  uint32_t v = 0;
+  for (int i = 0; i < kb; i++) v |= (uint32_t)row[i] << (8 * i);
+  return v;
+}
+
+// One workgroup a tile at a time, K in stages of 128 in two buffers that
+// LDS-DMA fills.  A wavefront computes 16 TM rows by 16 TN columns, W's rows the
+// first operand: a lane then has 4 TN consecutive columns of one row of y, if
+// row 4 a + b of W's tile t is column 4 TN a + 4 t + b.  The rows' fragments
+// stay in registers over a stage, W's pass through four of them; the last two of
+// a stage are multiplied row tile by row tile, so that the next stage's rows can
+// be read behind them, and the barrier between two stages has multiplications
+// on both sides.
+template <typename S, bool WIDE>
+__global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Params a, int tiles_n) {
+  constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW;
+  static_assert(TN % 4 == 0 && NX % 2 == 0 && NW % 2 == 0, "four buffers of W; the swizzle goes by a load's number");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wn = wave % S::WN, wm = wave / S::WN;
+  const int kb = (a.K + 127) / 128, KT = max(kb, 2);
+
+  // tiles of this workgroup: XCD b & 7 takes a contiguous run of them, its
+  // workgroups take them in turn; 8 rows of tiles high, so that what an XCD
+  // works on at a time shares its rows in the L2
+  const int parts = a.tile_expert ? a.tile / BM : 1;
+  const int tiles_m = a.tile_expert ? ld_uniform(a.num_tiles) * parts : (int)((a.M + BM - 1) / BM);
+  const int64_t tiles = (int64_t)tiles_m * tiles_n, per = (tiles + 7) / 8;
+  const int step = gridDim.x >> 3;
+  const int64_t first = (blockIdx.x & 7) * per, last = min(first + per, tiles);
+  int64_t t = first + (blockIdx.x >> 3);
+  if (t >= last) return;
+
+  struct At {
+    int64_t m0, end;
+    int n0;
+    const uint8_t* w;
+    const float* w_sf;
+  };
+  auto tile_at = [&](int64_t t) {
+    constexpr int GM = 8;
+    const int group = (int)(t / (GM * tiles_n)), in = (int)(t - (int64_t)group * GM * tiles_n);
+    const int rows = min(GM, tiles_m - group * GM), tm = group * GM + in % rows;
+    At o;
+    o.n0 = in / rows * BN;
+    if (!a.tile_expert) {
+      o.m0 = (int64_t)tm * BM;
+      o.end = min(a.M, o.m0 + BM);
+      o.w = a.w;
+      o.w_sf = a.w_sf;
+    } else {
+      const int pt = tm / parts, e = ld_uniform(a.tile_expert + pt);
+      o.m0 = (int64_t)pt * a.tile + (tm - pt * parts) * BM;
+      o.end = min(o.m0 + BM, (int64_t)ld_uniform(a.tile_limit + pt));
+      o.w = a.w + (int64_t)e * a.N * a.K;
+      o.w_sf = a.w_sf + (int64_t)e * ((a.N + 127) / 128) * kb;
+    }
+    return o;
+  };
+
+  // what the loads of the moment read: buffers that end with the tile's last row
+  // (rows past it read as 0), this lane's place in them (row lane / 8 of eight, a
+  // chunk of 16 bytes swizzled by row / 2, whose bit 2 is the load's parity), and
+  // the scales' rows (past the last: that one; such products are not stored)
+  __amdgpu_buffer_rsrc_t xb, wb;
+  const uint8_t* xsf;
+  const float* wsf;
+  int last_m;
+  const int chunk = 16 * ((lane & 7) ^ (lane >> 4));
+  const uint32_t place_x = (uint32_t)(8 * NX * wave + (lane >> 3)) * (uint32_t)a.K;
+  // row of W that lane / 8 loads: a load's eight rows of LDS, 8 i + 0 .. 7, are
+  // rows 4 c .. 4 c + 3 of W for two c
+  const uint32_t place_w = (uint32_t)((lane >> 5) * 4 * TN + ((lane >> 3) & 3)) * (uint32_t)a.K;
+  auto aim = [&](const At& o) {
+    last_m = max(0, (int)(o.end - o.m0) - 1);
+    xb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x + o.m0 * a.K), 0, (last_m + 1) * a.K, 0x00020000);
+    wb = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.w + (int64_t)o.n0 * a.K), 0,
+                                           min(BN, a.N - o.n0) * a.K, 0x00020000);
+    xsf = a.x_sf + o.m0 * kb;
+    wsf = o.w_sf + (int64_t)(min(o.n0 + 16 * TN * wn, a.N - 1) >> 7) * kb;
+  };
+  // (a chunk past the end of K: the row's first one)
+  auto issue = [&](int s, uint8_t* st) {
+    uint32_t k[2];
+#pragma unroll
+    for (int v = 0; v < 2; v++) {
+      k[v] = (uint32_t)(128 * s + (chunk ^ (64 * v)));
+      k[v] = k[v] < (uint32_t)a.K ? k[v] : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < NX; i++)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void_t*)(st + 1024 * (NX * wave + i)), 16,
+                                               place_x + k[i & 1] + (uint32_t)(8 * i * a.K), 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < NW; i++) {
+      const int j = 8 * (NW * wave + i), in = j % (16 * TN);  // the load's first row of LDS
+      const int n = j - in + ((in >> 2) & 3) * (4 * TN) + 4 * (in >> 4);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wb, (lds_void_t*)(st + S::X_BYTES + 1024 * (NW * wave + i)), 16,
+                                               place_w + k[i & 1] + (uint32_t)(n * a.K), 0, 0, 0);
+    }
+  };
+
+  const int swizzle = (r >> 1) & 7;
+  const int at0 = 128 * r + 16 * (q ^ swizzle), at1 = 128 * r + 16 * ((q + 4) ^ swizzle);
+  struct Frag {
+    u32x4_t lo, hi;
+  };
+  auto read_x = [&](const uint8_t* st, int m) {
+    const uint8_t* p = st + 2048 * (TM * wm + m);
+    return Frag{ld16(p + at0), ld16(p + at1)};
+  };
+  auto read_w = [&](const uint8_t* st, int t) {
+    const uint8_t* p = st + S::X_BYTES + 2048 * (TN * wn + t);
+    return Frag{ld16(p + at0), ld16(p + at1)};
+  };
+  auto mul = [&](const Frag& w, const Frag& x, int xs) {
+    const i32x8_t c = {(int)w.lo[0], (int)w.lo[1], (int)w.lo[2], (int)w.lo[3],
+                       (int)w.hi[0], (int)w.hi[1], (int)w.hi[2], (int)w.hi[3]};
+    const i32x8_t b = {(int)x.lo[0], (int)x.lo[1], (int)x.lo[2], (int)x.lo[3],
+                       (int)x.hi[0], (int)x.hi[1], (int)x.hi[2], (int)x.hi[3]};
+    const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c, b, none, 0, 0, 0, 127, 0, xs);
+  };
+
+  Frag x[TM], w[4];
+  f32x4_t acc[TN][TM], p[TM];
+  uint32_t word[TM], later[TM];  // scale bytes of the stages from this one on, and of the next four
+  float ws;
+  auto load_scales = [&](int g) {
+#pragma unroll
+    for (int m = 0; m < TM; m++) later[m] = scale_word(xsf + min(16 * (TM * wm + m) + r, last_m) * kb, g, kb);
+  };
+  auto add = [&](int t, int m, const f32x4_t& v, float s) {
+#pragma unroll
+    for (int i = 0; i < 4; i++) acc[t][m][i] = fmaf(v[i], s, acc[t][m][i]);
+  };
+
+  At o = tile_at(t);
+  aim(o);
+  load_scales(0);
+  issue(0, smem);
+  issue(1, smem + S::STAGE);
+  ws = ld_uniform(wsf);
+  int buf = 0;
+  stage_barrier();
+#pragma unroll
+  for (int m = 0; m < TM; m++) {
+    x[m] = read_x(smem, m);
+    word[m] = later[m];
+  }
+  w[0] = read_w(smem, 0);
+  w[1] = read_w(smem, 1);
+
+#pragma unroll 1
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < TN; i++)
+#pragma unroll
+      for (int m = 0; m < TM; m++) acc[i][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t tn = t + step;
+    const bool more = tn < last;
+    const At next = more ? tile_at(tn) : o;
+    const float* wsf_of_this = wsf;
+#pragma unroll 1
+    for (int s = 0; s < KT; s++) {
+      uint8_t* st = smem + buf * S::STAGE;
+      buf ^= 1;
+      const uint8_t* sn = smem + buf * S::STAGE;
+      if (128 * (s + 1) > a.K) {  // values past the end of K
+        const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
+#pragma unroll
+        for (int m = 0; m < TM; m++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            x[m].lo[i] = in0 ? x[m].lo[i] : 0u;
+            x[m].hi[i] = in1 ? x[m].hi[i] : 0u;
+          }
+      }
+#pragma unroll
+      for (int i = 0; i < TN - 2; i++) {
+        w[(i + 2) & 3] = read_w(st, i + 2);
+#pragma unroll
+        for (int m = 0; m < TM; m++) {
+          if (i > 0) add(i - 1, m, p[m], ws);
+          p[m] = mul(w[i & 3], x[m], (int)word[m]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // every fragment of the stage is on its way to registers, the next stage has landed
+      stage_barrier();
+      const float wl = ws;
+      if (s + 2 == KT) aim(next);
+      const int ahead = s + 2 < KT ? s + 2 : s + 2 - KT;  // of this tile or of the next one
+      issue(ahead, st);
+      ws = ld_uniform(s + 1 < KT ? wsf_of_this + min(s + 1, kb - 1) : wsf);
+      const bool fresh = s + 1 == KT || ((s + 1) & 3) == 0;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < TM; m++) {
+        const f32x4_t u = mul(w[(TN - 2) & 3], x[m], (int)word[m]), v = mul(w[(TN - 1) & 3], x[m], (int)word[m]);
+        x[m] = read_x(sn, m);
+        if (m < 2) w[m] = read_w(sn, m);
+        add(TN - 3, m, p[m], wl);
+        add(TN - 2, m, u, wl);
+        add(TN - 1, m, v, wl);
+        word[m] = fresh ? later[m] : word[m] >> 8;
+      }
+      if ((ahead & 3) == 0) load_scales(ahead >> 2);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    store_tile<S, WIDE>(a, acc, o.m0 + 16 * TM * wm, o.end, o.n0 + 16 * TN * wn, smem + S::T_OFF + S::OUT * wave, lane);
+    if (!more) break;
+    t = tn;
+    o = next;
+  }
+  __builtin_amdgcn_s_waitcnt(0x0070);  // no LDS-DMA load may be in flight when the workgroup ends
+}
+
+bool wide_rows(const LinearFp8Params& a) {
+  return !a.y_f32 && !a.accumulate && a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
+}
+
+// Allows a kernel more than the default dynamic LDS, once per device, and
+// gives the device's number of compute units.  Calls of several threads may
+// come here at once: one word says that it has been done, and is the number.
+template <auto KERN>
+hipError_t allow_lds(int bytes, int* cus) {
+  static std::atomic<int> count[64] = {};  // 0: not yet
+  int dev = 0;
+  hipError_t err = hipGetDevice(&dev);
+  if (err != hipSuccess) return err;
+  const bool known = dev >= 0 && dev < 64;
+  *cus = known ? count[dev].load(std::memory_order_acquire) : 0;
+  if (*cus > 0) return hipSuccess;
+  err = hipFuncSetAttribute((const void*)KERN, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err != hipSuccess) return err;
+  err = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (err == hipSuccess && known) count[dev].store(*cus, std::memory_order_release);
+  return err;
+}
+
+template <typename S, bool WIDE>
+hipError_t launch_tile_as(const LinearFp8Params& a, hipStream_t s) {
+  constexpr int PER_CU = 160 * 1024 / S::LDS;
+  static_assert(PER_CU >= 1, "two stages exceed the CU's LDS");
+  int cus = 0;
+  const hipError_t err = allow_lds<fp8_tile_kernel<S, WIDE>>(S::LDS, &cus);
+  if (err != hipSuccess) return err;
+  const int tn = (a.N + S::BN - 1) / S::BN;
+  const int64_t tm = a.tile_expert ? (int64_t)a.tiles * (a.tile / S::BM) : (a.M + S::BM - 1) / S::BM;
+  const int64_t most = (int64_t)(cus / 8) * 8 * PER_CU;
+  const int64_t grid = min(max(most, (int64_t)8), (tm * tn + 7) / 8 * 8);
+  fp8_tile_kernel<S, WIDE><<<(unsigned)grid, S::NT, S::LDS, s>>>(a, tn);
+  return hipGetLastError();
+}
+template <typename S>
+hipError_t launch_tile(const LinearFp8Params& a, hipStream_t s) {
+  return wide_rows(a) ? launch_tile_as<S, true>(a, s) : launch_tile_as<S, false>(a, s);
+}
+
+using Big = Tile<4, 2, 4, 8>;    // 256 x 256, eight wavefronts, one workgroup a CU
+using Middle = Tile<2, 2, 4, 4>; // 128 x 128, four, two a CU
+using Small = Tile<2, 2, 2, 4>;  // 64 x 128
+
 }  // namespace
 
 hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
-  const int64_t height = a.tile_expert ? a.tile : a.M;
-  if (height <= 16) return launch_stream<1>(a, s);
-  if (height <= 32) return launch_stream<2>(a, s);
-  return launch_stream<4>(a, s);
+  constexpr int64_t CUS = 256;
+  if (a.tile_expert) {
+    if (a.tile <= 16) return launch_stream<1>(a, s);
+    if (a.tile <= 32) return launch_stream<2>(a, s);
+    if (a.tile <= 64) return launch_stream<4>(a, s);
+    if (a.tile <= 128) return launch_tile<Middle>(a, s);
+    return launch_tile<Big>(a, s);
+  }
+  if (a.M <= 16) return launch_stream<1>(a, s);
+  if (a.M <= 32) return launch_stream<2>(a, s);
+  if (a.M <= 64) return launch_stream<4>(a, s);
+  auto tiles = [&](int m, int n) { return ((a.M + m - 1) / m) * ((a.N + n - 1) / n); };
+  const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS;
+  if (4 * big >= 3 * CUS * rounds) return launch_tile<Big>(a, s);
+  if (tiles(128, 128) <= CUS) return launch_tile<Small>(a, s);
+  return launch_tile<Middle>(a, s);
 }
 
 }  // namespace moe
