@@ -348,12 +348,85 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   uint32_t word[TM], later[TM];  // scale bytes of the stages from this one on, and of the next four
   float ws;
   auto load_scales = [&](int g) {
+    if (kb >= 4) {  // four bytes; a word that reaches past the row's end: its last four
+      const int at = min(4 * g, kb - 4);
 #pragma unroll
-    for (int m = 0; m < TM; m++) later[m] = scale_word(xsf + min(16 * (TM * wm + m) + r, last_m) * kb, g, kb);
+      for (int m = 0; m < TM; m++)
+        __builtin_memcpy(&later[m], xsf + min(16 * (TM * wm + m) + r, last_m) * kb + at, 4);
+    } else {
+#pragma unroll
+      for (int m = 0; m < TM; m++) {
+        const uint8_t* row = xsf + min(16 * (TM * wm + m) + r, last_m) * kb;
+        later[m] = (uint32_t)row[0] | (uint32_t)row[min(1, kb - 1)] << 8 | (uint32_t)row[kb - 1] << 16;
+      }
+    }
   };
   auto add = [&](int t, int m, const f32x4_t& v, float s) {
 #pragma unroll
     for (int i = 0; i < 4; i++) acc[t][m][i] = fmaf(v[i], s, acc[t][m][i]);
+  };
+  auto pin_all = [&]() {
+#pragma unroll
+    for (int i = 0; i < TN; i++)
+#pragma unroll
+      for (int m = 0; m < TM; m++) asm volatile("" : "+v"(acc[i][m]));
+  };
+  int buf = 0;
+  // One stage; its loads fetch stage `ahead` of what is aimed at; `wsn`: W's
+  // scale of the next stage.
+  auto stage = [&](int ahead, const float* wsn) {
+    uint8_t* st = smem + buf * S::STAGE;
+    buf ^= 1;
+    const uint8_t* sn = smem + buf * S::STAGE;
+#pragma unroll
+    for (int i = 0; i < TN - 2; i++) {
+      w[(i + 2) & 3] = read_w(st, i + 2);
+#pragma unroll
+      for (int m = 0; m < TM; m++) {
+        if (i > 0) add(i - 1, m, p[m], ws);
+        p[m] = mul(w[i & 3], x[m], (int)word[m]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // every fragment of the stage is in registers, the next stage has landed
+    stage_barrier();
+    issue(ahead, st);
+    const float wl = ws;
+    ws = ld_uniform(wsn);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < TM; m++) {
+      const f32x4_t u = mul(w[(TN - 2) & 3], x[m], (int)word[m]), v = mul(w[(TN - 1) & 3], x[m], (int)word[m]);
+      x[m] = read_x(sn, m);
+      if (m < 2) w[m] = read_w(sn, m);
+      add(TN - 3, m, p[m], wl);
+      add(TN - 2, m, u, wl);
+      add(TN - 1, m, v, wl);
+      word[m] >>= 8;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    pin_all();
+  };
+  // the scales of the four stages from s on, and the loads of those after them
+  auto next_scales = [&](int s) {
+    if ((s & 3) == 0) {
+      const int past = max(0, s + 4 - kb), shift = kb >= 4 ? 8 * min(past, 3) : 0;
+#pragma unroll
+      for (int m = 0; m < TM; m++) word[m] = later[m] >> shift;
+      if (s + 4 < KT) load_scales((s >> 2) + 1);
+    }
+  };
+  auto mask = [&](int s) {  // values past the end of K
+    if (128 * (s + 1) > a.K) {
+      const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
+#pragma unroll
+      for (int m = 0; m < TM; m++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+          x[m].lo[i] = in0 ? x[m].lo[i] : 0u;
+          x[m].hi[i] = in1 ? x[m].hi[i] : 0u;
+        }
+    }
   };
 
   At o = tile_at(t);
@@ -362,13 +435,9 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   issue(0, smem);
   issue(1, smem + S::STAGE);
   ws = ld_uniform(wsf);
-  int buf = 0;
   stage_barrier();
 #pragma unroll
-  for (int m = 0; m < TM; m++) {
-    x[m] = read_x(smem, m);
-    word[m] = later[m];
-  }
+  for (int m = 0; m < TM; m++) x[m] = read_x(smem, m);
   w[0] = read_w(smem, 0);
   w[1] = read_w(smem, 1);
 
@@ -381,54 +450,24 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
     const int64_t tn = t + step;
     const bool more = tn < last;
     const At next = more ? tile_at(tn) : o;
-    const float* wsf_of_this = wsf;
+    int s = 0;
 #pragma unroll 1
-    for (int s = 0; s < KT; s++) {
-      uint8_t* st = smem + buf * S::STAGE;
-      buf ^= 1;
-      const uint8_t* sn = smem + buf * S::STAGE;
-      if (128 * (s + 1) > a.K) {  // values past the end of K
-        const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
-#pragma unroll
-        for (int m = 0; m < TM; m++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            x[m].lo[i] = in0 ? x[m].lo[i] : 0u;
-            x[m].hi[i] = in1 ? x[m].hi[i] : 0u;
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < TN - 2; i++) {
-        w[(i + 2) & 3] = read_w(st, i + 2);
-#pragma unroll
-        for (int m = 0; m < TM; m++) {
-          if (i > 0) add(i - 1, m, p[m], ws);
-          p[m] = mul(w[i & 3], x[m], (int)word[m]);
-        }
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      // every fragment of the stage is on its way to registers, the next stage has landed
-      stage_barrier();
-      const float wl = ws;
-      if (s + 2 == KT) aim(next);
-      const int ahead = s + 2 < KT ? s + 2 : s + 2 - KT;  // of this tile or of the next one
-      issue(ahead, st);
-      ws = ld_uniform(s + 1 < KT ? wsf_of_this + min(s + 1, kb - 1) : wsf);
-      const bool fresh = s + 1 == KT || ((s + 1) & 3) == 0;
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int m = 0; m < TM; m++) {
-        const f32x4_t u = mul(w[(TN - 2) & 3], x[m], (int)word[m]), v = mul(w[(TN - 1) & 3], x[m], (int)word[m]);
-        x[m] = read_x(sn, m);
-        if (m < 2) w[m] = read_w(sn, m);
-        add(TN - 3, m, p[m], wl);
-        add(TN - 2, m, u, wl);
-        add(TN - 1, m, v, wl);
-        word[m] = fresh ? later[m] : word[m] >> 8;
-      }
-      if ((ahead & 3) == 0) load_scales(ahead >> 2);
-      __builtin_amdgcn_sched_barrier(0);
+    for (; s < KT - 2; s++) {
+      next_scales(s);
+      stage(s + 2, wsf + s + 1);
     }
+    // the last two fetch the first ones of the next tile (without one, of this
+    // tile again, unread)
+    next_scales(s);
+    mask(s);
+    const float* wl = wsf + min(s + 1, kb - 1);
+    aim(next);
+    stage(0, wl);
+    s++;
+    next_scales(s);
+    mask(s);
+    load_scales(0);
+    stage(1, wsf);
     store_tile<S, WIDE>(a, acc, o.m0 + 16 * TM * wm, o.end, o.n0 + 16 * TN * wn, smem + S::T_OFF + S::OUT * wave, lane);
     if (!more) break;
     t = tn;
