@@ -6,9 +6,8 @@
 // any fp32 value, which it does not take: the product of each 128 of K is a
 // sum of its own, from zero, that one fused multiply-add with W's scale adds to
 // the fp32 sum.
-#include <atomic>
-
 #include "device_common.h"
+#include "dynamic_lds.h"
 #include "internal.h"
 
 namespace moe {
@@ -478,25 +477,6 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
 
 bool wide_rows(const LinearFp8Params& a) {
   return !a.y_f32 && !a.accumulate && a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
-}
-
-// Allows a kernel more than the default dynamic LDS, once per device, and
-// gives the device's number of compute units.  Calls of several threads may
-// come here at once: one word says that it has been done, and is the number.
-template <auto KERN>
-hipError_t allow_lds(int bytes, int* cus) {
-  static std::atomic<int> count[64] = {};  // 0: not yet
-  int dev = 0;
-  hipError_t err = hipGetDevice(&dev);
-  if (err != hipSuccess) return err;
-  const bool known = dev >= 0 && dev < 64;
-  *cus = known ? count[dev].load(std::memory_order_acquire) : 0;
-  if (*cus > 0) return hipSuccess;
-  err = hipFuncSetAttribute((const void*)KERN, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (err != hipSuccess) return err;
-  err = hipDeviceGetAttribute(cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (err == hipSuccess && known) count[dev].store(*cus, std::memory_order_release);
-  return err;
 }
 
 template <typename S, bool WIDE>

@@ -1,93 +1,243 @@
 // wgrad_fp8.hip -- the gradient of a product's weights, dW = dy^T x, from rows of
 // x kept in 8 bits: of one matrix, or of every expert from its rows.
 //
-// x's codes are decoded to bf16 once, on their way into LDS, where both operands
-// lie with the rows (the sum's index) apart; a code times a power of two is exact
-// in bf16, so the products are exact and the sums fp32.
+// The sum runs over the rows, in which both operands are contiguous the other
+// way; gfx950's transposing LDS read (ds_read_b64_tr_b16) turns 4 rows of 16
+// values into the fragments that the matrix instruction takes.  x's codes are
+// decoded to bf16 once a workgroup, on their way into LDS: a code times a power
+// of two is exact there, so the products are exact and the sums fp32.
 #include "device_common.h"
+#include "dynamic_lds.h"
 #include "internal.h"
 
 namespace moe {
 
 namespace {
 
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) void lds_void_t;
+
 // 16 codes under one E8M0 code as bf16 pairs
-DEV void decode16(const u32x4_t& c, uint32_t code, uint32_t (&o)[8]) {
+DEV void decode16(const u32x4_t& c, uint32_t code, u32x4_t& lo, u32x4_t& hi) {
   const float s = e8m0_scale_operand(code);
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    o[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, false));
-    o[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], s, true));
+    const uint32_t v = c[i];
+    const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, s, false);
+    const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, s, true);
+    u32x4_t& o = i < 2 ? lo : hi;
+    o[2 * (i & 1)] = __builtin_bit_cast(uint32_t, a);
+    o[2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, b);
   }
 }
 
-constexpr int BN = 128, BK = 128, ST = 32;
+// s_waitcnt immediates (gfx9 encoding): vmcnt(n), LDS accesses all done
+constexpr int waitcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
 
-__global__ __launch_bounds__(256) void wgrad_simple_kernel(const WgradParams a, int tiles_n, int tiles_k) {
-  constexpr int P = ST + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t dn[BN * P], xk[BK * P];
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int e = blockIdx.x / (tiles_n * tiles_k), t = blockIdx.x - e * tiles_n * tiles_k;
-  const int n0 = t / tiles_k * BN, k0 = t % tiles_k * BK;
+template <int TN_, int TK_>
+struct Tile {
+  static constexpr int TN = TN_, TK = TK_;        // 16 x 16 results of a wavefront, four of them as 2 x 2
+  static constexpr int BN = 32 * TN, BK = 32 * TK;
+  static constexpr int ST = 32;                   // rows of a stage
+  static constexpr int PN = 2 * BN, PK = 2 * BK;  // bytes of a row in LDS
+  static constexpr int STAGE = ST * (PN + PK);
+  static constexpr int NBUF = 3;
+  static constexpr int LDS = NBUF * STAGE;
+  static constexpr int ND = ST * PN / 4096;       // LDS-DMA loads of dy a wavefront and stage
+  static constexpr int NX = ST * BK / 4096;       // 16-byte loads of x a thread and stage
+};
+
+// The units of 32 bytes (16 values) of row m are swizzled by this, so that the
+// eight rows that half a wavefront's transposing read takes (0 - 3 and 8 - 11
+// past a multiple of 16, or four more) lie in different banks.
+template <int P>
+DEV int swizzle(int m) {
+  if constexpr (P >= 256) return (m & 3) | (((m >> 3) & 1) << 2);
+  else return ((m >> 1) & 1) | (((m >> 3) & 1) << 1);
+}
+
+// One tile of dW a workgroup.  dy goes into LDS by LDS-DMA two stages ahead, x
+// through registers: loaded two stages ahead, decoded and written one ahead.
+// Rows past the end of the range are read as 0 (the buffers end there).
+template <typename S>
+__global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
+  constexpr int TN = S::TN, TK = S::TK, PN = S::PN, PK = S::PK, ND = S::ND, NX = S::NX;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wk = wave >> 1;
+
+  // tile of this workgroup: the XCDs (workgroups are dealt to them round robin)
+  // take contiguous runs of tiles, 8 tiles of n high, so that those an XCD works on
+  // share their rows in its L2
+  const int64_t tiles = (int64_t)a.experts * tiles_n * tiles_k, per = (tiles + 7) / 8;
+  const int64_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
+  if (t >= tiles || (int64_t)(blockIdx.x >> 3) >= per) return;
+  const int e = (int)(t / (tiles_n * tiles_k)), in_e = (int)(t - (int64_t)e * tiles_n * tiles_k);
+  constexpr int GM = 8;
+  const int group = in_e / (GM * tiles_k), in = in_e - group * GM * tiles_k;
+  const int high = min(GM, tiles_n - group * GM);
+  const int n0 = (group * GM + in % high) * S::BN, k0 = in / high * S::BK;
+
   const int64_t first = a.offsets ? ld_uniform(a.offsets + e) : 0;
-  const int64_t end = a.offsets ? first + ld_uniform(a.counts + e) : a.M;
+  const int64_t rows = a.offsets ? ld_uniform(a.counts + e) : a.M;
+  const int stages = (int)((rows + S::ST - 1) / S::ST);
   const int nb = (a.K + 127) / 128;
-  f32x4_t acc[4][4];
+
+  // LDS-DMA of dy: lane's row of a load and its chunk of 16 bytes, swizzled at
+  // the source (a load fills LDS in lane order)
+  constexpr int RD = 1024 / PN;  // rows of a load
+  uint32_t dy_at[ND];
 #pragma unroll
-  for (int i = 0; i < 4; i++)
-#pragma unroll
-    for (int j = 0; j < 4; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-  const int wn = 64 * (wave & 1), wk = 64 * (wave >> 1), r = lane & 15, q = lane >> 4;
-  for (int64_t m0 = first; m0 < end; m0 += ST) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-      const int m = (tid >> 4) + 16 * i, n = 8 * (tid & 15);
-      u32x4_t v = {0u, 0u, 0u, 0u};
-      if (m0 + m < end && n0 + n < a.N) v = *reinterpret_cast<const u32x4_t*>(a.dy + (m0 + m) * a.N + n0 + n);
-#pragma unroll
-      for (int j = 0; j < 8; j++) dn[(n + j) * P + m] = (uint16_t)(v[j >> 1] >> (16 * (j & 1)));
-    }
-    {
-      const int m = tid >> 3, k = 16 * (tid & 7);
-      uint32_t o[8] = {};
-      if (m0 + m < end && k0 + k < a.K)
-        decode16(*reinterpret_cast<const u32x4_t*>(a.x + (m0 + m) * a.K + k0 + k),
-                 a.x_sf[(m0 + m) * nb + (k0 >> 7)], o);
-#pragma unroll
-      for (int j = 0; j < 16; j++) xk[(k + j) * P + m] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
-    }
-    __syncthreads();
-    bf16x8_t f[4], g[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      f[i] = *reinterpret_cast<const bf16x8_t*>(dn + (wn + 16 * i + r) * P + 8 * q);
-      g[i] = *reinterpret_cast<const bf16x8_t*>(xk + (wk + 16 * i + r) * P + 8 * q);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; i++)
-#pragma unroll
-      for (int j = 0; j < 4; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i], g[j], acc[i][j], 0, 0, 0);
+  for (int i = 0; i < ND; i++) {
+    const int m = RD * (ND * wave + i) + lane / (PN / 16), c = lane % (PN / 16);
+    dy_at[i] = (uint32_t)m * (uint32_t)(2 * a.N) + 16 * (((c >> 1) ^ swizzle<PN>(m)) * 2 + (c & 1));
   }
+  auto load_dy = [&](int s, int buf) {
+    const int64_t m0 = first + (int64_t)s * S::ST;
+    const int left = (int)min((int64_t)S::ST, max((int64_t)0, rows - (int64_t)s * S::ST));
+    // (columns past N: of the next row, not stored)
+    const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint16_t*>(a.dy + m0 * a.N + n0), 0, left > 0 ? left * 2 * a.N - 2 * n0 : 0, 0x00020000);
 #pragma unroll
-  for (int i = 0; i < 4; i++)
+    for (int i = 0; i < ND; i++) {
+      const uint32_t at = dy_at[i] + 0u;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void_t*)(smem + buf * S::STAGE + 1024 * (ND * wave + i)), 16, at,
+                                               0, 0, 0);
+    }
+  };
+  // x: thread's rows of a stage, 16 codes of each
+  constexpr int CX = S::BK / 16;  // threads a row
+  const int xm = tid / CX, xc = tid % CX;
+  const bool inside = k0 + 16 * xc < a.K;
+  struct Codes {
+    u32x4_t q[NX];
+    uint32_t sf[NX];
+  };
+  auto load_x = [&](int s, Codes& o) {
+    const int64_t m0 = first + (int64_t)s * S::ST;
+    const int left = (int)min((int64_t)S::ST, max((int64_t)0, rows - (int64_t)s * S::ST));
+    const __amdgpu_buffer_rsrc_t b =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x + m0 * a.K), 0, left * a.K, 0x00020000);
+    const __amdgpu_buffer_rsrc_t f =
+        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x_sf + m0 * nb), 0, left * nb, 0x00020000);
 #pragma unroll
-    for (int j = 0; j < 4; j++)
+    for (int i = 0; i < NX; i++) {
+      const int m = xm + 256 / CX * i;
+      const uint32_t past = 0x80000000u;  // (reads as 0)
+      o.q[i] = __builtin_amdgcn_raw_buffer_load_b128(b, inside ? (uint32_t)(m * a.K + k0 + 16 * xc) : past, 0, 0);
+      o.sf[i] = __builtin_amdgcn_raw_buffer_load_b8(f, inside ? (uint32_t)(m * nb + ((k0 + 16 * xc) >> 7)) : past, 0, 0);
+    }
+  };
+  auto store_x = [&](const Codes& o, int buf) {
 #pragma unroll
-      for (int c = 0; c < 4; c++) {
-        const int n = n0 + wn + 16 * i + 4 * q + c, k = k0 + wk + 16 * j + r;
-        if (n >= a.N || k >= a.K) continue;
-        float* p = a.dw + ((int64_t)e * a.N + n) * a.K + k;
-        *p = a.accumulate ? *p + acc[i][j][c] : acc[i][j][c];
+    for (int i = 0; i < NX; i++) {
+      const int m = xm + 256 / CX * i;
+      u32x4_t lo, hi;
+      decode16(o.q[i], o.sf[i], lo, hi);
+      uint8_t* p = smem + buf * S::STAGE + S::ST * PN + m * PK + 32 * (xc ^ swizzle<PK>(m));
+      *reinterpret_cast<u32x4_t*>(p) = lo;
+      *reinterpret_cast<u32x4_t*>(p + 16) = hi;
+    }
+  };
+
+  // fragments: of 16 columns, rows 8 q .. 8 q + 7, by two reads whose lane
+  // addresses 4 columns of one row
+  const int fm = 8 * q + (r >> 2);
+  const int dy_frag = fm * PN + 32 * swizzle<PN>(fm) + 8 * (r & 3);
+  const int x_frag = S::ST * PN + fm * PK + 32 * swizzle<PK>(fm) + 8 * (r & 3);
+  auto frag = [&](int at, int pitch) {
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(smem + at));
+    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(smem + at + 4 * pitch));
+    typedef short i16x8_t __attribute__((ext_vector_type(8)));
+    const i16x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8_t, v);
+  };
+
+  f32x4_t acc[TK][TN];
+#pragma unroll
+  for (int i = 0; i < TK; i++)
+#pragma unroll
+    for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (stages > 0) {
+    Codes x0, x1;
+    load_x(0, x0);
+    load_dy(0, 0);
+    load_x(1, x1);
+    load_dy(1, 1);
+    store_x(x0, 0);
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    int buf = 0;
+    // stage s: x of the next one is in `next`, that of the one after it goes to `later`
+    auto stage = [&](int s, Codes& next, Codes& later) {
+      const int b1 = buf == 2 ? 0 : buf + 1, b2 = b1 == 2 ? 0 : b1 + 1;
+      load_x(s + 2, later);
+      load_dy(s + 2, b2);
+      const int base = buf * S::STAGE;
+      bf16x8_t d[TN];
+#pragma unroll
+      for (int j = 0; j < TN; j++) d[j] = frag((base + dy_frag) ^ (32 * (TN * wn + j)), PN);
+#pragma unroll
+      for (int i = 0; i < TK; i++) {
+        const bf16x8_t f = frag((base + x_frag) ^ (32 * (TK * wk + i)), PK);
+#pragma unroll
+        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, d[j], acc[i][j], 0, 0, 0);
       }
+      store_x(next, b1);
+      // the next stage's dy has landed: all but this stage's loads are done
+      __builtin_amdgcn_s_waitcnt(waitcnt(ND + 2 * NX));
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      buf = b1;
+    };
+    int s = 0;
+#pragma unroll 1
+    for (; s + 1 < stages; s += 2) {
+      stage(s, x1, x0);
+      stage(s + 1, x0, x1);
+    }
+    if (s < stages) stage(s, x1, x0);
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));  // no LDS-DMA load may be in flight when the workgroup ends
+  }
+
+  // element i of lane (r, q): k = 4 q + i, n = r
+  float* dw = a.dw + (int64_t)e * a.N * a.K;
+#pragma unroll
+  for (int j = 0; j < TN; j++) {
+    const int n = n0 + 16 * (TN * wn + j) + r;
+#pragma unroll
+    for (int i = 0; i < TK; i++) {
+      const int k = k0 + 16 * (TK * wk + i) + 4 * q;
+      if (n >= a.N || k >= a.K) continue;
+      f32x4_t* p = reinterpret_cast<f32x4_t*>(dw + (int64_t)n * a.K + k);
+      *p = a.accumulate ? *p + acc[i][j] : acc[i][j];
+    }
+  }
+}
+
+template <typename S>
+hipError_t launch(const WgradParams& a, hipStream_t s) {
+  const int tn = (a.N + S::BN - 1) / S::BN, tk = (a.K + S::BK - 1) / S::BK;
+  int cus = 0;
+  const hipError_t err = allow_lds<wgrad_kernel<S>>(S::LDS, &cus);
+  if (err != hipSuccess) return err;
+  const int64_t grid = ((int64_t)a.experts * tn * tk + 7) / 8 * 8;
+  wgrad_kernel<S><<<(unsigned)grid, 256, S::LDS, s>>>(a, tn, tk);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_wgrad_fp8(const WgradParams& a, hipStream_t s) {
-  const int tn = (a.N + BN - 1) / BN, tk = (a.K + BK - 1) / BK;
-  wgrad_simple_kernel<<<(unsigned)((int64_t)a.experts * tn * tk), 256, 0, s>>>(a, tn, tk);
-  return hipGetLastError();
+  constexpr int64_t CUS = 256;
+  const int64_t large = (int64_t)a.experts * ((a.N + 127) / 128) * ((a.K + 255) / 256);
+  if (large < CUS) return launch<Tile<2, 4>>(a, s);
+  return launch<Tile<4, 8>>(a, s);
 }
 
 }  // namespace moe
