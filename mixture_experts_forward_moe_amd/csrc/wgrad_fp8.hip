@@ -16,7 +16,6 @@ namespace {
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-typedef __attribute__((address_space(3))) void lds_void_t;
 
 // 16 codes under one E8M0 code as bf16 pairs
 DEV void decode16(const u32x4_t& c, uint32_t code, u32x4_t& lo, u32x4_t& hi) {
@@ -32,8 +31,14 @@ DEV void decode16(const u32x4_t& c, uint32_t code, u32x4_t& lo, u32x4_t& hi) {
   }
 }
 
-// s_waitcnt immediates (gfx9 encoding): vmcnt(n), LDS accesses all done
-constexpr int waitcnt(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
+// workgroup barrier over LDS that waits for this wavefront's LDS accesses only (a
+// release fence would also wait for every load in flight)
+DEV void stage_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 template <int TN_, int TK_>
 struct Tile {
@@ -42,10 +47,9 @@ struct Tile {
   static constexpr int ST = 32;                   // rows of a stage
   static constexpr int PN = 2 * BN, PK = 2 * BK;  // bytes of a row in LDS
   static constexpr int STAGE = ST * (PN + PK);
-  static constexpr int NBUF = 3;
-  static constexpr int LDS = NBUF * STAGE;
-  static constexpr int ND = ST * PN / 4096;       // LDS-DMA loads of dy a wavefront and stage
-  static constexpr int NX = ST * BK / 4096;       // 16-byte loads of x a thread and stage
+  static constexpr int LDS = 2 * STAGE;
+  static constexpr int ND = ST * PN / 4096;       // 16-byte loads of dy a thread and stage
+  static constexpr int NX = ST * BK / 4096;       // and of x
 };
 
 // The units of 32 bytes (16 values) of row m are swizzled by this, so that the
@@ -57,9 +61,11 @@ DEV int swizzle(int m) {
   else return ((m >> 1) & 1) | (((m >> 3) & 1) << 1);
 }
 
-// One tile of dW a workgroup.  dy goes into LDS by LDS-DMA two stages ahead, x
-// through registers: loaded two stages ahead, decoded and written one ahead.
-// Rows past the end of the range are read as 0 (the buffers end there).
+// One tile of dW a workgroup.  Both operands go through registers: loaded two
+// stages ahead, written into LDS one ahead.  (LDS-DMA of dy is slower: the
+// compiler cannot tell its target from what a transposing read takes, and waits
+// for all of it.)  Rows past the end of the range are read as 0: the buffers
+// end there.
 template <typename S>
 __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
   constexpr int TN = S::TN, TK = S::TK, PN = S::PN, PK = S::PK, ND = S::ND, NX = S::NX;
@@ -84,60 +90,50 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
   const int stages = (int)((rows + S::ST - 1) / S::ST);
   const int nb = (a.K + 127) / 128;
 
-  // LDS-DMA of dy: lane's row of a load and its chunk of 16 bytes, swizzled at
-  // the source (a load fills LDS in lane order)
-  constexpr int RD = 1024 / PN;  // rows of a load
-  uint32_t dy_at[ND];
-#pragma unroll
-  for (int i = 0; i < ND; i++) {
-    const int m = RD * (ND * wave + i) + lane / (PN / 16), c = lane % (PN / 16);
-    dy_at[i] = (uint32_t)m * (uint32_t)(2 * a.N) + 16 * (((c >> 1) ^ swizzle<PN>(m)) * 2 + (c & 1));
-  }
-  auto load_dy = [&](int s, int buf) {
-    const int64_t m0 = first + (int64_t)s * S::ST;
-    const int left = (int)min((int64_t)S::ST, max((int64_t)0, rows - (int64_t)s * S::ST));
-    // (columns past N: of the next row, not stored)
-    const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(a.dy + m0 * a.N + n0), 0, left > 0 ? left * 2 * a.N - 2 * n0 : 0, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < ND; i++) {
-      const uint32_t at = dy_at[i] + 0u;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_void_t*)(smem + buf * S::STAGE + 1024 * (ND * wave + i)), 16, at,
-                                               0, 0, 0);
-    }
-  };
-  // x: thread's rows of a stage, 16 codes of each
-  constexpr int CX = S::BK / 16;  // threads a row
-  const int xm = tid / CX, xc = tid % CX;
+  // thread's rows of a stage and the 16 bytes it loads of each: 8 values of dy, 16
+  // codes of x (columns past the end of a row of dy: of the next row, not stored)
+  constexpr int CD = S::BN / 8, CX = S::BK / 16;  // threads a row
+  const int dm = tid / CD, dc = tid % CD, xm = tid / CX, xc = tid % CX;
   const bool inside = k0 + 16 * xc < a.K;
-  struct Codes {
-    u32x4_t q[NX];
+  const uint32_t past = 0x80000000u;  // (reads as 0)
+  struct Rows {
+    u32x4_t d[ND], q[NX];
     uint32_t sf[NX];
   };
-  auto load_x = [&](int s, Codes& o) {
+  auto load = [&](int s, Rows& o) {
     const int64_t m0 = first + (int64_t)s * S::ST;
     const int left = (int)min((int64_t)S::ST, max((int64_t)0, rows - (int64_t)s * S::ST));
-    const __amdgpu_buffer_rsrc_t b =
+    const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.dy + m0 * a.N), 0,
+                                                                       left * 2 * a.N, 0x00020000);
+    const __amdgpu_buffer_rsrc_t c =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x + m0 * a.K), 0, left * a.K, 0x00020000);
     const __amdgpu_buffer_rsrc_t f =
         __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x_sf + m0 * nb), 0, left * nb, 0x00020000);
 #pragma unroll
     for (int i = 0; i < NX; i++) {
       const int m = xm + 256 / CX * i;
-      const uint32_t past = 0x80000000u;  // (reads as 0)
-      o.q[i] = __builtin_amdgcn_raw_buffer_load_b128(b, inside ? (uint32_t)(m * a.K + k0 + 16 * xc) : past, 0, 0);
+      o.q[i] = __builtin_amdgcn_raw_buffer_load_b128(c, inside ? (uint32_t)(m * a.K + k0 + 16 * xc) : past, 0, 0);
       o.sf[i] = __builtin_amdgcn_raw_buffer_load_b8(f, inside ? (uint32_t)(m * nb + ((k0 + 16 * xc) >> 7)) : past, 0, 0);
     }
+#pragma unroll
+    for (int i = 0; i < ND; i++)
+      o.d[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)((dm + 256 / CD * i) * 2 * a.N + 2 * n0 + 16 * dc), 0, 0);
   };
-  auto store_x = [&](const Codes& o, int buf) {
+  auto store = [&](const Rows& o, int buf) {
+    uint8_t* st = smem + buf * S::STAGE;
 #pragma unroll
     for (int i = 0; i < NX; i++) {
       const int m = xm + 256 / CX * i;
       u32x4_t lo, hi;
       decode16(o.q[i], o.sf[i], lo, hi);
-      uint8_t* p = smem + buf * S::STAGE + S::ST * PN + m * PK + 32 * (xc ^ swizzle<PK>(m));
+      uint8_t* p = st + S::ST * PN + m * PK + 32 * (xc ^ swizzle<PK>(m));
       *reinterpret_cast<u32x4_t*>(p) = lo;
       *reinterpret_cast<u32x4_t*>(p + 16) = hi;
+    }
+#pragma unroll
+    for (int i = 0; i < ND; i++) {
+      const int m = dm + 256 / CD * i;
+      *reinterpret_cast<u32x4_t*>(st + m * PN + 32 * ((dc >> 1) ^ swizzle<PN>(m)) + 16 * (dc & 1)) = o.d[i];
     }
   };
 
@@ -161,23 +157,17 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
     for (int j = 0; j < TN; j++) acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (stages > 0) {
-    Codes x0, x1;
-    load_x(0, x0);
-    load_dy(0, 0);
-    load_x(1, x1);
-    load_dy(1, 1);
-    store_x(x0, 0);
-    __builtin_amdgcn_s_waitcnt(waitcnt(0));
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
+    Rows x0, x1;
+    load(0, x0);
+    load(1, x1);
+    store(x0, 0);
+    stage_barrier();
     int buf = 0;
-    // stage s: x of the next one is in `next`, that of the one after it goes to `later`
-    auto stage = [&](int s, Codes& next, Codes& later) {
-      const int b1 = buf == 2 ? 0 : buf + 1, b2 = b1 == 2 ? 0 : b1 + 1;
-      load_x(s + 2, later);
-      load_dy(s + 2, b2);
+    // stage s: the rows of the next one are in `next`, those of the one after it go to `later`
+    auto stage = [&](int s, Rows& next, Rows& later) {
+      load(s + 2, later);
       const int base = buf * S::STAGE;
+      buf ^= 1;
       bf16x8_t d[TN];
 #pragma unroll
       for (int j = 0; j < TN; j++) d[j] = frag((base + dy_frag) ^ (32 * (TN * wn + j)), PN);
@@ -187,13 +177,8 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
 #pragma unroll
         for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, d[j], acc[i][j], 0, 0, 0);
       }
-      store_x(next, b1);
-      // the next stage's dy has landed: all but this stage's loads are done
-      __builtin_amdgcn_s_waitcnt(waitcnt(ND + 2 * NX));
-      asm volatile("" ::: "memory");
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      buf = b1;
+      store(next, buf);
+      stage_barrier();
     };
     int s = 0;
 #pragma unroll 1
@@ -202,7 +187,6 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
       stage(s + 1, x0, x1);
     }
     if (s < stages) stage(s, x1, x0);
-    __builtin_amdgcn_s_waitcnt(waitcnt(0));  // no LDS-DMA load may be in flight when the workgroup ends
   }
 
   // element i of lane (r, q): k = 4 q + i, n = r
