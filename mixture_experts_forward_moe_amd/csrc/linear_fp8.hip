@@ -233,7 +233,7 @@ DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
 template <typename S, bool WIDE>
 __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Params a, int tiles_n) {
   constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW;
-  static_assert(TN % 4 == 0 && NX % 2 == 0 && NW % 2 == 0, "four buffers of W; the swizzle goes by a load's number");
+  static_assert(TN % 4 == 0 && NX >= 1 && NW >= 1, "four buffers of W; whole loads");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -301,16 +301,17 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   };
   // (a chunk past the end of K: the row's first one)
   auto issue = [&](int s, uint8_t* st) {
-    uint32_t k[2];
+    uint32_t k[2];  // of loads of even and odd number
 #pragma unroll
     for (int v = 0; v < 2; v++) {
       k[v] = (uint32_t)(128 * s + (chunk ^ (64 * v)));
       k[v] = k[v] < (uint32_t)a.K ? k[v] : 0u;
     }
+    const uint32_t kx[2] = {NX % 2 && (wave & 1) ? k[1] : k[0], NX % 2 && (wave & 1) ? k[0] : k[1]};
 #pragma unroll
     for (int i = 0; i < NX; i++)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(xb, (lds_void_t*)(st + 1024 * (NX * wave + i)), 16,
-                                               place_x + k[i & 1] + (uint32_t)(8 * i * a.K), 0, 0, 0);
+                                               place_x + kx[i & 1] + (uint32_t)(8 * i * a.K), 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < NW; i++) {
       const int j = 8 * (NW * wave + i), in = j % (16 * TN);  // the load's first row of LDS
@@ -501,6 +502,7 @@ hipError_t launch_tile(const LinearFp8Params& a, hipStream_t s) {
 using Big = Tile<4, 2, 4, 8>;    // 256 x 256, eight wavefronts, one workgroup a CU
 using Middle = Tile<2, 2, 4, 4>; // 128 x 128, four, two a CU
 using Small = Tile<2, 2, 2, 4>;  // 64 x 128
+using Low = Tile<1, 4, 2, 4>;    // 32 x 256
 
 }  // namespace
 
@@ -508,8 +510,8 @@ hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
   constexpr int64_t CUS = 256;
   if (a.tile_expert) {
     if (a.tile <= 16) return launch_stream<1>(a, s);
-    if (a.tile <= 32) return launch_stream<2>(a, s);
-    if (a.tile <= 64) return launch_stream<4>(a, s);
+    if (a.tile <= 32) return launch_tile<Low>(a, s);
+    if (a.tile <= 64) return launch_tile<Small>(a, s);
     if (a.tile <= 128) return launch_tile<Middle>(a, s);
     return launch_tile<Big>(a, s);
   }

@@ -73,15 +73,14 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
   const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wk = wave >> 1;
 
-  // tile of this workgroup: the XCDs (workgroups are dealt to them round robin)
-  // take contiguous runs of tiles, 8 tiles of n high, so that those an XCD works on
-  // share their rows in its L2
-  const int64_t tiles = (int64_t)a.experts * tiles_n * tiles_k, per = (tiles + 7) / 8;
-  const int64_t t = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-  if (t >= tiles || (int64_t)(blockIdx.x >> 3) >= per) return;
-  const int e = (int)(t / (tiles_n * tiles_k)), in_e = (int)(t - (int64_t)e * tiles_n * tiles_k);
+  // tile of this workgroup: an XCD (workgroups are dealt to them round robin) takes
+  // a run of every expert's tiles, so that experts with many rows cost all XCDs the
+  // same, 8 tiles of n high, so that those it works on share their rows in its L2
+  const int tiles = tiles_n * tiles_k, per = (tiles + 7) / 8;
+  const int slot = blockIdx.x >> 3, e = slot / per, t = (blockIdx.x & 7) * per + slot - e * per;
+  if (e >= a.experts || t >= tiles) return;
   constexpr int GM = 8;
-  const int group = in_e / (GM * tiles_k), in = in_e - group * GM * tiles_k;
+  const int group = t / (GM * tiles_k), in = t - group * GM * tiles_k;
   const int high = min(GM, tiles_n - group * GM);
   const int n0 = (group * GM + in % high) * S::BN, k0 = in / high * S::BK;
 
@@ -210,7 +209,7 @@ hipError_t launch(const WgradParams& a, hipStream_t s) {
   int cus = 0;
   const hipError_t err = allow_lds<wgrad_kernel<S>>(S::LDS, &cus);
   if (err != hipSuccess) return err;
-  const int64_t grid = ((int64_t)a.experts * tn * tk + 7) / 8 * 8;
+  const int64_t grid = ((int64_t)tn * tk + 7) / 8 * 8 * a.experts;
   wgrad_kernel<S><<<(unsigned)grid, 256, S::LDS, s>>>(a, tn, tk);
   return hipGetLastError();
 }
