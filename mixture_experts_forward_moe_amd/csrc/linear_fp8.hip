@@ -186,24 +186,26 @@ hipError_t launch_stream(const LinearFp8Params& a, hipStream_t s) {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 
-// Workgroup barrier: this wavefront's LDS accesses and its loads are done
-// (written out: a release fence would not say which loads).
+// Workgroup barrier: this wavefront's LDS accesses are done, and its loads but for
+// the newest VM (written out: a release fence would wait for all of them).
+template <int VM>
 DEV void stage_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | (7 << 4));  // vmcnt(VM) lgkmcnt(0)
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
 
-template <int WM_, int WN_, int TM_, int TN_>
+template <int WM_, int WN_, int TM_, int TN_, int NBUF_>
 struct Tile {
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // wavefronts, 16 x 16 results of each
+  static constexpr int NBUF = NBUF_;                            // stages in LDS
   static constexpr int NT = 64 * WM * WN;
   static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
   static constexpr int X_BYTES = BM * 128;
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int OUT = 16 * 16 * TN * 2;                  // a wavefront's way out: 16 rows
-  static constexpr int T_OFF = 2 * STAGE;
+  static constexpr int T_OFF = NBUF * STAGE;
   static constexpr int LDS = T_OFF + WM * WN * OUT;
   static constexpr int NX = BM * 8 / NT, NW = BN * 8 / NT;      // LDS-DMA loads a wavefront and stage
 };
@@ -222,7 +224,7 @@ DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
   return v;
 }
 
-// One workgroup a tile at a time, K in stages of 128 in two buffers that
+// One workgroup a tile at a time, K in stages of 128 in a ring of buffers that
 // LDS-DMA fills.  A wavefront computes 16 TM rows by 16 TN columns, W's rows the
 // first operand: a lane then has 4 TN consecutive columns of one row of y, if
 // row 4 a + b of W's tile t is column 4 TN a + 4 t + b.  The rows' fragments
@@ -232,13 +234,13 @@ DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
 // on both sides.
 template <typename S, bool WIDE>
 __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Params a, int tiles_n) {
-  constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW;
+  constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW, NBUF = S::NBUF;
   static_assert(TN % 4 == 0 && NX >= 1 && NW >= 1, "four buffers of W; whole loads");
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wn = wave % S::WN, wm = wave / S::WN;
-  const int kb = (a.K + 127) / 128, KT = max(kb, 2);
+  const int kb = (a.K + 127) / 128, KT = max(kb, NBUF);
 
   // tiles of this workgroup: XCD b & 7 takes a contiguous run of them, its
   // workgroups take them in turn; 8 rows of tiles high, so that what an XCD
@@ -376,7 +378,7 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   // scale of the next stage.
   auto stage = [&](int ahead, const float* wsn) {
     uint8_t* st = smem + buf * S::STAGE;
-    buf ^= 1;
+    buf = buf == NBUF - 1 ? 0 : buf + 1;
     const uint8_t* sn = smem + buf * S::STAGE;
 #pragma unroll
     for (int i = 0; i < TN - 2; i++) {
@@ -389,7 +391,7 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
       __builtin_amdgcn_sched_barrier(0);
     }
     // every fragment of the stage is in registers, the next stage has landed
-    stage_barrier();
+    stage_barrier<(NBUF - 2) * (NX + NW)>();
     issue(ahead, st);
     const float wl = ws;
     ws = ld_uniform(wsn);
@@ -432,10 +434,10 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   At o = tile_at(t);
   aim(o);
   load_scales(0);
-  issue(0, smem);
-  issue(1, smem + S::STAGE);
+#pragma unroll
+  for (int i = 0; i < NBUF; i++) issue(i, smem + i * S::STAGE);
   ws = ld_uniform(wsf);
-  stage_barrier();
+  stage_barrier<(NBUF - 1) * (NX + NW)>();
 #pragma unroll
   for (int m = 0; m < TM; m++) x[m] = read_x(smem, m);
   w[0] = read_w(smem, 0);
@@ -452,22 +454,21 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
     const At next = more ? tile_at(tn) : o;
     int s = 0;
 #pragma unroll 1
-    for (; s < KT - 2; s++) {
+    for (; s < KT - NBUF; s++) {
       next_scales(s);
-      stage(s + 2, wsf + s + 1);
+      stage(s + NBUF, wsf + s + 1);
     }
-    // the last two fetch the first ones of the next tile (without one, of this
+    // the last ones fetch the first ones of the next tile (without one, of this
     // tile again, unread)
-    next_scales(s);
-    mask(s);
-    const float* wl = wsf + min(s + 1, kb - 1);
-    aim(next);
-    stage(0, wl);
-    s++;
-    next_scales(s);
-    mask(s);
-    load_scales(0);
-    stage(1, wsf);
+    const float* of_this = wsf;
+#pragma unroll
+    for (int i = 0; i < NBUF; i++, s++) {
+      next_scales(s);
+      mask(s);
+      if (i == 0) aim(next);
+      if (i == NBUF - 1) load_scales(0);
+      stage(i, i == NBUF - 1 ? wsf : of_this + min(s + 1, kb - 1));
+    }
     store_tile<S, WIDE>(a, acc, o.m0 + 16 * TM * wm, o.end, o.n0 + 16 * TN * wn, smem + S::T_OFF + S::OUT * wave, lane);
     if (!more) break;
     t = tn;
@@ -499,10 +500,10 @@ hipError_t launch_tile(const LinearFp8Params& a, hipStream_t s) {
   return wide_rows(a) ? launch_tile_as<S, true>(a, s) : launch_tile_as<S, false>(a, s);
 }
 
-using Big = Tile<4, 2, 4, 8>;    // 256 x 256, eight wavefronts, one workgroup a CU
-using Middle = Tile<2, 2, 4, 4>; // 128 x 128, four, two a CU
-using Small = Tile<2, 2, 2, 4>;  // 64 x 128
-using Low = Tile<1, 4, 2, 4>;    // 32 x 256
+using Big = Tile<4, 2, 4, 8, 2>;    // 256 x 256, eight wavefronts, one workgroup a CU
+using Middle = Tile<2, 2, 4, 4, 2>; // 128 x 128, four, two a CU
+using Small = Tile<2, 2, 2, 4, 3>;  // 64 x 128
+using Low = Tile<1, 4, 2, 4, 2>;    // 32 x 256
 
 }  // namespace
 
