@@ -6,6 +6,8 @@
 // any fp32 value, which it does not take: the product of each 128 of K is a
 // sum of its own, from zero, that one fused multiply-add with W's scale adds to
 // the fp32 sum.
+#include <type_traits>
+
 #include "device_common.h"
 #include "dynamic_lds.h"
 #include "internal.h"
@@ -23,23 +25,21 @@ struct Group {
   const float* w_sf;
 };
 
-// group g of rows of `height` (with a plan: part of one of its tiles)
-DEV bool group_of(const LinearFp8Params& a, int g, int height, Group& o) {
+// group g of 16 rows: a plan's tile, which has as many
+DEV bool group_of(const LinearFp8Params& a, int g, Group& o) {
+  o.first = (int64_t)g * 16;
   if (!a.tile_expert) {
-    o.first = (int64_t)g * height;
-    o.end = min(a.M, o.first + height);
+    o.end = min(a.M, o.first + 16);
     o.w = a.w;
     o.w_sf = a.w_sf;
-    return o.first < o.end;
+    return true;
   }
-  const int parts = max(1, a.tile / height), t = g / parts;
-  const int e = ld_uniform(a.tile_expert + t);
+  const int e = ld_uniform(a.tile_expert + g);
   if (e < 0) return false;
-  o.first = (int64_t)t * a.tile + (g - t * parts) * height;
-  o.end = min(o.first + height, (int64_t)ld_uniform(a.tile_limit + t));
+  o.end = ld_uniform(a.tile_limit + g);
   o.w = a.w + (int64_t)e * a.N * a.K;
   o.w_sf = a.w_sf + (int64_t)e * ((a.N + 127) / 128) * ((a.K + 127) / 128);
-  return o.first < o.end;
+  return true;
 }
 
 // ------------------------------------------------------------- way out
@@ -95,13 +95,44 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
       wave_fence();  // and written again once they have been
     } else {
       if (row0 + r >= end) continue;
+      const int64_t at = (row0 + r) * a.N + n;
+      // sixteen bytes at a time where y allows it
+      const bool four = a.y_f32 && a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0;
+      const bool eight = !a.y_f32 && a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
 #pragma unroll
-      for (int t = 0; t < TN; t++)
+      for (int c = 0; c < TN / 2; c++) {
+        const int col = n + 8 * c;
+        if (col >= a.N) continue;
+        float v[8];
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const int col = n + 4 * t + i;
-          if (col < a.N) store_one(a, row0 + r, col, a.bias ? acc[t][m][i] + a.bias[col] : acc[t][m][i]);
+        for (int i = 0; i < 8; i++) {
+          v[i] = acc[2 * c + (i >> 2)][m][i & 3];
+          if (a.bias) v[i] += a.bias[min(col + i, a.N - 1)];
         }
+        if (four) {
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            f32x4_t* p = reinterpret_cast<f32x4_t*>(reinterpret_cast<float*>(a.y) + at + 8 * c + 4 * h);
+            if (col + 4 * h >= a.N) continue;
+            f32x4_t o = {v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]};
+            if (a.accumulate) o = *p + o;
+            *p = o;
+          }
+        } else if (eight) {
+          u32x4_t* p = reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.y) + at + 8 * c);
+          const u32x4_t old = a.accumulate ? *p : u32x4_t{0u, 0u, 0u, 0u};
+          u32x4_t o;
+#pragma unroll
+          for (int i = 0; i < 4; i++)
+            o[i] = pack_bf16x2(__uint_as_float(old[i] << 16) + v[2 * i],
+                               __uint_as_float(old[i] & 0xffff0000u) + v[2 * i + 1]);
+          *p = o;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; i++)
+            if (col + i < a.N) store_one(a, row0 + r, col + i, v[i]);
+        }
+      }
     }
   }
 }
@@ -110,75 +141,60 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
 
 constexpr int STREAM_WAVES = 8;
 
-// 16 MT rows of x a workgroup: it streams 16 rows of W once, its wavefronts
-// splitting K, straight into registers; their sums meet in LDS in a fixed order.
+// 16 rows of x and 16 of W a workgroup: its wavefronts split K and load both
+// straight into registers; their sums meet in LDS in a fixed order.
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane (row r = lane & 15, group q = lane
 // >> 4) holds 32 values of K of its row; which ones is the same for both
 // operands, and the scale is one for all of them.
-template <int MT>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void fp8_stream_kernel(const LinearFp8Params a, int tiles_n) {
   constexpr int NW = STREAM_WAVES;
-  __shared__ f32x4_t part[NW][MT][64];
+  __shared__ f32x4_t part[NW][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = blockIdx.x / tiles_n, n0 = (blockIdx.x - g * tiles_n) * 16;
   Group o;
-  if (!group_of(a, g, 16 * MT, o)) return;
+  if (!group_of(a, g, o)) return;
   const int kb = (a.K + 127) / 128;
   const int per = (kb + NW - 1) / NW, s_first = wave * per, s_end = min(s_first + per, kb);
   const uint8_t* w = o.w + (int64_t)min(a.N - 1, n0 + r) * a.K + 16 * q;
   const float* wsf = o.w_sf + (int64_t)(n0 >> 7) * kb;
-  const uint8_t *x[MT], *xsf[MT];
-#pragma unroll
-  for (int m = 0; m < MT; m++) {
-    const int64_t row = min(o.first + 16 * m + r, o.end - 1);
-    x[m] = a.x + row * a.K + 16 * q;
-    xsf[m] = a.x_sf + row * kb;
-  }
-  f32x4_t acc[MT];
-#pragma unroll
-  for (int m = 0; m < MT; m++) acc[m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t xr = min(o.first + r, o.end - 1);
+  const uint8_t *x = a.x + xr * a.K + 16 * q, *xsf = a.x_sf + xr * kb;
+  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  const u32x4_t zero = {0u, 0u, 0u, 0u};
   for (int s = s_first; s < s_end; s++) {
-    const u32x4_t zero = {0u, 0u, 0u, 0u};
     const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
     const u32x4_t w0 = in0 ? ld16(w + 128 * s) : zero, w1 = in1 ? ld16(w + 128 * s + 64) : zero;
+    const u32x4_t x0 = in0 ? ld16(x + 128 * s) : zero, x1 = in1 ? ld16(x + 128 * s + 64) : zero;
     const float ws = wsf[s];
+    const int xs = xsf[s];
     const i32x8_t b = {(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]};
+    const i32x8_t c = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+    const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
+    const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c, b, none, 0, 0, 0, xs, 0, 127);
 #pragma unroll
-    for (int m = 0; m < MT; m++) {
-      const u32x4_t x0 = in0 ? ld16(x[m] + 128 * s) : zero, x1 = in1 ? ld16(x[m] + 128 * s + 64) : zero;
-      const int xs = xsf[m][s];
-      const i32x8_t c = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-      const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
-      const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c, b, none, 0, 0, 0, xs, 0, 127);
-#pragma unroll
-      for (int i = 0; i < 4; i++) acc[m][i] = fmaf(p[i], ws, acc[m][i]);
-    }
+    for (int i = 0; i < 4; i++) acc[i] = fmaf(p[i], ws, acc[i]);
   }
-#pragma unroll
-  for (int m = 0; m < MT; m++) part[wave][m][lane] = acc[m];
+  part[wave][lane] = acc;
   __syncthreads();
   // element i of lane (r, q): row 4 q + i, column r
-  if (wave >= MT || n0 + r >= a.N) return;
-  f32x4_t v = part[0][wave][lane];
+  if (wave > 0 || n0 + r >= a.N) return;
+  f32x4_t v = part[0][lane];
 #pragma unroll
-  for (int k = 1; k < NW; k++) v += part[k][wave][lane];
+  for (int k = 1; k < NW; k++) v += part[k][lane];
   const int n = n0 + r;
   const float bias = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
-    const int64_t row = o.first + 16 * wave + 4 * q + i;
-    if (row >= o.end) continue;
-    store_one(a, row, n, v[i] + bias);
+    const int64_t row = o.first + 4 * q + i;
+    if (row < o.end) store_one(a, row, n, v[i] + bias);
   }
 }
 
-template <int MT>
 hipError_t launch_stream(const LinearFp8Params& a, hipStream_t s) {
   const int tn = (a.N + 15) / 16;
-  const int64_t groups = a.tile_expert ? (int64_t)a.tiles * (a.tile > 16 * MT ? a.tile / (16 * MT) : 1)
-                                       : (a.M + 16 * MT - 1) / (16 * MT);
-  fp8_stream_kernel<MT><<<(unsigned)(groups * tn), 64 * STREAM_WAVES, 0, s>>>(a, tn);
+  const int64_t groups = a.tile_expert ? a.tiles : (a.M + 15) / 16;
+  fp8_stream_kernel<<<(unsigned)(groups * tn), 64 * STREAM_WAVES, 0, s>>>(a, tn);
   return hipGetLastError();
 }
 
@@ -196,16 +212,18 @@ DEV void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int WM_, int WN_, int TM_, int TN_, int NBUF_>
+template <int WM_, int WN_, int TM_, int TN_, int NBUF_, int KG_>
 struct Tile {
   static constexpr int WM = WM_, WN = WN_, TM = TM_, TN = TN_;  // wavefronts, 16 x 16 results of each
   static constexpr int NBUF = NBUF_;                            // stages in LDS
-  static constexpr int NT = 64 * WM * WN;
+  static constexpr int KG = KG_;                                // groups of wavefronts that split K
+  static constexpr int NT = 64 * WM * WN;                       // threads of a group
   static constexpr int BM = 16 * TM * WM, BN = 16 * TN * WN;
   static constexpr int X_BYTES = BM * 128;
   static constexpr int STAGE = (BM + BN) * 128;
   static constexpr int OUT = 16 * 16 * TN * 2;                  // a wavefront's way out: 16 rows
-  static constexpr int T_OFF = NBUF * STAGE;
+  static constexpr int RING = NBUF * STAGE;
+  static constexpr int T_OFF = KG * RING;
   static constexpr int LDS = T_OFF + WM * WN * OUT;
   static constexpr int NX = BM * 8 / NT, NW = BN * 8 / NT;      // LDS-DMA loads a wavefront and stage
 };
@@ -233,14 +251,17 @@ DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
 // be read behind them, and the barrier between two stages has multiplications
 // on both sides.
 template <typename S, bool WIDE>
-__global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Params a, int tiles_n) {
-  constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW, NBUF = S::NBUF;
+__global__ __launch_bounds__(S::NT * S::KG, 2) void fp8_tile_kernel(const LinearFp8Params a, int tiles_n) {
+  constexpr int TM = S::TM, TN = S::TN, BM = S::BM, BN = S::BN, NX = S::NX, NW = S::NW, NBUF = S::NBUF, KG = S::KG;
   static_assert(TN % 4 == 0 && NX >= 1 && NW >= 1, "four buffers of W; whole loads");
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % (S::WM * S::WN);
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / S::NT);
+  uint8_t* smem = smem_all + kg * S::RING;
   const int wn = wave % S::WN, wm = wave / S::WN;
-  const int kb = (a.K + 127) / 128, KT = max(kb, NBUF);
+  // stages of a K group (some past the end of K, whose values count as 0)
+  const int kb = (a.K + 127) / 128, KT = max((kb + KG - 1) / KG, NBUF), first_s = kg * KT;
 
   // tiles of this workgroup: XCD b & 7 takes a contiguous run of them, its
   // workgroups take them in turn; 8 rows of tiles high, so that what an XCD
@@ -306,7 +327,7 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
     uint32_t k[2];  // of loads of even and odd number
 #pragma unroll
     for (int v = 0; v < 2; v++) {
-      k[v] = (uint32_t)(128 * s + (chunk ^ (64 * v)));
+      k[v] = (uint32_t)(128 * (first_s + s) + (chunk ^ (64 * v)));
       k[v] = k[v] < (uint32_t)a.K ? k[v] : 0u;
     }
     const uint32_t kx[2] = {NX % 2 && (wave & 1) ? k[1] : k[0], NX % 2 && (wave & 1) ? k[0] : k[1]};
@@ -351,7 +372,7 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   float ws;
   auto load_scales = [&](int g) {
     if (kb >= 4) {  // four bytes; a word that reaches past the row's end: its last four
-      const int at = min(4 * g, kb - 4);
+      const int at = min(first_s + 4 * g, kb - 4);
 #pragma unroll
       for (int m = 0; m < TM; m++)
         __builtin_memcpy(&later[m], xsf + min(16 * (TM * wm + m) + r, last_m) * kb + at, 4);
@@ -374,9 +395,11 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
       for (int m = 0; m < TM; m++) asm volatile("" : "+v"(acc[i][m]));
   };
   int buf = 0;
-  // One stage; its loads fetch stage `ahead` of what is aimed at; `wsn`: W's
-  // scale of the next stage.
-  auto stage = [&](int ahead, const float* wsn) {
+  // One stage; its loads fetch stage `ahead` of what is aimed at (K groups have
+  // one tile and fetch nothing in its last stages); `wsn`: W's scale of the next
+  // stage.
+  auto stage = [&](int ahead, const float* wsn, auto tail_) {
+    constexpr bool LOAD = KG == 1 || !decltype(tail_)::value;
     uint8_t* st = smem + buf * S::STAGE;
     buf = buf == NBUF - 1 ? 0 : buf + 1;
     const uint8_t* sn = smem + buf * S::STAGE;
@@ -391,8 +414,8 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
       __builtin_amdgcn_sched_barrier(0);
     }
     // every fragment of the stage is in registers, the next stage has landed
-    stage_barrier<(NBUF - 2) * (NX + NW)>();
-    issue(ahead, st);
+    stage_barrier<LOAD ? (NBUF - 2) * (NX + NW) : 0>();
+    if constexpr (LOAD) issue(ahead, st);
     const float wl = ws;
     ws = ld_uniform(wsn);
     __builtin_amdgcn_sched_barrier(0);
@@ -412,15 +435,16 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   // the scales of the four stages from s on, and the loads of those after them
   auto next_scales = [&](int s) {
     if ((s & 3) == 0) {
-      const int past = max(0, s + 4 - kb), shift = kb >= 4 ? 8 * min(past, 3) : 0;
+      const int past = max(0, first_s + s + 4 - kb), shift = kb >= 4 ? 8 * min(past, 3) : 0;
 #pragma unroll
       for (int m = 0; m < TM; m++) word[m] = later[m] >> shift;
       if (s + 4 < KT) load_scales((s >> 2) + 1);
     }
   };
   auto mask = [&](int s) {  // values past the end of K
-    if (128 * (s + 1) > a.K) {
-      const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
+    const int k = 128 * (first_s + s);
+    if (k + 128 > a.K) {
+      const bool in0 = k + 16 * q < a.K, in1 = k + 64 + 16 * q < a.K;
 #pragma unroll
       for (int m = 0; m < TM; m++)
 #pragma unroll
@@ -436,7 +460,7 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
   load_scales(0);
 #pragma unroll
   for (int i = 0; i < NBUF; i++) issue(i, smem + i * S::STAGE);
-  ws = ld_uniform(wsf);
+  ws = ld_uniform(wsf + min(first_s, kb - 1));
   stage_barrier<(NBUF - 1) * (NX + NW)>();
 #pragma unroll
   for (int m = 0; m < TM; m++) x[m] = read_x(smem, m);
@@ -456,7 +480,8 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
 #pragma unroll 1
     for (; s < KT - NBUF; s++) {
       next_scales(s);
-      stage(s + NBUF, wsf + s + 1);
+      if constexpr (KG > 1) mask(s);
+      stage(s + NBUF, wsf + min(first_s + s + 1, kb - 1), std::false_type());
     }
     // the last ones fetch the first ones of the next tile (without one, of this
     // tile again, unread)
@@ -465,11 +490,29 @@ __global__ __launch_bounds__(S::NT, 2) void fp8_tile_kernel(const LinearFp8Param
     for (int i = 0; i < NBUF; i++, s++) {
       next_scales(s);
       mask(s);
-      if (i == 0) aim(next);
-      if (i == NBUF - 1) load_scales(0);
-      stage(i, i == NBUF - 1 ? wsf : of_this + min(s + 1, kb - 1));
+      if (KG == 1 && i == 0) aim(next);
+      if (KG == 1 && i == NBUF - 1) load_scales(0);
+      stage(i, i == NBUF - 1 ? wsf : of_this + min(first_s + s + 1, kb - 1), std::true_type());
     }
-    store_tile<S, WIDE>(a, acc, o.m0 + 16 * TM * wm, o.end, o.n0 + 16 * TN * wn, smem + S::T_OFF + S::OUT * wave, lane);
+    // the K groups' sums: the upper half hands its own to the lower one, until the
+    // first group has all of them
+#pragma unroll
+    for (int half = KG / 2; half >= 1; half /= 2) {
+      f32x4_t* to = reinterpret_cast<f32x4_t*>(smem_all);
+      const int at = ((kg & (half - 1)) * S::WM * S::WN + wave) * TN * TM * 64 + lane;
+      __syncthreads();  // what was read or handed over before
+      if (kg >= half && kg < 2 * half) {
+#pragma unroll
+        for (int i = 0; i < TN * TM; i++) to[at + 64 * i] = acc[i / TM][i % TM];
+      }
+      __syncthreads();
+      if (kg < half) {
+#pragma unroll
+        for (int i = 0; i < TN * TM; i++) acc[i / TM][i % TM] += to[at + 64 * i];
+      }
+    }
+    if (kg > 0) return;
+    store_tile<S, WIDE>(a, acc, o.m0 + 16 * TM * wm, o.end, o.n0 + 16 * TN * wn, smem_all + S::T_OFF + S::OUT * wave, lane);
     if (!more) break;
     t = tn;
     o = next;
@@ -490,9 +533,9 @@ hipError_t launch_tile_as(const LinearFp8Params& a, hipStream_t s) {
   if (err != hipSuccess) return err;
   const int tn = (a.N + S::BN - 1) / S::BN;
   const int64_t tm = a.tile_expert ? (int64_t)a.tiles * (a.tile / S::BM) : (a.M + S::BM - 1) / S::BM;
-  const int64_t most = (int64_t)(cus / 8) * 8 * PER_CU;
-  const int64_t grid = min(max(most, (int64_t)8), (tm * tn + 7) / 8 * 8);
-  fp8_tile_kernel<S, WIDE><<<(unsigned)grid, S::NT, S::LDS, s>>>(a, tn);
+  const int64_t most = (int64_t)(cus >= 8 ? cus / 8 * 8 : 8) * PER_CU, tiles = (tm * tn + 7) / 8 * 8;
+  const int64_t grid = S::KG == 1 && tiles > most ? most : tiles;  // (K groups: a tile a workgroup)
+  fp8_tile_kernel<S, WIDE><<<(unsigned)grid, S::NT * S::KG, S::LDS, s>>>(a, tn);
   return hipGetLastError();
 }
 template <typename S>
@@ -500,28 +543,50 @@ hipError_t launch_tile(const LinearFp8Params& a, hipStream_t s) {
   return wide_rows(a) ? launch_tile_as<S, true>(a, s) : launch_tile_as<S, false>(a, s);
 }
 
-using Big = Tile<4, 2, 4, 8, 2>;    // 256 x 256, eight wavefronts, one workgroup a CU
-using Middle = Tile<2, 2, 4, 4, 2>; // 128 x 128, four, two a CU
-using Small = Tile<2, 2, 2, 4, 3>;  // 64 x 128
-using Low = Tile<1, 4, 2, 4, 2>;    // 32 x 256
+// rows x columns of a tile; wavefronts of 16 TM x 16 TN; stages; K groups
+using Big = Tile<4, 2, 4, 8, 2, 1>;     // 256 x 256, eight wavefronts, one workgroup a CU
+using Middle = Tile<2, 2, 4, 4, 2, 1>;  // 128 x 128, four, two workgroups a CU
+using Small = Tile<2, 2, 2, 4, 3, 1>;   // 64 x 128, four, two
+using Low = Tile<1, 4, 2, 4, 2, 1>;     // 32 x 256, four, two
+using Split2 = Tile<2, 2, 2, 4, 3, 2>;  // 64 x 128, K in two
+using Split4 = Tile<2, 1, 2, 4, 2, 4>;  // 64 x 64, K in four
+using Split4Low = Tile<1, 1, 2, 4, 2, 4>;  // 32 x 64, K in four
 
 }  // namespace
 
 hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
   constexpr int64_t CUS = 256;
   if (a.tile_expert) {
-    if (a.tile <= 16) return launch_stream<1>(a, s);
+    // (experts of 4096 x 6144, 32 of them: 16 rows a tile through the tiled kernel
+    // would multiply half of nothing; 1000 rows in tiles of 32: 190 us, 396 streamed
+    // in 16-row pieces; 2000 in tiles of 64: 204 against 621)
+    if (a.tile <= 16) return launch_stream(a, s);
     if (a.tile <= 32) return launch_tile<Low>(a, s);
     if (a.tile <= 64) return launch_tile<Small>(a, s);
     if (a.tile <= 128) return launch_tile<Middle>(a, s);
     return launch_tile<Big>(a, s);
   }
-  if (a.M <= 16) return launch_stream<1>(a, s);
-  if (a.M <= 32) return launch_stream<2>(a, s);
-  if (a.M <= 64) return launch_stream<4>(a, s);
   auto tiles = [&](int m, int n) { return ((a.M + m - 1) / m) * ((a.N + n - 1) / n); };
+  // The streaming kernel while its 16 x 16 tiles have little to do together: it
+  // waits for memory once, the others for each stage (128 x 724 x 1024: 6.2 us
+  // against 8.4; 128 x 256 x 8192: 12.9 against 15.2; 512 x 724 x 1024: 11.4
+  // against 8.6; 64 x 4096 x 6144: 28.7 against 12.7).
+  if (a.M <= 16 || tiles(16, 16) * ((a.K + 127) / 128) <= 8192) return launch_stream(a, s);
+  // A wavefront alone on a SIMD is bound by its own instructions, about 1000 cycles
+  // a stage of 32 x 64 results.  While all tiles have a CU each, K is split over
+  // more wavefronts: 64 x 4096 x 6144 12.7 us against 24.9 in 64 x 128 tiles, 128 x 4096
+  // x 4096 10.7 against 19.3, 256 x 4096 x 4096 13.1 against 19.7, 512 x 4096 x 4096
+  // 19.0 against 22.1.
+  if (tiles(32, 64) <= CUS) return launch_tile<Split4Low>(a, s);
+  if (tiles(64, 64) <= CUS) return launch_tile<Split4>(a, s);
+  if (tiles(64, 128) <= CUS) return launch_tile<Split2>(a, s);
+  // 256 x 256 tiles where they fill whole rounds of the CUs, three quarters at
+  // least (8000 x 2000 x 2000, one full round: 53.6 us against 49.5 in 128 x 128 tiles;
+  // 4096 x 4096 x 4096: 77 against 99)
   const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS;
-  if (4 * big >= 3 * CUS * rounds) return launch_tile<Big>(a, s);
+  if (4 * big >= 3 * CUS * rounds && a.K >= 1024) return launch_tile<Big>(a, s);
+  // (4096 x 724 x 1024, 192 tiles of 128 x 128: 19.2 us in 64 x 128, 20.7; 2048 x 4096 x
+  // 2048, 512 of them: 29.9, 26.4)
   if (tiles(128, 128) <= CUS) return launch_tile<Small>(a, s);
   return launch_tile<Middle>(a, s);
 }
