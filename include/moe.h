@@ -692,8 +692,8 @@ moe_status_t moe_finalize_backward(const uint16_t* dout, const uint16_t* y2, con
  * which w's scale joins to the next in one fused multiply-add.  Inside it the matrix
  * instruction adds up each group of 8 consecutive values first, and keeps of a
  * product the bits down to 2^-13 of the power of two of the group's largest one:
- * off by up to 8 * 2^-13 of that product, in an fp32 y too.  bias and accumulation
- * are one fp32 addition each, y is rounded once.  M, N >= 0; K positive.
+ * off by up to 8 * 2^-13 of that product, in an fp32 y too.  bias is a term of the fp32
+ * sum, the accumulation onto y an addition after it, and y is rounded once.  M, N >= 0; K positive.
  * K a multiple of 16, at most 2^20; x and w 16-byte aligned, y aligned to its
  * elements; M and N at most 2^26, M * N at most 2^36 (else MOE_ERR_UNSUPPORTED).
  * Each output is one sum in an order that depends on M, N and K alone: reproducible

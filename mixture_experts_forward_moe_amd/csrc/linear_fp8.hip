@@ -62,6 +62,9 @@ DEV void store_one(const LinearFp8Params& a, int64_t row, int n, float v) {
 template <typename S, bool WIDE>
 DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM], int64_t m0, int64_t end, int n0,
                     uint8_t* out, int lane) {
+  // (what follows from the lane is computed here, not held over the main loop, where
+  // it would be spilled, and read back behind the stores)
+  asm volatile("" : "+v"(lane));
   constexpr int TM = S::TM, TN = S::TN, W = 4 * TN;  // columns of a lane
   constexpr int C = 2 * TN;                          // chunks of 16 bytes in a row
   const int r = lane & 15, q = lane >> 4, n = n0 + W * q;
@@ -74,10 +77,7 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
       for (int c = 0; c < TN / 2; c++) {
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          v[i] = acc[2 * c + (i >> 2)][m][i & 3];
-          if (a.bias) v[i] += a.bias[min(n + 8 * c + i, a.N - 1)];
-        }
+        for (int i = 0; i < 8; i++) v[i] = acc[2 * c + (i >> 2)][m][i & 3];
         u32x4_t o;
 #pragma unroll
         for (int i = 0; i < 4; i++) o[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
@@ -85,12 +85,18 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
       }
       wave_fence();  // the rows are read by other lanes
       constexpr int ROWS = 64 / C;  // rows a store
+      const int c = lane % C;
+      u32x4_t o[16 / ROWS];
 #pragma unroll
       for (int i = 0; i < 16 / ROWS; i++) {
-        const int rr = ROWS * i + lane / C, c = lane % C;
-        const u32x4_t o = *reinterpret_cast<const u32x4_t*>(out + 16 * (C * rr + (c ^ (rr & (C - 1)))));
+        const int rr = ROWS * i + lane / C;
+        o[i] = *reinterpret_cast<const u32x4_t*>(out + 16 * (C * rr + (c ^ (rr & (C - 1)))));
+      }
+#pragma unroll
+      for (int i = 0; i < 16 / ROWS; i++) {
+        const int rr = ROWS * i + lane / C;
         if (row0 + rr < end && n0 + 8 * c < a.N)
-          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.y) + (row0 + rr) * a.N + n0 + 8 * c) = o;
+          *reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.y) + (row0 + rr) * a.N + n0 + 8 * c) = o[i];
       }
       wave_fence();  // and written again once they have been
     } else {
@@ -105,10 +111,7 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
         if (col >= a.N) continue;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-          v[i] = acc[2 * c + (i >> 2)][m][i & 3];
-          if (a.bias) v[i] += a.bias[min(col + i, a.N - 1)];
-        }
+        for (int i = 0; i < 8; i++) v[i] = acc[2 * c + (i >> 2)][m][i & 3];
         if (four) {
 #pragma unroll
           for (int h = 0; h < 2; h++) {
@@ -473,6 +476,16 @@ __global__ __launch_bounds__(S::NT * S::KG, 2) void fp8_tile_kernel(const Linear
     for (int i = 0; i < TN; i++)
 #pragma unroll
       for (int m = 0; m < TM; m++) acc[i][m] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    if (a.bias && kg == 0) {  // the sums start with it
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+        f32x4_t b;
+#pragma unroll
+        for (int c = 0; c < 4; c++) b[c] = a.bias[min(o.n0 + 16 * TN * wn + 4 * TN * q + 4 * i + c, a.N - 1)];
+#pragma unroll
+        for (int m = 0; m < TM; m++) acc[i][m] = b;
+      }
+    }
     const int64_t tn = t + step;
     const bool more = tn < last;
     const At next = more ? tile_at(tn) : o;
