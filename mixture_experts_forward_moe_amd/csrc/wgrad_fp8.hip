@@ -40,14 +40,16 @@ DEV void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
-template <int TN_, int TK_>
+template <int TN_, int TK_, int MG_>
 struct Tile {
+  static constexpr int MG = MG_;                  // groups of four wavefronts that split the rows
   static constexpr int TN = TN_, TK = TK_;        // 16 x 16 results of a wavefront, four of them as 2 x 2
   static constexpr int BN = 32 * TN, BK = 32 * TK;
   static constexpr int ST = 32;                   // rows of a stage
   static constexpr int PN = 2 * BN, PK = 2 * BK;  // bytes of a row in LDS
   static constexpr int STAGE = ST * (PN + PK);
-  static constexpr int LDS = 2 * STAGE;
+  static constexpr int BUFFERS = 2 * STAGE;       // of a group
+  static constexpr int LDS = MG * BUFFERS;
   static constexpr int ND = ST * PN / 4096;       // 16-byte loads of dy a thread and stage
   static constexpr int NX = ST * BK / 4096;       // and of x
 };
@@ -67,11 +69,13 @@ DEV int swizzle(int m) {
 // for all of it.)  Rows past the end of the range are read as 0: the buffers
 // end there.
 template <typename S>
-__global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
-  constexpr int TN = S::TN, TK = S::TK, PN = S::PN, PK = S::PK, ND = S::ND, NX = S::NX;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 63, r = lane & 15, q = lane >> 4;
+__global__ __launch_bounds__(256 * S::MG, S::MG == 1 ? 2 : 4) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
+  constexpr int TN = S::TN, TK = S::TK, PN = S::PN, PK = S::PK, ND = S::ND, NX = S::NX, MG = S::MG;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
+  const int tid = threadIdx.x & 255, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wk = wave >> 1;
+  const int mg = MG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+  uint8_t* smem = smem_all + mg * S::BUFFERS;
 
   // tile of this workgroup: an XCD (workgroups are dealt to them round robin) takes
   // a run of every expert's tiles, so that experts with many rows cost all XCDs the
@@ -84,9 +88,11 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
   const int high = min(GM, tiles_n - group * GM);
   const int n0 = (group * GM + in % high) * S::BN, k0 = in / high * S::BK;
 
-  const int64_t first = a.offsets ? ld_uniform(a.offsets + e) : 0;
-  const int64_t rows = a.offsets ? ld_uniform(a.counts + e) : a.M;
-  const int stages = (int)((rows + S::ST - 1) / S::ST);
+  // rows of this group: as many stages for each (past the end they are 0)
+  const int64_t all = a.offsets ? ld_uniform(a.counts + e) : a.M;
+  const int stages = (int)((all + S::ST * MG - 1) / (S::ST * MG));
+  const int64_t skip = (int64_t)mg * stages * S::ST, first = (a.offsets ? ld_uniform(a.offsets + e) : 0) + skip;
+  const int64_t rows = all - skip;
   const int nb = (a.K + 127) / 128;
 
   // thread's rows of a stage and the 16 bytes it loads of each: 8 values of dy, 16
@@ -188,6 +194,25 @@ __global__ __launch_bounds__(256, 2) void wgrad_kernel(const WgradParams a, int 
     if (s < stages) stage(s, x1, x0);
   }
 
+  // the groups' sums: the upper half hands its own to the lower one, until the first
+  // group has all of them (every wavefront is past its reads of the buffers)
+#pragma unroll
+  for (int half = MG / 2; half >= 1; half /= 2) {
+    f32x4_t* to = reinterpret_cast<f32x4_t*>(smem_all);
+    const int at = ((mg & (half - 1)) * 4 + wave) * TN * TK * 64 + lane;
+    __syncthreads();
+    if (mg >= half && mg < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < TN * TK; i++) to[at + 64 * i] = acc[i / TN][i % TN];
+    }
+    __syncthreads();
+    if (mg < half) {
+#pragma unroll
+      for (int i = 0; i < TN * TK; i++) acc[i / TN][i % TN] += to[at + 64 * i];
+    }
+  }
+  if (mg > 0) return;
+
   // element i of lane (r, q): k = 4 q + i, n = r
   float* dw = a.dw + (int64_t)e * a.N * a.K;
 #pragma unroll
@@ -210,7 +235,7 @@ hipError_t launch(const WgradParams& a, hipStream_t s) {
   const hipError_t err = allow_lds<wgrad_kernel<S>>(S::LDS, &cus);
   if (err != hipSuccess) return err;
   const int64_t grid = ((int64_t)tn * tk + 7) / 8 * 8 * a.experts;
-  wgrad_kernel<S><<<(unsigned)grid, 256, S::LDS, s>>>(a, tn, tk);
+  wgrad_kernel<S><<<(unsigned)grid, 256 * S::MG, S::LDS, s>>>(a, tn, tk);
   return hipGetLastError();
 }
 
@@ -218,9 +243,18 @@ hipError_t launch(const WgradParams& a, hipStream_t s) {
 
 hipError_t launch_wgrad_fp8(const WgradParams& a, hipStream_t s) {
   constexpr int64_t CUS = 256;
-  const int64_t large = (int64_t)a.experts * ((a.N + 127) / 128) * ((a.K + 255) / 256);
-  if (large < CUS) return launch<Tile<2, 4>>(a, s);
-  return launch<Tile<4, 8>>(a, s);
+  auto tiles = [&](int n, int k) { return (int64_t)a.experts * ((a.N + n - 1) / n) * ((a.K + k - 1) / k); };
+  // 128 x 256 tiles while there are two for each CU (4096 x 4096 x 4096, 512 of them:
+  // 133 us against 142 in 128 x 128 tiles; 1000 x 4096 x 4096: 47 against 51)
+  if (tiles(128, 256) >= 2 * CUS) return launch<Tile<4, 8, 1>>(a, s);
+  // 128 x 128, rows in two, while that is one for every other CU (1237 x 2056 x 1568,
+  // 221 of them: 22.4 us, in 64 x 128 tiles 23.8, in 128 x 256 35; 4096 x 2048 x 2048:
+  // 48, 51, 87)
+  if (tiles(128, 128) > CUS / 2) return launch<Tile<4, 4, 2>>(a, s);
+  // 64 x 128 below, rows in two, or in four where they are many (16384 x 1024 x 1024:
+  // 113 us in two, 93 in four; 64 x 2048 x 2048: 9.2, 14.7)
+  if (a.M / a.experts < 1024) return launch<Tile<2, 4, 2>>(a, s);
+  return launch<Tile<2, 4, 4>>(a, s);
 }
 
 }  // namespace moe
