@@ -16,6 +16,13 @@ namespace {
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
+
+// LDS at a byte address
+template <typename T>
+DEV T* lds(uint32_t at) {
+  return (T*)(uintptr_t)at;
+}
 
 // 16 codes under one E8M0 code as bf16 pairs
 DEV void decode16(const u32x4_t& c, uint32_t code, u32x4_t& lo, u32x4_t& hi) {
@@ -31,10 +38,12 @@ DEV void decode16(const u32x4_t& c, uint32_t code, u32x4_t& lo, u32x4_t& hi) {
   }
 }
 
-// workgroup barrier over LDS that waits for this wavefront's LDS accesses only (a
-// release fence would also wait for every load in flight)
+// workgroup barrier over LDS that waits for this wavefront's LDS accesses but the
+// newest LEFT (a release fence would also wait for every load in flight)
+template <int LEFT>
 DEV void stage_barrier() {
-  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  static_assert(LEFT <= 15, "four bits");
+  __builtin_amdgcn_s_waitcnt(0xC07F | (LEFT << 8));
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
@@ -48,7 +57,7 @@ struct Tile {
   static constexpr int ST = 32;                   // rows of a stage
   static constexpr int PN = 2 * BN, PK = 2 * BK;  // bytes of a row in LDS
   static constexpr int STAGE = ST * (PN + PK);
-  static constexpr int BUFFERS = 2 * STAGE;       // of a group
+  static constexpr int BUFFERS = 3 * STAGE;       // of a group
   static constexpr int LDS = MG * BUFFERS;
   static constexpr int ND = ST * PN / 4096;       // 16-byte loads of dy a thread and stage
   static constexpr int NX = ST * BK / 4096;       // and of x
@@ -63,19 +72,21 @@ DEV int swizzle(int m) {
   else return ((m >> 1) & 1) | (((m >> 3) & 1) << 1);
 }
 
-// One tile of dW a workgroup.  Both operands go through registers: loaded two
-// stages ahead, written into LDS one ahead.  (LDS-DMA of dy is slower: the
+// One tile of dW a workgroup.  Both operands go through registers: loaded four
+// stages ahead, written into LDS two ahead between the multiplications, so that a
+// wavefront's fragments of the next stage are on their way at the barrier (with two
+// buffers, all of a stage written behind its last read: 16384 x 4096 x 6144 790 us,
+// now 748, 1.1 PFLOP/s; experts of 16384 tokens 1435, now 1320).  (LDS-DMA of dy is slower: the
 // compiler cannot tell its target from what a transposing read takes, and waits
 // for all of it.)  Rows past the end of the range are read as 0: the buffers
 // end there.
 template <typename S>
-__global__ __launch_bounds__(256 * S::MG, S::MG == 1 ? 2 : 4) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
+__global__ __launch_bounds__(256 * S::MG, S::MG == 4 ? 4 : 2) void wgrad_kernel(const WgradParams a, int tiles_n, int tiles_k) {
   constexpr int TN = S::TN, TK = S::TK, PN = S::PN, PK = S::PK, ND = S::ND, NX = S::NX, MG = S::MG;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem_all[];
   const int tid = threadIdx.x & 255, lane = tid & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), wn = wave & 1, wk = wave >> 1;
   const int mg = MG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
-  uint8_t* smem = smem_all + mg * S::BUFFERS;
 
   // tile of this workgroup: an XCD (workgroups are dealt to them round robin) takes
   // a run of every expert's tiles, so that experts with many rows cost all XCDs the
@@ -105,51 +116,65 @@ __global__ __launch_bounds__(256 * S::MG, S::MG == 1 ? 2 : 4) void wgrad_kernel(
     u32x4_t d[ND], q[NX];
     uint32_t sf[NX];
   };
-  auto load = [&](int s, Rows& o) {
+  struct From {  // of a stage: buffers that end with the range
+    __amdgpu_buffer_rsrc_t d, q, sf;
+  };
+  auto from = [&](int s) {
     const int64_t m0 = first + (int64_t)s * S::ST;
     const int left = (int)min((int64_t)S::ST, max((int64_t)0, rows - (int64_t)s * S::ST));
-    const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.dy + m0 * a.N), 0,
-                                                                       left * 2 * a.N, 0x00020000);
-    const __amdgpu_buffer_rsrc_t c =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x + m0 * a.K), 0, left * a.K, 0x00020000);
-    const __amdgpu_buffer_rsrc_t f =
-        __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x_sf + m0 * nb), 0, left * nb, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < NX; i++) {
-      const int m = xm + 256 / CX * i;
-      o.q[i] = __builtin_amdgcn_raw_buffer_load_b128(c, inside ? (uint32_t)(m * a.K + k0 + 16 * xc) : past, 0, 0);
-      o.sf[i] = __builtin_amdgcn_raw_buffer_load_b8(f, inside ? (uint32_t)(m * nb + ((k0 + 16 * xc) >> 7)) : past, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < ND; i++)
-      o.d[i] = __builtin_amdgcn_raw_buffer_load_b128(b, (uint32_t)((dm + 256 / CD * i) * 2 * a.N + 2 * n0 + 16 * dc), 0, 0);
+    From o;
+    o.d = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(a.dy + m0 * a.N), 0, left * 2 * a.N, 0x00020000);
+    o.q = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x + m0 * a.K), 0, left * a.K, 0x00020000);
+    o.sf = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(a.x_sf + m0 * nb), 0, left * nb, 0x00020000);
+    return o;
   };
-  auto store = [&](const Rows& o, int buf) {
-    uint8_t* st = smem + buf * S::STAGE;
-#pragma unroll
-    for (int i = 0; i < NX; i++) {
-      const int m = xm + 256 / CX * i;
-      u32x4_t lo, hi;
-      decode16(o.q[i], o.sf[i], lo, hi);
-      uint8_t* p = st + S::ST * PN + m * PK + 32 * (xc ^ swizzle<PK>(m));
-      *reinterpret_cast<u32x4_t*>(p) = lo;
-      *reinterpret_cast<u32x4_t*>(p + 16) = hi;
-    }
-#pragma unroll
-    for (int i = 0; i < ND; i++) {
-      const int m = dm + 256 / CD * i;
-      *reinterpret_cast<u32x4_t*>(st + m * PN + 32 * ((dc >> 1) ^ swizzle<PN>(m)) + 16 * (dc & 1)) = o.d[i];
-    }
+  const uint32_t d_from = (uint32_t)(dm * 2 * a.N + 2 * n0 + 16 * dc);
+  const uint32_t q_from = inside ? (uint32_t)(xm * a.K + k0 + 16 * xc) : past;
+  const uint32_t sf_from = inside ? (uint32_t)(xm * nb + ((k0 + 16 * xc) >> 7)) : past;
+  auto load_d = [&](const From& f, Rows& o, int i) {
+    o.d[i] = __builtin_amdgcn_raw_buffer_load_b128(f.d, d_from + (uint32_t)(256 / CD * i * 2 * a.N), 0, 0);
   };
-
-  // fragments: of 16 columns, rows 8 q .. 8 q + 7, by two reads whose lane
-  // addresses 4 columns of one row
+  auto load_x = [&](const From& f, Rows& o, int i) {
+    o.q[i] = __builtin_amdgcn_raw_buffer_load_b128(f.q, q_from + (uint32_t)(256 / CX * i * a.K), 0, 0);
+    o.sf[i] = __builtin_amdgcn_raw_buffer_load_b8(f.sf, sf_from + (uint32_t)(256 / CX * i * nb), 0, 0);
+  };
+  auto load = [&](int s, Rows& o) {
+    const From f = from(s);
+#pragma unroll
+    for (int i = 0; i < NX; i++) load_x(f, o, i);
+#pragma unroll
+    for (int i = 0; i < ND; i++) load_d(f, o, i);
+  };
+  // LDS addresses in the first of the group's buffers: where this thread's rows
+  // go (those of x are 16 apart and those of dy 16 or 32, so they have one swizzle),
+  // and of the fragments of 16 columns, rows 8 q .. 8 q + 7, two reads whose lane
+  // addresses 4 columns of one row; column tile j is the first one's address xor 32 j
+  static_assert((256 / CX % 16 == 0 || NX == 1) && 256 / CD % 16 == 0, "rows of a thread");
+  const uint32_t base = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)smem_all + mg * S::BUFFERS;
+  const uint32_t x_to = base + S::ST * PN + xm * PK + 32 * (xc ^ swizzle<PK>(xm));
+  const uint32_t d_to = base + dm * PN + 32 * ((dc >> 1) ^ swizzle<PN>(dm)) + 16 * (dc & 1);
   const int fm = 8 * q + (r >> 2);
-  const int dy_frag = fm * PN + 32 * swizzle<PN>(fm) + 8 * (r & 3);
-  const int x_frag = S::ST * PN + fm * PK + 32 * swizzle<PK>(fm) + 8 * (r & 3);
-  auto frag = [&](int at, int pitch) {
-    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(smem + at));
-    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t*)(smem + at + 4 * pitch));
+  const uint32_t d_at = (base + fm * PN + 32 * swizzle<PN>(fm) + 8 * (r & 3)) ^ (32 * TN * wn);
+  const uint32_t x_at = (base + S::ST * PN + fm * PK + 32 * swizzle<PK>(fm) + 8 * (r & 3)) ^ (32 * TK * wk);
+  auto store_x = [&](const Rows& o, uint32_t st, int i) {
+    u32x4_t lo, hi;
+    decode16(o.q[i], o.sf[i], lo, hi);
+    lds_u32x4_t* p = lds<lds_u32x4_t>(x_to + st + (uint32_t)(256 / CX * i * PK));
+    p[0] = lo;
+    p[1] = hi;
+  };
+  auto store_d = [&](const Rows& o, uint32_t st, int i) {
+    *lds<lds_u32x4_t>(d_to + st + (uint32_t)(256 / CD * i * PN)) = o.d[i];
+  };
+  auto store = [&](const Rows& o, uint32_t st) {
+#pragma unroll
+    for (int i = 0; i < NX; i++) store_x(o, st, i);
+#pragma unroll
+    for (int i = 0; i < ND; i++) store_d(o, st, i);
+  };
+  auto frag = [&](uint32_t at, int pitch) {
+    const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds<lds_i16x4_t>(at));
+    const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds<lds_i16x4_t>(at + (uint32_t)(4 * pitch)));
     typedef short i16x8_t __attribute__((ext_vector_type(8)));
     const i16x8_t v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
     return __builtin_bit_cast(bf16x8_t, v);
@@ -166,32 +191,62 @@ __global__ __launch_bounds__(256 * S::MG, S::MG == 1 ? 2 : 4) void wgrad_kernel(
     load(0, x0);
     load(1, x1);
     store(x0, 0);
-    stage_barrier();
-    int buf = 0;
-    // stage s: the rows of the next one are in `next`, those of the one after it go to `later`
-    auto stage = [&](int s, Rows& next, Rows& later) {
-      load(s + 2, later);
-      const int base = buf * S::STAGE;
-      buf ^= 1;
-      bf16x8_t d[TN];
+    load(2, x0);
+    store(x1, S::STAGE);
+    load(3, x1);
+    stage_barrier<0>();
+    constexpr int AHEAD = 3, RING = 4;  // x's fragments
+    bf16x8_t d0[TN], d1[TN], f[RING];
+    uint32_t b0 = 0, b1 = S::STAGE, b2 = 2 * S::STAGE;  // buffers of this stage, the next one, the one after it
+    auto read_d = [&](uint32_t st, int j) { return frag((d_at + st) ^ (32u * j), PN); };
+    auto read_x = [&](uint32_t st, int i) { return frag((x_at + st) ^ (32u * i), PK); };
 #pragma unroll
-      for (int j = 0; j < TN; j++) d[j] = frag((base + dy_frag) ^ (32 * (TN * wn + j)), PN);
+    for (int j = 0; j < TN; j++) d0[j] = read_d(0, j);
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) f[i] = read_x(0, i);
+    // Stage s.  `rows` holds those of s + 2, which go into the third buffer piece by
+    // piece between the multiplications, and takes those of s + 4; the first fragments
+    // of s + 1, in LDS since the last barrier, are read behind the last of s.
+    auto stage = [&](int s, Rows& rows, bf16x8_t (&d)[TN], bf16x8_t (&dn)[TN]) {
+      const From o = from(s + 4);
 #pragma unroll
       for (int i = 0; i < TK; i++) {
-        const bf16x8_t f = frag((base + x_frag) ^ (32 * (TK * wk + i)), PK);
+        f[(i + AHEAD) % RING] = i + AHEAD < TK ? read_x(b0, (i + AHEAD) % TK) : read_x(b1, (i + AHEAD) % TK);
+        if (i >= TK - 2) {
 #pragma unroll
-        for (int j = 0; j < TN; j++) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f, d[j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < TN / 2; j++) dn[TN / 2 * (i - TK + 2) + j] = read_d(b1, TN / 2 * (i - TK + 2) + j);
+        }
+        constexpr int P = TK - 2, PIECES = NX + ND;  // pieces, in the steps before the last two
+#pragma unroll
+        for (int c = 0; c < PIECES; c++) {
+          if (c * P / PIECES != i) continue;
+          if (c < NX) {
+            store_x(rows, b2, c % NX);
+            load_x(o, rows, c % NX);
+          } else {
+            store_d(rows, b2, c - NX);
+            load_d(o, rows, c - NX);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < TN; j++)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[i % RING], d[j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      store(next, buf);
-      stage_barrier();
+      // all LDS accesses but the reads of the last two steps (of the next stage) are done
+      stage_barrier<2 * (2 + TN)>();
+      const uint32_t t = b0;
+      b0 = b1;
+      b1 = b2;
+      b2 = t;
     };
     int s = 0;
 #pragma unroll 1
     for (; s + 1 < stages; s += 2) {
-      stage(s, x1, x0);
-      stage(s + 1, x0, x1);
+      stage(s, x0, d0, d1);
+      stage(s + 1, x1, d1, d0);
     }
-    if (s < stages) stage(s, x1, x0);
+    if (s < stages) stage(s, x0, d0, d1);
   }
 
   // the groups' sums: the upper half hands its own to the lower one, until the first
