@@ -632,7 +632,8 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
  *  weights : E4M3 codes [N, K] and an fp32 scale for each block of 128 x 128,
  *            [ceil(N / 128), ceil(K / 128)]; the scales may be any finite value.
  * Rows in a plan's order are [route_slots, ..]; padding slots are neither read
- * nor written by any of the calls. */
+ * nor written by any of the calls.  An output may not overlap an input or another
+ * output, except where a call says so. */
 
 /* Row quantisation of bf16 x [rows, cols], row stride in elements (0 =
  * contiguous; shorter than cols: MOE_ERR_INVALID_ARGUMENT).  cols a multiple of
@@ -693,7 +694,8 @@ moe_status_t moe_finalize_backward(const uint16_t* dout, const uint16_t* y2, con
  * instruction adds up each group of 8 consecutive values first, and keeps of a
  * product the bits down to 2^-13 of the power of two of the group's largest one:
  * off by up to 8 * 2^-13 of that product, in an fp32 y too.  bias is a term of the fp32
- * sum, the accumulation onto y an addition after it, and y is rounded once.  M, N >= 0; K positive.
+ * sum, the accumulation onto y an addition after it, and y is rounded once.  M, N >= 0;
+ * K positive.
  * K a multiple of 16, at most 2^20; x and w 16-byte aligned, y aligned to its
  * elements; M and N at most 2^26, M * N at most 2^36 (else MOE_ERR_UNSUPPORTED).
  * Each output is one sum in an order that depends on M, N and K alone: reproducible
@@ -706,8 +708,9 @@ moe_status_t moe_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const uint8_t
  * expert e, y[s] = bf16(x[s] W_e^T).  x E4M3 [route_slots, K] with x_sf
  * [route_slots, ceil(K / 128)], w E4M3 [E_l, N, K], w_sf fp32 [E_l, ceil(N / 128),
  * ceil(K / 128)], y bf16 [route_slots, N], 16-byte aligned.  N a multiple of 8;
- * otherwise the limits of moe_linear_fp8, with N and K at most 2^16.  The tile that
- * moe_default_tile gives for MOE_QUANT_MXFP8_MXFP4 suits it.  The sums' order depends
+ * otherwise the limits of moe_linear_fp8, with N and K at most 2^16, and with a tile
+ * of 16 rows max_tiles * ceil(N / 16) below 2^23.  The tile that moe_default_tile
+ * gives for MOE_QUANT_MXFP8_MXFP4 suits it.  The sums' order depends
  * on the plan's tile, N and K alone. */
 moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const moe_plan_t* plan, const uint8_t* w,
                                     const float* w_sf, int N, int K, uint16_t* y, moe_stream_t stream);
@@ -724,7 +727,8 @@ moe_status_t moe_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const ui
 
 /* moe_grouped_linear_fp8_wgrad: the same of every expert from the valid slots of its
  * range: dy bf16 [route_slots, N], x E4M3 [route_slots, K] with x_sf, dw fp32
- * [E_l, N, K].  An expert without a route gets zeros (or keeps its values). */
+ * [E_l, N, K], E_l * N * K at most 2^37 (else MOE_ERR_UNSUPPORTED).  An expert without
+ * a route gets zeros (or keeps its values). */
 moe_status_t moe_grouped_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf,
                                           const moe_plan_t* plan, int N, int K, int accumulate, float* dw,
                                           moe_stream_t stream);

@@ -245,7 +245,7 @@ DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
   return v;
 }
 
-// One workgroup a tile at a time, K in stages of 128 in a ring of buffers that
+// One workgroup a tile at a time (a plan's tiles have BM rows), K in stages of 128 in a ring of buffers that
 // LDS-DMA fills.  A wavefront computes 16 TM rows by 16 TN columns, W's rows the
 // first operand: a lane then has 4 TN consecutive columns of one row of y, if
 // row 4 a + b of W's tile t is column 4 TN a + 4 t + b.  The rows' fragments
@@ -269,8 +269,7 @@ __global__ __launch_bounds__(S::NT * S::KG, 2) void fp8_tile_kernel(const Linear
   // tiles of this workgroup: XCD b & 7 takes a contiguous run of them, its
   // workgroups take them in turn; 8 rows of tiles high, so that what an XCD
   // works on at a time shares its rows in the L2
-  const int parts = a.tile_expert ? a.tile / BM : 1;
-  const int tiles_m = a.tile_expert ? ld_uniform(a.num_tiles) * parts : (int)((a.M + BM - 1) / BM);
+  const int tiles_m = a.tile_expert ? ld_uniform(a.num_tiles) : (int)((a.M + BM - 1) / BM);
   const int64_t tiles = (int64_t)tiles_m * tiles_n, per = (tiles + 7) / 8;
   const int step = gridDim.x >> 3;
   const int64_t first = (blockIdx.x & 7) * per, last = min(first + per, tiles);
@@ -289,15 +288,14 @@ __global__ __launch_bounds__(S::NT * S::KG, 2) void fp8_tile_kernel(const Linear
     const int rows = min(GM, tiles_m - group * GM), tm = group * GM + in % rows;
     At o;
     o.n0 = in / rows * BN;
+    o.m0 = (int64_t)tm * BM;
     if (!a.tile_expert) {
-      o.m0 = (int64_t)tm * BM;
       o.end = min(a.M, o.m0 + BM);
       o.w = a.w;
       o.w_sf = a.w_sf;
     } else {
-      const int pt = tm / parts, e = ld_uniform(a.tile_expert + pt);
-      o.m0 = (int64_t)pt * a.tile + (tm - pt * parts) * BM;
-      o.end = min(o.m0 + BM, (int64_t)ld_uniform(a.tile_limit + pt));
+      const int e = ld_uniform(a.tile_expert + tm);
+      o.end = ld_uniform(a.tile_limit + tm);
       o.w = a.w + (int64_t)e * a.N * a.K;
       o.w_sf = a.w_sf + (int64_t)e * ((a.N + 127) / 128) * kb;
     }
@@ -545,7 +543,7 @@ hipError_t launch_tile_as(const LinearFp8Params& a, hipStream_t s) {
   const hipError_t err = allow_lds<fp8_tile_kernel<S, WIDE>>(S::LDS, &cus);
   if (err != hipSuccess) return err;
   const int tn = (a.N + S::BN - 1) / S::BN;
-  const int64_t tm = a.tile_expert ? (int64_t)a.tiles * (a.tile / S::BM) : (a.M + S::BM - 1) / S::BM;
+  const int64_t tm = a.tile_expert ? (int64_t)a.tiles : (a.M + S::BM - 1) / S::BM;
   const int64_t most = (int64_t)(cus >= 8 ? cus / 8 * 8 : 8) * PER_CU, tiles = (tm * tn + 7) / 8 * 8;
   const int64_t grid = S::KG == 1 && tiles > most ? most : tiles;  // (K groups: a tile a workgroup)
   fp8_tile_kernel<S, WIDE><<<(unsigned)grid, S::NT * S::KG, S::LDS, s>>>(a, tn);
@@ -570,36 +568,38 @@ using Split4Low = Tile<1, 1, 2, 4, 2, 4>;  // 32 x 64, K in four
 hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
   constexpr int64_t CUS = 256;
   if (a.tile_expert) {
-    // (experts of 4096 x 6144, 32 of them: 16 rows a tile through the tiled kernel
-    // would multiply half of nothing; 1000 rows in tiles of 32: 190 us, 396 streamed
-    // in 16-row pieces; 2000 in tiles of 64: 204 against 621)
-    if (a.tile <= 16) return launch_stream(a, s);
-    if (a.tile <= 32) return launch_tile<Low>(a, s);
-    if (a.tile <= 64) return launch_tile<Small>(a, s);
-    if (a.tile <= 128) return launch_tile<Middle>(a, s);
-    return launch_tile<Big>(a, s);
+    // a workgroup for each of the plan's tiles (32 experts of 4096 x 6144, in tiles of 32
+    // and 64 against streaming the same plan in pieces of 16: 1000 rows 206 us, 396; 2000
+    // rows 208, 621)
+    switch (a.tile) {
+      case 16: return launch_stream(a, s);
+      case 32: return launch_tile<Low>(a, s);
+      case 64: return launch_tile<Small>(a, s);
+      case 128: return launch_tile<Middle>(a, s);
+      default: return launch_tile<Big>(a, s);  // 256
+    }
   }
   auto tiles = [&](int m, int n) { return ((a.M + m - 1) / m) * ((a.N + n - 1) / n); };
   // The streaming kernel while its 16 x 16 tiles have little to do together: it
   // waits for memory once, the others for each stage (128 x 724 x 1024: 6.2 us
   // against 8.4; 128 x 256 x 8192: 12.9 against 15.2; 512 x 724 x 1024: 11.4
-  // against 8.6; 64 x 4096 x 6144: 28.7 against 12.7).
+  // against 8.6; 64 x 4096 x 6144: 28.7 against 11.3).
   if (a.M <= 16 || tiles(16, 16) * ((a.K + 127) / 128) <= 8192) return launch_stream(a, s);
   // A wavefront alone on a SIMD is bound by its own instructions, about 1000 cycles
   // a stage of 32 x 64 results.  While all tiles have a CU each, K is split over
-  // more wavefronts: 64 x 4096 x 6144 12.7 us against 24.9 in 64 x 128 tiles, 128 x 4096
-  // x 4096 10.7 against 19.3, 256 x 4096 x 4096 13.1 against 19.7, 512 x 4096 x 4096
-  // 19.0 against 22.1.
+  // more wavefronts: 64 x 4096 x 6144 11.3 us against 24.9 in 64 x 128 tiles, 128 x 4096
+  // x 4096 8.3 against 19.3, 256 x 4096 x 4096 13.1 against 19.7, 512 x 4096 x 4096
+  // 16.1 against 22.1.
   if (tiles(32, 64) <= CUS) return launch_tile<Split4Low>(a, s);
   if (tiles(64, 64) <= CUS) return launch_tile<Split4>(a, s);
   if (tiles(64, 128) <= CUS) return launch_tile<Split2>(a, s);
   // 256 x 256 tiles where they fill whole rounds of the CUs, three quarters at
   // least (8000 x 2000 x 2000, one full round: 53.6 us against 49.5 in 128 x 128 tiles;
-  // 4096 x 4096 x 4096: 77 against 99)
+  // 4096 x 4096 x 4096: 68 against 99)
   const int64_t big = tiles(256, 256), rounds = (big + CUS - 1) / CUS;
   if (4 * big >= 3 * CUS * rounds && a.K >= 1024) return launch_tile<Big>(a, s);
   // (4096 x 724 x 1024, 192 tiles of 128 x 128: 19.2 us in 64 x 128, 20.7; 2048 x 4096 x
-  // 2048, 512 of them: 29.9, 26.4)
+  // 2048, 512 of them: 29.9, 22.5)
   if (tiles(128, 128) <= CUS) return launch_tile<Small>(a, s);
   return launch_tile<Middle>(a, s);
 }

@@ -299,15 +299,16 @@ hipError_t launch(const WgradParams& a, hipStream_t s) {
 hipError_t launch_wgrad_fp8(const WgradParams& a, hipStream_t s) {
   constexpr int64_t CUS = 256;
   auto tiles = [&](int n, int k) { return (int64_t)a.experts * ((a.N + n - 1) / n) * ((a.K + k - 1) / k); };
-  // 128 x 256 tiles while there are two for each CU (4096 x 4096 x 4096, 512 of them:
-  // 133 us against 142 in 128 x 128 tiles; 1000 x 4096 x 4096: 47 against 51)
-  if (tiles(128, 256) >= 2 * CUS) return launch<Tile<4, 8, 1>>(a, s);
+  // 128 x 256 tiles while there is one for each CU (4096 x 4096 x 4096, 512 of them:
+  // 147 us against 183 in 128 x 128 tiles; 2048 x 4096 x 2048, 256: 48 against 51; 32
+  // experts of 512 rows, 4096 x 1536: 347 against 555)
+  if (tiles(128, 256) >= CUS) return launch<Tile<4, 8, 1>>(a, s);
   // 128 x 128, rows in two, while that is one for every other CU (1237 x 2056 x 1568,
-  // 221 of them: 22.4 us, in 64 x 128 tiles 23.8, in 128 x 256 35; 4096 x 2048 x 2048:
-  // 48, 51, 87)
+  // 221 of them: 22.7 us, in 64 x 128 tiles 25.0, in 128 x 256 34; 4096 x 2048 x 2048:
+  // 48, 55, 82)
   if (tiles(128, 128) > CUS / 2) return launch<Tile<4, 4, 2>>(a, s);
   // 64 x 128 below, rows in two, or in four where they are many (16384 x 1024 x 1024:
-  // 113 us in two, 93 in four; 64 x 2048 x 2048: 9.2, 14.7)
+  // 121 us in two, 99 in four; 512 x 1024 x 1024: 9.1, 9.9; 64 x 2048 x 2048: 8.8, 14.5)
   if (a.M / a.experts < 1024) return launch<Tile<2, 4, 2>>(a, s);
   return launch<Tile<2, 4, 4>>(a, s);
 }
