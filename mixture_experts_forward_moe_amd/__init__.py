@@ -647,18 +647,14 @@ def _nb(cols: int) -> int:
     return (cols + 127) // 128
 
 
-def _sizes(where, **given):
-    """The two sizes of each tensor, one after another."""
+def _two(where, name, t):
+    """The two sizes of a tensor."""
     try:
-        return [n for t in given.values() for n in _two(t.shape)]
+        a, b = t.shape
+        return a, b
     except (AttributeError, ValueError):
-        _shapes(where, **given)
+        _shapes(where, **{name: t})
         raise
-
-
-def _two(shape):
-    a, b = shape
-    return a, b
 
 
 def _plan_arg(where, plan, dev):
@@ -674,7 +670,7 @@ def moe_quantize_fp8(x, q, q_sf, stream=None):
     """E4M3 codes q [rows, cols] and E8M0 scales q_sf [rows, ceil(cols / 128)]
     of bf16 rows x, which may be strided."""
     w = "moe_quantize_fp8"
-    rows, cols = _sizes(w, x=x)
+    rows, cols = _two(w, "x", x)
     dev = x.get_device()
     xp, xs = _rows(w, "x", x, (rows, cols), _BF16, dev)
     _check(lib().moe_quantize_fp8(xp, xs, rows, cols, _arg(w, "q", q, (rows, cols), _BYTE, dev),
@@ -703,7 +699,7 @@ def moe_dispatch(x, plan: MoePlan, rows=None, q=None, q_sf=None, stream=None):
     routes: as bf16 rows [route_slots, H], and / or quantised, q [route_slots,
     H] with q_sf [route_slots, ceil(H / 128)]."""
     w = "moe_dispatch"
-    M, H = _sizes(w, x=x)
+    H = _two(w, "x", x)[1]
     dev = x.get_device()
     p = _plan_arg(w, plan, dev)
     n = plan.route_slots
@@ -717,7 +713,7 @@ def moe_dispatch_backward(d_rows, plan: MoePlan, dx, accumulate=False, stream=No
     """dx [M, H] = (dx +) the sum of d_rows [route_slots, H] over each token's
     routes."""
     w = "moe_dispatch_backward"
-    n, H = _sizes(w, d_rows=d_rows)
+    H = _two(w, "d_rows", d_rows)[1]
     dev = d_rows.get_device()
     p = _plan_arg(w, plan, dev)
     _check(lib().moe_dispatch_backward(_arg(w, "d_rows", d_rows, (plan.route_slots, H), _BF16, dev), p, H,
@@ -730,7 +726,7 @@ def moe_finalize_backward(dout, y2, plan: MoePlan, topk_weights, dy2=None, q=Non
     """The gradients of moe_finalize: of its rows (dy2 bf16 [route_slots, H],
     and / or quantised in q, q_sf) and, with y2, of the routing weights."""
     w = "moe_finalize_backward"
-    M, H = _sizes(w, dout=dout)
+    H = _two(w, "dout", dout)[1]
     dev = dout.get_device()
     p = _plan_arg(w, plan, dev)
     n = plan.route_slots
@@ -747,7 +743,8 @@ def moe_linear_fp8(x, x_sf, w, w_sf, y, bias=None, accumulate=False, stream=None
     w E4M3 [N, K] with fp32 w_sf [ceil(N / 128), ceil(K / 128)], y bf16 or fp32
     [M, N].  What the matrix instruction keeps of a product stands in moe.h."""
     f = "moe_linear_fp8"
-    M, K, N, _ = _sizes(f, x=x, w=w)
+    M, K = _two(f, "x", x)
+    N = _two(f, "w", w)[0]
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_fp8(
@@ -762,7 +759,7 @@ def moe_grouped_linear_fp8(x, x_sf, plan: MoePlan, w, w_sf, y, stream=None):
     [route_slots, K], w E4M3 [E_l, N, K] with w_sf [E_l, ceil(N / 128),
     ceil(K / 128)], y bf16 [route_slots, N]."""
     f = "moe_grouped_linear_fp8"
-    n, K, _, N = _sizes(f, x=x, y=y)
+    K, N = _two(f, "x", x)[1], _two(f, "y", y)[1]
     dev = x.get_device()
     p = _plan_arg(f, plan, dev)
     n, E = plan.route_slots, plan.num_local_experts
@@ -776,7 +773,8 @@ def moe_linear_fp8_wgrad(dy, x, x_sf, dw, accumulate=False, stream=None):
     """dw [N, K] = dy^T x (+ dw) in fp32, from bf16 dy [M, N] and the product's
     rows in 8 bits, x E4M3 [M, K] with x_sf."""
     f = "moe_linear_fp8_wgrad"
-    M, N, _, K = _sizes(f, dy=dy, x=x)
+    M, N = _two(f, "dy", dy)
+    K = _two(f, "x", x)[1]
     dev = dy.get_device()
     _check(lib().moe_linear_fp8_wgrad(
         _arg(f, "dy", dy, (M, N), _BF16, dev), _arg(f, "x", x, (M, K), _BYTE, dev),
@@ -788,7 +786,7 @@ def moe_grouped_linear_fp8_wgrad(dy, x, x_sf, plan: MoePlan, dw, accumulate=Fals
     """The same of every expert, dw [E_l, N, K], from the valid slots of its
     range: dy bf16 [route_slots, N], x E4M3 [route_slots, K]."""
     f = "moe_grouped_linear_fp8_wgrad"
-    n, N, _, K = _sizes(f, dy=dy, x=x)
+    N, K = _two(f, "dy", dy)[1], _two(f, "x", x)[1]
     dev = dy.get_device()
     p = _plan_arg(f, plan, dev)
     n, E = plan.route_slots, plan.num_local_experts
@@ -805,7 +803,7 @@ def moe_gated_act_fp8(h, y, y_sf, hq=None, hq_sf=None, plan: MoePlan | None = No
     backward pass (hq [rows, 2I], hq_sf [rows, 2 ceil(I / 128)]).  With a plan
     its valid slots are the rows."""
     w = "moe_gated_act_fp8"
-    rows, I = _sizes(w, y=y)
+    rows, I = _two(w, "y", y)
     dev = y.get_device()
     p = None if plan is None else _plan_arg(w, plan, dev)
     if plan is not None:
@@ -824,7 +822,7 @@ def moe_gated_act_fp8_backward(hq, hq_sf, dy, dh=None, dq=None, dq_sf=None, plan
     [rows, I]: dh bf16 [rows, 2I] and / or quantised, dq [rows, 2I] with dq_sf
     [rows, 2 ceil(I / 128)]."""
     w = "moe_gated_act_fp8_backward"
-    rows, I = _sizes(w, dy=dy)
+    rows, I = _two(w, "dy", dy)
     dev = dy.get_device()
     p = None if plan is None else _plan_arg(w, plan, dev)
     if plan is not None:

@@ -266,20 +266,38 @@ __global__ __launch_bounds__(256 * S::MG, S::MG == 4 ? 4 : 2) void wgrad_kernel(
       for (int i = 0; i < TN * TK; i++) acc[i / TN][i % TN] += to[at + 64 * i];
     }
   }
-  if (mg > 0) return;
+  if constexpr (MG > 1) {
+    __syncthreads();  // (what was handed over has been read)
+    if (mg > 0) return;
+  }
 
-  // element i of lane (r, q): k = 4 q + i, n = r
-  float* dw = a.dw + (int64_t)e * a.N * a.K;
+  // element i of lane (r, q): k = 4 q + i, n = r.  Out through a part of LDS of the
+  // wavefront's own (what others may still read of the buffers is of no stage), 16 rows
+  // at a time, their chunks of 16 bytes swizzled by the row, in lines of 64 TK bytes.
+  constexpr int C = 4 * TK, LINES = 64 / C;  // chunks of a row; rows a store
+  uint8_t* out = smem_all + wave * 16 * 16 * C;
+  const int c = lane % C, k = k0 + 16 * TK * wk + 4 * c;
+  float* dw = a.dw + (int64_t)e * a.N * a.K + k;
 #pragma unroll
   for (int j = 0; j < TN; j++) {
-    const int n = n0 + 16 * (TN * wn + j) + r;
 #pragma unroll
-    for (int i = 0; i < TK; i++) {
-      const int k = k0 + 16 * (TK * wk + i) + 4 * q;
-      if (n >= a.N || k >= a.K) continue;
-      f32x4_t* p = reinterpret_cast<f32x4_t*>(dw + (int64_t)n * a.K + k);
-      *p = a.accumulate ? *p + acc[i][j] : acc[i][j];
+    for (int i = 0; i < TK; i++)
+      *reinterpret_cast<f32x4_t*>(out + 16 * (C * r + ((4 * i + q) ^ (r & 7)))) = acc[i][j];
+    wave_fence();
+    f32x4_t v[16 / LINES];
+#pragma unroll
+    for (int i = 0; i < 16 / LINES; i++) {
+      const int row = LINES * i + lane / C;
+      v[i] = *reinterpret_cast<const f32x4_t*>(out + 16 * (C * row + (c ^ (row & 7))));
     }
+#pragma unroll
+    for (int i = 0; i < 16 / LINES; i++) {
+      const int n = n0 + 16 * (TN * wn + j) + LINES * i + lane / C;
+      if (n >= a.N || k >= a.K) continue;
+      f32x4_t* p = reinterpret_cast<f32x4_t*>(dw + (int64_t)n * a.K);
+      *p = a.accumulate ? *p + v[i] : v[i];
+    }
+    wave_fence();
   }
 }
 
