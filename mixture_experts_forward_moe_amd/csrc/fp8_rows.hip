@@ -137,6 +137,7 @@ __global__ __launch_bounds__(256) void fp8_rows_kernel(const uint16_t* x, int64_
 
 // A wavefront reads its part of a token's row once, and writes it at the
 // slots of the token's routes; a token without a local route is not read.
+// 65536 tokens of 6144, 65000 routes, codes: 174 us, 6.9 TB/s.
 template <int U>
 __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams a, int parts) {
   const int64_t w = wave_number(), t = w / parts;
@@ -176,43 +177,33 @@ __global__ __launch_bounds__(256) void dispatch_kernel(const DispatchParams a, i
   }
 }
 
-// dx[t] = the sum over the token's routes, in their order, in fp32
-template <int U>
+// dx[t] = the sum over the token's routes, in their order, in fp32.  (A piece a
+// wavefront: four of them at once are no faster, 16384 tokens of 8 routes of 4096
+// 239 us and 241, 8192 of 2 of 8192 74 and 81.)
 __global__ __launch_bounds__(256) void dispatch_backward_kernel(const uint16_t* dxp, const int32_t* slots, int64_t M,
                                                                 int top_k, int H, int accumulate, int parts,
                                                                 uint16_t* dx) {
   const int64_t w = wave_number(), t = w / parts;
   if (t >= M) return;
-  const int lane = threadIdx.x & 63, c0 = (int)(w - t * parts) * (PIECE * U) + 8 * lane;
+  const int lane = threadIdx.x & 63, c = (int)(w - t * parts) * PIECE + 8 * lane;
   const int slot = lane < top_k ? slots[t * top_k + lane] : -1;
   uint64_t routes = __ballot(slot >= 0);
-  float acc[U][8];
-#pragma unroll
-  for (int u = 0; u < U; u++) {
-    const int c = c0 + PIECE * u;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (accumulate && c < H) v = ld8(dx + t * H + c);
-    unpack8(v, acc[u]);
-  }
+  float acc[8];
+  u32x4_t old = {0u, 0u, 0u, 0u};
+  if (accumulate && c < H) old = ld8(dx + t * H + c);
+  unpack8(old, acc);
   while (routes) {
     const int j = __builtin_ctzll(routes);
     routes &= routes - 1;
     const int64_t s = __builtin_amdgcn_readlane(slot, j);
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int c = c0 + PIECE * u;
-      if (c >= H) continue;
+    if (c < H) {
       float v[8];
       unpack8(ld8(dxp + s * H + c), v);
 #pragma unroll
-      for (int i = 0; i < 8; i++) acc[u][i] += v[i];
+      for (int i = 0; i < 8; i++) acc[i] += v[i];
     }
   }
-#pragma unroll
-  for (int u = 0; u < U; u++) {
-    const int c = c0 + PIECE * u;
-    if (c < H) st8(dx + t * H + c, pack8(acc[u]));
-  }
+  if (c < H) st8(dx + t * H + c, pack8(acc));
 }
 
 // ------------------------------------------------------------- gradients of the finalize
@@ -220,7 +211,8 @@ __global__ __launch_bounds__(256) void dispatch_backward_kernel(const uint16_t* 
 // A workgroup takes a token: its dout row stays in registers (NI pieces of
 // 2048 values), each of its routes' y2 rows passes once.  The dot products are
 // sums of fp32 products within a lane, then over the lanes and the wavefronts
-// in a fixed order.
+// in a fixed order.  16384 tokens of 8 routes of 4096 (y2 read, gradients written in
+// bf16 and in codes): 550 us, 5.1 TB/s.
 template <int NI>
 __global__ __launch_bounds__(256) void finalize_backward_kernel(const FinalizeBackwardParams a) {
   __shared__ float part[4][64];
@@ -314,6 +306,8 @@ DEV GatePart gate_part(float g, float u, const GateAct& p) {
 
 // y = f(g) up(u) of eight columns a lane, rounded to bf16 and quantised; g and u
 // quantised too where they are kept.  A plan's padding slots are passed over.
+// 65536 x 2048: 207 us, 4.5 TB/s (GeGLU 185), its gradient 248, 5.4 TB/s: HBM, and the
+// few rows' 3.2 to 3.6 us are a launch's and one trip to memory.
 template <int AK, int U>
 __global__ __launch_bounds__(256) void act_kernel(const ActParams a, int parts) {
   const int64_t w = wave_number(), row = w / parts;
@@ -423,7 +417,8 @@ __global__ __launch_bounds__(256) void act_backward_kernel(const ActBackwardPara
 // ------------------------------------------------------------- weights
 
 // A workgroup takes a block of 128 x 128: scale = amax / 448 (2^-126 at least),
-// codes of w / scale, stored in w's order and, through LDS, transposed.
+// codes of w / scale, stored in w's order and, through LDS, transposed.  32 x 4096 x
+// 6144: 450 us, with the transposed codes 604, both 5.3 TB/s.
 __global__ __launch_bounds__(256) void fp8_weight_kernel(const uint16_t* w, int N, int K, uint8_t* q, float* sf,
                                                          uint8_t* qt, float* sft) {
   constexpr int PITCH = BLOCK + 4;
@@ -505,8 +500,10 @@ __global__ __launch_bounds__(256) void fp8_weight_kernel(const uint16_t* w, int 
 int parts_of(int cols, int u) { return (cols + PIECE * u - 1) / (PIECE * u); }
 unsigned grid_of(int64_t rows, int parts) { return (unsigned)((rows * parts + 3) / 4); }
 
-// Few rows: a piece a wavefront, so that all of them are on their way at once;
-// many: four, whose loads go out together.
+// Few rows: a piece a wavefront, so that all of them are on their way at once; many:
+// several, whose loads go out together.  Rows quantised, one piece and four: 8 x 6144
+// 2.4 us and 2.7, 2048 x 4096 5.4 and 4.9, 16384 x 4096 33.5 and 30.2 (6.7 TB/s);
+// activations, one and two: 301 x 1536 3.4 and 4.3, 65536 x 2048 226 and 207.
 bool few(int64_t rows, int cols) { return rows * parts_of(cols, 1) <= 4096; }
 
 }  // namespace
@@ -530,26 +527,24 @@ hipError_t launch_quantize_fp8_weight(const uint16_t* w, int batches, int N, int
   return hipGetLastError();
 }
 
+// (With codes, one piece and two: 512 tokens of 8 routes of 4096 5.7 us and 7.3, 65536
+// of about one route of 6144 219 and 174; bf16 alone is no faster in two, those 231 and
+// 252.)
 hipError_t launch_dispatch(const DispatchParams& a, hipStream_t s) {
-  if (few(a.M, a.H)) {
+  if (few(a.M, a.H) || !a.q) {
     const int p = parts_of(a.H, 1);
     dispatch_kernel<1><<<grid_of(a.M, p), 256, 0, s>>>(a, p);
   } else {
-    const int p = parts_of(a.H, 4);
-    dispatch_kernel<4><<<grid_of(a.M, p), 256, 0, s>>>(a, p);
+    const int p = parts_of(a.H, 2);
+    dispatch_kernel<2><<<grid_of(a.M, p), 256, 0, s>>>(a, p);
   }
   return hipGetLastError();
 }
 
 hipError_t launch_dispatch_backward(const uint16_t* dxp, const int32_t* slots, int64_t M, int top_k, int H,
                                     int accumulate, uint16_t* dx, hipStream_t s) {
-  if (few(M, H)) {
-    const int p = parts_of(H, 1);
-    dispatch_backward_kernel<1><<<grid_of(M, p), 256, 0, s>>>(dxp, slots, M, top_k, H, accumulate, p, dx);
-  } else {
-    const int p = parts_of(H, 4);
-    dispatch_backward_kernel<4><<<grid_of(M, p), 256, 0, s>>>(dxp, slots, M, top_k, H, accumulate, p, dx);
-  }
+  const int p = parts_of(H, 1);
+  dispatch_backward_kernel<<<grid_of(M, p), 256, 0, s>>>(dxp, slots, M, top_k, H, accumulate, p, dx);
   return hipGetLastError();
 }
 
