@@ -983,7 +983,7 @@ moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const
   const moe_status_t s = linear_fp8_shape(plan->route_slots, N, K, 1 << 16);
   if (s != MOE_OK) return s;
   if (N % 8 != 0) return MOE_ERR_UNSUPPORTED;
-  // (tiles of 16 rows: 512 threads for each 16 columns, below 2^32 in all)
+  // (tiles of 16 rows: 512 threads for each 32 columns or fewer, below 2^32 in all)
   if (plan->tile == 16 && (int64_t)plan->max_tiles * ((N + 15) / 16) >= 1 << 23) return MOE_ERR_UNSUPPORTED;
   if (plan->M > 0 && N > 0 && (!x || !x_sf || !w || !w_sf || !y)) return MOE_ERR_INVALID_ARGUMENT;
   if (unaligned16(x) || unaligned16(w) || unaligned16(y) || unaligned4(w_sf)) return MOE_ERR_UNSUPPORTED;

@@ -144,48 +144,63 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
 
 constexpr int STREAM_WAVES = 8;
 
-// 16 rows of x and 16 of W a workgroup: its wavefronts split K and load both
+// 16 rows of x and 16 TN of W a workgroup: its wavefronts split K and load both
 // straight into registers; their sums meet in LDS in a fixed order.
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane (row r = lane & 15, group q = lane
 // >> 4) holds 32 values of K of its row; which ones is the same for both
 // operands, and the scale is one for all of them.
+template <int TN>
 __global__ __launch_bounds__(64 * STREAM_WAVES) void fp8_stream_kernel(const LinearFp8Params a, int tiles_n) {
   constexpr int NW = STREAM_WAVES;
-  __shared__ f32x4_t part[NW][64];
+  __shared__ f32x4_t part[NW][TN][64];
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int g = blockIdx.x / tiles_n, n0 = (blockIdx.x - g * tiles_n) * 16;
+  const int g = blockIdx.x / tiles_n, n0 = (blockIdx.x - g * tiles_n) * (16 * TN);
   Group o;
   if (!group_of(a, g, o)) return;
   const int kb = (a.K + 127) / 128;
   const int per = (kb + NW - 1) / NW, s_first = wave * per, s_end = min(s_first + per, kb);
-  const uint8_t* w = o.w + (int64_t)min(a.N - 1, n0 + r) * a.K + 16 * q;
+  const uint8_t* w[TN];
+#pragma unroll
+  for (int t = 0; t < TN; t++) w[t] = o.w + (int64_t)min(a.N - 1, n0 + 16 * t + r) * a.K + 16 * q;
   const float* wsf = o.w_sf + (int64_t)(n0 >> 7) * kb;
   const int64_t xr = min(o.first + r, o.end - 1);
   const uint8_t *x = a.x + xr * a.K + 16 * q, *xsf = a.x_sf + xr * kb;
-  f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4_t acc[TN];
+#pragma unroll
+  for (int t = 0; t < TN; t++) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   const u32x4_t zero = {0u, 0u, 0u, 0u};
   for (int s = s_first; s < s_end; s++) {
     const bool in0 = 128 * s + 16 * q < a.K, in1 = 128 * s + 64 + 16 * q < a.K;
-    const u32x4_t w0 = in0 ? ld16(w + 128 * s) : zero, w1 = in1 ? ld16(w + 128 * s + 64) : zero;
+    u32x4_t w0[TN], w1[TN];
+#pragma unroll
+    for (int t = 0; t < TN; t++) {
+      w0[t] = in0 ? ld16(w[t] + 128 * s) : zero;
+      w1[t] = in1 ? ld16(w[t] + 128 * s + 64) : zero;
+    }
     const u32x4_t x0 = in0 ? ld16(x + 128 * s) : zero, x1 = in1 ? ld16(x + 128 * s + 64) : zero;
     const float ws = wsf[s];
     const int xs = xsf[s];
-    const i32x8_t b = {(int)w0[0], (int)w0[1], (int)w0[2], (int)w0[3], (int)w1[0], (int)w1[1], (int)w1[2], (int)w1[3]};
     const i32x8_t c = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
-    const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
-    const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c, b, none, 0, 0, 0, xs, 0, 127);
 #pragma unroll
-    for (int i = 0; i < 4; i++) acc[i] = fmaf(p[i], ws, acc[i]);
+    for (int t = 0; t < TN; t++) {
+      const i32x8_t b = {(int)w0[t][0], (int)w0[t][1], (int)w0[t][2], (int)w0[t][3],
+                         (int)w1[t][0], (int)w1[t][1], (int)w1[t][2], (int)w1[t][3]};
+      const f32x4_t none = {0.0f, 0.0f, 0.0f, 0.0f};
+      const f32x4_t p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(c, b, none, 0, 0, 0, xs, 0, 127);
+#pragma unroll
+      for (int i = 0; i < 4; i++) acc[t][i] = fmaf(p[i], ws, acc[t][i]);
+    }
   }
-  part[wave][lane] = acc;
+#pragma unroll
+  for (int t = 0; t < TN; t++) part[wave][t][lane] = acc[t];
   __syncthreads();
   // element i of lane (r, q): row 4 q + i, column r
-  if (wave > 0 || n0 + r >= a.N) return;
-  f32x4_t v = part[0][lane];
+  if (wave >= TN || n0 + 16 * wave + r >= a.N) return;
+  f32x4_t v = part[0][wave][lane];
 #pragma unroll
-  for (int k = 1; k < NW; k++) v += part[k][lane];
-  const int n = n0 + r;
+  for (int k = 1; k < NW; k++) v += part[k][wave][lane];
+  const int n = n0 + 16 * wave + r;
   const float bias = a.bias ? a.bias[n] : 0.0f;
 #pragma unroll
   for (int i = 0; i < 4; i++) {
@@ -194,10 +209,19 @@ __global__ __launch_bounds__(64 * STREAM_WAVES) void fp8_stream_kernel(const Lin
   }
 }
 
+// 32 columns a workgroup, which read x once for both halves, where that leaves one for
+// each CU at least: 8 x 8192 x 8192 14.6 us against 16.9, 4 x 65536 x 2048 23 against 26,
+// 32 experts of 555 rows, 4096 x 6144, 228 against 295, of 68 rows 145 against 142; 8 x
+// 4096 x 6144, 128 workgroups, 10.1 against 7.3.
 hipError_t launch_stream(const LinearFp8Params& a, hipStream_t s) {
-  const int tn = (a.N + 15) / 16;
   const int64_t groups = a.tile_expert ? a.tiles : (a.M + 15) / 16;
-  fp8_stream_kernel<<<(unsigned)(groups * tn), 64 * STREAM_WAVES, 0, s>>>(a, tn);
+  const int tn = (a.N + 31) / 32;
+  if (groups * tn >= 256) {
+    fp8_stream_kernel<2><<<(unsigned)(groups * tn), 64 * STREAM_WAVES, 0, s>>>(a, tn);
+  } else {
+    const int t1 = (a.N + 15) / 16;
+    fp8_stream_kernel<1><<<(unsigned)(groups * t1), 64 * STREAM_WAVES, 0, s>>>(a, t1);
+  }
   return hipGetLastError();
 }
 
@@ -580,11 +604,12 @@ hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
     }
   }
   auto tiles = [&](int m, int n) { return ((a.M + m - 1) / m) * ((a.N + n - 1) / n); };
-  // The streaming kernel while its 16 x 16 tiles have little to do together: it
-  // waits for memory once, the others for each stage (128 x 724 x 1024: 6.2 us
-  // against 8.4; 128 x 256 x 8192: 12.9 against 15.2; 512 x 724 x 1024: 11.4
-  // against 8.6; 64 x 4096 x 6144: 28.7 against 11.3).
-  if (a.M <= 16 || tiles(16, 16) * ((a.K + 127) / 128) <= 8192) return launch_stream(a, s);
+  // The streaming kernel while its 16 x 16 tiles have little to do together, or are few:
+  // it waits for memory once, the others for each stage (128 x 724 x 1024: 4.7 us against
+  // 6.4; 32 x 2048 x 2048 4.9, 5.6; 128 x 256 x 8192, 128 tiles, 11.4, 13.2; 256 x 1024 x
+  // 1024 5.7, 4.7; 64 x 2048 x 2048 5.9, 5.7; 32 x 4096 x 4096 9.3, 8.2).
+  const int64_t pieces = tiles(16, 16);
+  if (a.M <= 16 || pieces * ((a.K + 127) / 128) <= 4096 || pieces <= CUS / 2) return launch_stream(a, s);
   // A wavefront alone on a SIMD is bound by its own instructions, about 1000 cycles
   // a stage of 32 x 64 results.  While all tiles have a CU each, K is split over
   // more wavefronts: 64 x 4096 x 6144 11.3 us against 24.9 in 64 x 128 tiles, 128 x 4096

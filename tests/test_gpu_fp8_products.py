@@ -44,7 +44,7 @@ SHAPES = [(1, 1, 16), (1, 17, 128), (3, 64, 144), (8, 300, 1040), (16, 16, 8192)
           (31, 33, 400), (33, 136, 2064), (64, 200, 512), (65, 1000, 1552), (100, 129, 4096), (128, 128, 128),
           (129, 257, 272), (200, 520, 96), (256, 256, 1024), (300, 1024, 2048), (511, 2056, 1568), (513, 768, 640),
           (1000, 3000, 528), (1237, 2056, 1568), (2048, 2048, 512), (2500, 1111, 1024), (4096, 4096, 1168),
-          (5000, 520, 160), (7001, 264, 4112)]
+          (5000, 520, 160), (7001, 264, 4112), (1, 8200, 160), (5, 8193, 400), (16, 9011, 1168), (12, 16384, 144)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
