@@ -5,6 +5,7 @@ with nothing to do)."""
 import ctypes
 
 import pytest
+import torch  # noqa: F401  (before the library, which is loaded below: one HIP runtime for both)
 
 import mixture_experts_forward_moe_amd as moe
 
