@@ -101,6 +101,7 @@ __global__ __launch_bounds__(256 * S::MG, S::MG == 4 ? 4 : 2) void wgrad_kernel(
 
   // rows of this group: as many stages for each (past the end they are 0)
   const int64_t all = a.offsets ? ld_uniform(a.counts + e) : a.M;
+  if (all == 0 && a.accumulate) return;  // nothing to add
   const int stages = (int)((all + S::ST * MG - 1) / (S::ST * MG));
   const int64_t skip = (int64_t)mg * stages * S::ST, first = (a.offsets ? ld_uniform(a.offsets + e) : 0) + skip;
   const int64_t rows = all - skip;
