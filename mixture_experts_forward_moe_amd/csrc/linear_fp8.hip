@@ -59,7 +59,8 @@ DEV void store_one(const LinearFp8Params& a, int64_t at, float v) {
 // bf16 that is overwritten, its rows aligned to 16 bytes, leaves through the
 // wavefront's own part of LDS, 16 rows at a time (chunks swizzled by the row), in whole
 // lines.  Rows of odd sizes do value by value, from neighbouring lanes (16384 x 6147 x
-// 4096: 533 us, 854 when a lane stores its own columns).
+// 4096: 533 us, 854 from the lanes that hold them), but in the kernels that split K,
+// which have a tile each and wait for it, from the lanes that hold them: 512 x 724 x 1024 6.7 us, 8.0 through LDS.
 template <typename S, bool WIDE>
 DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM], int64_t m0, int64_t end, int n0,
                     uint8_t* out, int lane) {
@@ -106,9 +107,17 @@ DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM]
       const bool four = a.y_f32 && a.N % 4 == 0 && ((uintptr_t)a.y & 15) == 0;
       const bool eight = !a.y_f32 && a.N % 8 == 0 && ((uintptr_t)a.y & 15) == 0;
       if (!four && !eight) {
-        // value by value, eight rows at a time, neighbouring lanes at neighbouring columns
         const int64_t at = row0 * a.N + n0;
         const int rows = (int)min((int64_t)16, end - row0), cols = a.N - n0;
+        if constexpr (S::KG > 1) {
+          if (r < rows) {
+#pragma unroll
+            for (int i = 0; i < W; i++)
+              if (W * q + i < cols) store_one(a, at + (r * a.N + W * q + i), acc[i >> 2][m][i & 3]);
+          }
+          continue;
+        }
+        // value by value, eight rows at a time, neighbouring lanes at neighbouring columns
 #pragma unroll
         for (int h = 0; h < 2; h++) {
           if ((r >> 3) == h) {
