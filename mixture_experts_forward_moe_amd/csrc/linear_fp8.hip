@@ -60,7 +60,8 @@ DEV void store_one(const LinearFp8Params& a, int64_t at, float v) {
 // wavefront's own part of LDS, 16 rows at a time (chunks swizzled by the row), in whole
 // lines.  Rows of odd sizes do value by value, from neighbouring lanes (16384 x 6147 x
 // 4096: 533 us, 854 from the lanes that hold them), but in the kernels that split K,
-// which have a tile each and wait for it, from the lanes that hold them: 512 x 724 x 1024 6.7 us, 8.0 through LDS.
+// which have a tile each and wait for it, from the lanes that hold them (512 x 724 x
+// 1024: 6.7 us, 8.0 through LDS).
 template <typename S, bool WIDE>
 DEV void store_tile(const LinearFp8Params& a, const f32x4_t (&acc)[S::TN][S::TM], int64_t m0, int64_t end, int n0,
                     uint8_t* out, int lane) {
