@@ -436,11 +436,12 @@ __global__ __launch_bounds__(S::NT * S::KG, 2) void fp8_tile_kernel(const Linear
 #pragma unroll
       for (int m = 0; m < TM; m++)
         __builtin_memcpy(&later[m], xsf + min(16 * (TM * wm + m) + r, last_m) * kb + at, 4);
-    } else {
+    } else {  // the bytes from the K group's first block on (past the last one: that one, of values that count as 0)
+      const int b = KG == 1 ? 0 : min(first_s, kb - 1);
 #pragma unroll
       for (int m = 0; m < TM; m++) {
         const uint8_t* row = xsf + min(16 * (TM * wm + m) + r, last_m) * kb;
-        later[m] = (uint32_t)row[0] | (uint32_t)row[min(1, kb - 1)] << 8 | (uint32_t)row[kb - 1] << 16;
+        later[m] = (uint32_t)row[b] | (uint32_t)row[min(b + 1, kb - 1)] << 8 | (uint32_t)row[kb - 1] << 16;
       }
     }
   };
