@@ -101,8 +101,12 @@ DEV u32x4_t ld8(const uint16_t* p) { return *reinterpret_cast<const u32x4_t*>(p)
 DEV void st8(uint16_t* p, const u32x4_t& v) { *reinterpret_cast<u32x4_t*>(p) = v; }
 DEV void st8(uint8_t* p, const u32x2_t& v) { *reinterpret_cast<u32x2_t*>(p) = v; }
 
+// This wavefront's number in a grid_of: workgroups past ROW_OF_GRID go on in the
+// grid's next row, so that its threads stay below 2^32 in each dimension
+constexpr int64_t ROW_OF_GRID = 1 << 23;
 DEV int64_t wave_number() {
-  return (int64_t)blockIdx.x * (blockDim.x >> 6) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  return ((int64_t)blockIdx.y * ROW_OF_GRID + blockIdx.x) * (blockDim.x >> 6) +
+         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 }
 
 // ------------------------------------------------------------- rows
@@ -496,9 +500,14 @@ __global__ __launch_bounds__(256) void fp8_weight_kernel(const uint16_t* w, int 
   }
 }
 
-// Wavefronts of a row of `cols` values and the grid of them, four a workgroup
+// Wavefronts of a row of `cols` values and the grid of them, four a workgroup (up to
+// 2^22 tokens of 32 pieces: 2^25 workgroups)
 int parts_of(int cols, int u) { return (cols + PIECE * u - 1) / (PIECE * u); }
-unsigned grid_of(int64_t rows, int parts) { return (unsigned)((rows * parts + 3) / 4); }
+dim3 grid_of(int64_t rows, int parts) {
+  const int64_t n = (rows * parts + 3) / 4;
+  if (n <= ROW_OF_GRID) return dim3((unsigned)n);
+  return dim3((unsigned)ROW_OF_GRID, (unsigned)((n + ROW_OF_GRID - 1) / ROW_OF_GRID));
+}
 
 // Few rows: a piece a wavefront, so that all of them are on their way at once; many:
 // several, whose loads go out together.  Rows quantised, one piece and four: 8 x 6144

@@ -1,4 +1,4 @@
-"""Which kernels a call launches: it is captured into a graph, whose nodes are
+"""Which kernels a call launches, and with which grids: it is captured into a graph, whose nodes are
 read through the HIP runtime that the process has loaded (GPU tests only)."""
 import ctypes
 
@@ -24,9 +24,9 @@ def _runtime():
     return hip
 
 
-def kernels_of(call):
-    """The (mangled) names of the kernels that call(stream) launches, in no
-    order.  The call is recorded and not run."""
+def launches_of(call):
+    """Of each kernel that call(stream) launches, in no order: its (mangled)
+    name, its grid and its workgroup.  The call is recorded and not run."""
     hip = _runtime()
     stream = torch.cuda.Stream()
     torch.cuda.synchronize()
@@ -40,7 +40,7 @@ def kernels_of(call):
         call(stream)
     finally:
         do("hipStreamEndCapture", raw, ctypes.byref(graph))
-    names = []
+    found = []
     try:
         do("hipGraphGetNodes", graph, None, ctypes.byref(n))
         nodes = (ctypes.c_void_p * n.value)()
@@ -50,7 +50,11 @@ def kernels_of(call):
             do("hipGraphKernelNodeGetParams", ctypes.c_void_p(node), ctypes.byref(p))
             name = hip.hipKernelNameRefByPtr(ctypes.c_void_p(p.func), raw)
             assert name, "a kernel without a name"
-            names.append(name.decode())
+            found.append((name.decode(), (p.grid.x, p.grid.y, p.grid.z), (p.block.x, p.block.y, p.block.z)))
     finally:
         do("hipGraphDestroy", graph)
-    return names
+    return found
+
+
+def kernels_of(call):
+    return [name for name, _, _ in launches_of(call)]
