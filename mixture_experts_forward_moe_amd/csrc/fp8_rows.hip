@@ -287,7 +287,11 @@ __global__ __launch_bounds__(256) void finalize_backward_kernel(const FinalizeBa
 // f(g), f'(g), the up part and whether it follows u.  SwiGLU: min(g, l)
 // sigmoid(a min(g, l)) and clamp(u, -l, l) + b; past a limit the derivative is
 // 0, at it that of the inside.  Selections, not fminf, so that a NaN stays one.
-// Where the sigmoid or 1 - tanh^2 is 0 its product with what may overflow is 0.
+// Where a sigmoid is 0 its product with what may overflow is 0.
+// GeGLU: g (1 + tanh z) / 2 is g sigmoid(2 z); both sigmoid(2 z) and
+// sigmoid(-2 z) come from exp(-2 |z|), so that neither is a difference (1 +
+// tanh z would be off by 30% at g = -5); the reciprocal of what lies in [1, 2] is the
+// instruction's, a step off at most (65536 x 2048: 195 us, with a division 214).
 struct GatePart {
   float f, df, up, dup;
 };
@@ -295,10 +299,11 @@ template <int AK>
 DEV GatePart gate_part(float g, float u, const GateAct& p) {
   if constexpr (AK == ACT_GEGLU_TANH) {
     const float c = 0.7978845608028654f;
-    const float t = tanhf(c * (g + 0.044715f * g * g * g));
-    const float sech = (1.0f - t) * (1.0f + t);
-    const float slope = sech == 0.0f ? 0.0f : 0.5f * g * sech * (c * (1.0f + 3.0f * 0.044715f * g * g));
-    return {0.5f * g * (1.0f + t), 0.5f * (1.0f + t) + slope, u, 1.0f};
+    const float z = c * (g + 0.044715f * g * g * g);
+    const float e = expf(-2.0f * fabsf(z)), big = __builtin_amdgcn_rcpf(1.0f + e), small = e * big;
+    const float s = z > 0.0f ? big : small;
+    const float slope = small == 0.0f ? 0.0f : 2.0f * g * big * small * (c * (1.0f + 3.0f * 0.044715f * g * g));
+    return {g * s, s + slope, u, 1.0f};
   } else {
     const float gc = g > p.limit ? p.limit : g;
     const float uc = u > p.limit ? p.limit : u < -p.limit ? -p.limit : u;
