@@ -308,7 +308,8 @@ DEV GatePart gate_part(float g, float u, const GateAct& p) {
     const float gc = g > p.limit ? p.limit : g;
     const float uc = u > p.limit ? p.limit : u < -p.limit ? -p.limit : u;
     const float s = 1.0f / (1.0f + expf(-p.alpha * gc));
-    const float df = s == 0.0f ? 0.0f : s * (1.0f + p.alpha * gc * (1.0f - s));
+    // (a g may overflow where 1 - s is 0, which it is from 128 on; a NaN is one by s)
+    const float df = s == 0.0f ? 0.0f : s * (1.0f + fminf(p.alpha * gc, 128.0f) * (1.0f - s));
     return {gc * s, g > p.limit ? 0.0f : df, uc + p.beta, fabsf(u) > p.limit ? 0.0f : 1.0f};
   }
 }

@@ -83,3 +83,39 @@ def test_value_at_every_gate(kind, kw):
     tol = want.abs() * ((1 + U4) * (1 + U8) - 1) + f_off * up.abs() * 2 * U24 * (1 + U4) + f.abs() * U24
     low = 2.0 ** -126 * 2.0 ** -10 + 2.0 ** -126 * (h[:, :I].double().abs() + 1)
     near(ref.rows(y.cpu(), y_sf.cpu()), want, tol + low, "y")
+
+
+FAR = [2.0e38, 2.5e38, 3.2e38]
+
+
+@pytest.mark.parametrize("kind,kw", [("geglu", {}), ("swiglu", {}), ("swiglu", dict(alpha=1.702)),
+                                     ("swiglu", dict(alpha=-3.0)), ("swiglu", dict(alpha=1.702, beta=1.0, limit=7.0))])
+def test_gradient_of_the_largest_values(kind, kw):
+    """Gates and ups at the end of bf16's range, one at a time: gradients of finite values are finite numbers."""
+    say(f"gradient of the largest values {kind} {kw}")
+    I = 128
+    large = torch.tensor(FAR + [-v for v in FAR]).to(BF16)
+    n = len(large)
+    h = torch.full((2 * n + 1, 2 * I), 0.5).to(BF16)
+    h[:n, :I] = large[:, None]
+    h[n:2 * n, I:] = large[:, None]
+    h[2 * n, 0], h[2 * n, I + 1], h[2 * n, 2] = math.nan, math.nan, -math.inf
+    M = len(h)
+    y, y_sf, hq, hq_sf = (torch.empty(M, c, dtype=BYTE, device="cuda") for c in (I, 1, 2 * I, 2))
+    dh = torch.empty(M, 2 * I, dtype=BF16, device="cuda")
+    dy = torch.full((M, I), 2.0 ** -9).to(BF16)
+    dy[:, 1::2] = 0
+    moe.moe_gated_act_fp8(h.cuda(), y, y_sf, hq=hq, hq_sf=hq_sf, **kwargs(kind, kw))
+    moe.moe_gated_act_fp8_backward(hq, hq_sf, dy.cuda(), dh=dh, **kwargs(kind, kw))
+    got = dh.cpu().double()
+    assert bool(torch.isfinite(got[:-1]).all())
+    top = torch.finfo(torch.float32).max
+    kept = ref.halves_rows(hq.cpu(), hq_sf.cpu())[:-1].clamp(-top, top)
+    f, df, up, dup = ref.act(kind, kept[:, :I], kept[:, I:], **kw)
+    f = torch.where(torch.isnan(f), 0.0, f)
+    d = dy.double()[:-1]
+    want = torch.cat((d * df * up, d * f * dup), 1)
+    # ordinary values at 0.5, all else the value itself or 0: fp32's dozen roundings, and bf16's
+    near(got[:-1], want, want.abs() * (U8 + 32 * U24) + 2.0 ** -134, "dh")
+    # a gate's NaN reaches both halves, an up value's the gate's
+    assert set(torch.isnan(got[-1]).nonzero().flatten().tolist()) == {0, 1, 2, I, I + 2}
