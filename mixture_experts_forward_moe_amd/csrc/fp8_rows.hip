@@ -68,7 +68,7 @@ DEV u32x2_t quantize8(const u32x4_t& v, uint32_t& code) {
   return o;
 }
 
-// the eight values of codes under their E8M0 code, in fp32
+// the eight values of codes under their E8M0 code, in fp32, finite but for NaN codes
 DEV void decode8(const u32x2_t& q, uint32_t code, float (&v)[8]) {
   const float s = e8m0_scale_operand(code);
 #pragma unroll
@@ -79,6 +79,11 @@ DEV void decode8(const u32x2_t& q, uint32_t code, float (&v)[8]) {
     v[4 * i + 1] = lo[1];
     v[4 * i + 2] = hi[0];
     v[4 * i + 3] = hi[1];
+  }
+  if (code >= 247u) {  // 256 times 2^120, what the largest finite bf16 are rounded to, is past fp32: the end of its range
+    constexpr float TOP = 0x1.fffffep127f;
+#pragma unroll
+    for (int i = 0; i < 8; i++) v[i] = v[i] > TOP ? TOP : v[i] < -TOP ? -TOP : v[i];
   }
 }
 

@@ -86,15 +86,17 @@ def test_value_at_every_gate(kind, kw):
 
 
 FAR = [2.0e38, 2.5e38, 3.2e38]
+PAST = [3.29e38, 3.32e38, 3.38e38]  # kept as codes that stand for 2^128
 
 
+@pytest.mark.parametrize("values", [FAR, PAST])
 @pytest.mark.parametrize("kind,kw", [("geglu", {}), ("swiglu", {}), ("swiglu", dict(alpha=1.702)),
                                      ("swiglu", dict(alpha=-3.0)), ("swiglu", dict(alpha=1.702, beta=1.0, limit=7.0))])
-def test_gradient_of_the_largest_values(kind, kw):
+def test_gradient_of_the_largest_values(kind, kw, values):
     """Gates and ups at the end of bf16's range, one at a time: gradients of finite values are finite numbers."""
-    say(f"gradient of the largest values {kind} {kw}")
+    say(f"gradient of the largest values {kind} {kw} {values}")
     I = 128
-    large = torch.tensor(FAR + [-v for v in FAR]).to(BF16)
+    large = torch.tensor(values + [-v for v in values]).to(BF16)
     n = len(large)
     h = torch.full((2 * n + 1, 2 * I), 0.5).to(BF16)
     h[:n, :I] = large[:, None]
