@@ -230,6 +230,7 @@ class MoePlan:
 def moe_sort(topk_ids, num_experts: int, num_local_experts: int, local_expert_offset: int, tile: int,
              route_order: int = ROUTE_ORDER_AUTO, plan: MoePlan | None = None, stream=None) -> MoePlan:
     M, top_k = topk_ids.shape
+    _below_2_31("moe_sort", M | top_k)
     if plan is None:
         plan = MoePlan(M, top_k, num_local_experts, tile, topk_ids.device)
     _check(lib().moe_sort(_ptr(topk_ids), M, top_k, num_experts, num_local_experts, local_expert_offset, route_order,
@@ -313,6 +314,7 @@ def moe_forward(x, x_sf, topk_ids, topk_weights, w1, w1_sf, w1_alpha, w2, w2_sf,
     """The whole forward pass into `out` (bf16 [M, H]).  A workspace is taken
     from `workspace`, or allocated here (outside the library) when None."""
     M = topk_ids.shape[0]
+    _below_2_31("moe_forward", M)
     if opts is None:
         tile = kw.pop("tile", 0) or default_tile(M, top_k, num_experts, num_local_experts, quant_mode)
         fm = kw.get("finalize_mode", FINALIZE_DETERMINISTIC)
@@ -332,6 +334,7 @@ def moe_forward_noalloc(x, x_sf, topk_ids, topk_weights, w1, w1_sf, w1_alpha, w2
     """moe_forward with the library's own fixed scratch array as workspace
     (nothing is allocated, here or in the library)."""
     M = topk_ids.shape[0]
+    _below_2_31("moe_forward_noalloc", M)
     opts = make_opts(**kw)
     _check(lib().moe_forward_noalloc(_ptr(x), _ptr(x_sf), _ptr(topk_ids), _ptr(topk_weights), _ptr(w1), _ptr(w1_sf),
                                      _ptr(w1_alpha), _ptr(w2), _ptr(w2_sf), _ptr(w2_alpha), num_experts, top_k,
@@ -445,6 +448,13 @@ def _shapes(where, **given):
             raise MoeError(ERR_INVALID_ARGUMENT, f"{where}: {name} {what}")
 
 
+def _below_2_31(where: str, sizes: int):
+    """Refuses a tensor's sizes (or-ed together) that an int of the C ABI does
+    not hold: ctypes would cut them off."""
+    if sizes >> 31:
+        raise MoeError(ERR_UNSUPPORTED, f"{where}: a size is 2^31 or more")
+
+
 def _dtype(where: str, name: str, t) -> int:
     """moe_dtype_t of a floating tensor (bf16 also as 16-bit integers)."""
     if not _F32:
@@ -495,6 +505,7 @@ def moe_rmsnorm(x, weight, y=None, residual=None, residual_out=None, q=None, q_s
     except (AttributeError, ValueError):
         _shapes(w, x=x)
         raise
+    _below_2_31(w, M | H)
     dev = x.get_device()
     wd = _dtype(w, "weight", weight)
     xp, xs = _rows(w, "x", x, shape, _BF16, dev)
@@ -520,6 +531,7 @@ def moe_rmsnorm_backward(dy, h, weight, rstd, dx, dweight=None, dh=None, workspa
     except (AttributeError, ValueError):
         _shapes(w, dy=dy)
         raise
+    _below_2_31(w, M | H)
     dev = dy.get_device()
     wd = _dtype(w, "weight", weight)
     args = (_arg(w, "dy", dy, shape, _BF16, dev), _arg(w, "h", h, shape, _BF16, dev),
@@ -557,6 +569,7 @@ def moe_router_topk(logits, topk_ids, topk_weights, score=SCORE_SOFTMAX, renorma
     except (AttributeError, ValueError):
         _shapes(w, logits=logits, topk_ids=topk_ids)
         raise
+    _below_2_31(w, M | E | k)
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
@@ -583,6 +596,7 @@ def moe_balance_loss(logits, topk_ids, coef, expert_counts, mean_probs, prob_gra
     except (AttributeError, ValueError):
         _shapes(w, logits=logits, topk_ids=topk_ids)
         raise
+    _below_2_31(w, M | E | k)
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     lp, ls = _rows(w, "logits", logits, (M, E), _F32 if d else _BF16, dev)
@@ -604,6 +618,7 @@ def moe_router_backward(logits, topk_ids, d_logits, d_topk_weights=None, prob_gr
     except (AttributeError, ValueError):
         _shapes(w, logits=logits, topk_ids=topk_ids)
         raise
+    _below_2_31(w, M | E | k)
     dev = logits.get_device()
     d = _dtype(w, "logits", logits)
     if _dtype(w, "d_logits", d_logits) != d:
@@ -630,6 +645,7 @@ def moe_linear_mx(x, x_sf, w, w_sf, y, x_elem=0, alpha=None, bias=None, accumula
         _shapes(f, x=x, w=w)
         raise
     K *= 2
+    _below_2_31(f, M | N | K)
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_mx(
@@ -671,6 +687,7 @@ def moe_quantize_fp8(x, q, q_sf, stream=None):
     of bf16 rows x, which may be strided."""
     w = "moe_quantize_fp8"
     rows, cols = _two(w, "x", x)
+    _below_2_31(w, cols)
     dev = x.get_device()
     xp, xs = _rows(w, "x", x, (rows, cols), _BF16, dev)
     _check(lib().moe_quantize_fp8(xp, xs, rows, cols, _arg(w, "q", q, (rows, cols), _BYTE, dev),
@@ -686,6 +703,7 @@ def moe_quantize_fp8_weight(weight, q, sf, qt=None, sft=None, stream=None):
     if weight is None or weight.dim() not in (2, 3):
         raise MoeError(ERR_INVALID_ARGUMENT, f"{w}: weight must have two or three dimensions")
     lead, (N, K) = tuple(weight.shape[:-2]), weight.shape[-2:]
+    _below_2_31(w, N | K | (lead[0] if lead else 1))
     dev = weight.get_device()
     _check(lib().moe_quantize_fp8_weight(
         _arg(w, "weight", weight, (*lead, N, K), _BF16, dev), lead[0] if lead else 1, N, K,
@@ -700,6 +718,7 @@ def moe_dispatch(x, plan: MoePlan, rows=None, q=None, q_sf=None, stream=None):
     H] with q_sf [route_slots, ceil(H / 128)]."""
     w = "moe_dispatch"
     H = _two(w, "x", x)[1]
+    _below_2_31(w, H)
     dev = x.get_device()
     p = _plan_arg(w, plan, dev)
     n = plan.route_slots
@@ -714,6 +733,7 @@ def moe_dispatch_backward(d_rows, plan: MoePlan, dx, accumulate=False, stream=No
     routes."""
     w = "moe_dispatch_backward"
     H = _two(w, "d_rows", d_rows)[1]
+    _below_2_31(w, H)
     dev = d_rows.get_device()
     p = _plan_arg(w, plan, dev)
     _check(lib().moe_dispatch_backward(_arg(w, "d_rows", d_rows, (plan.route_slots, H), _BF16, dev), p, H,
@@ -727,6 +747,7 @@ def moe_finalize_backward(dout, y2, plan: MoePlan, topk_weights, dy2=None, q=Non
     and / or quantised in q, q_sf) and, with y2, of the routing weights."""
     w = "moe_finalize_backward"
     H = _two(w, "dout", dout)[1]
+    _below_2_31(w, H)
     dev = dout.get_device()
     p = _plan_arg(w, plan, dev)
     n = plan.route_slots
@@ -745,6 +766,7 @@ def moe_linear_fp8(x, x_sf, w, w_sf, y, bias=None, accumulate=False, stream=None
     f = "moe_linear_fp8"
     M, K = _two(f, "x", x)
     N = _two(f, "w", w)[0]
+    _below_2_31(f, M | N | K)
     dev = x.get_device()
     d = _dtype(f, "y", y)
     _check(lib().moe_linear_fp8(
@@ -760,6 +782,7 @@ def moe_grouped_linear_fp8(x, x_sf, plan: MoePlan, w, w_sf, y, stream=None):
     ceil(K / 128)], y bf16 [route_slots, N]."""
     f = "moe_grouped_linear_fp8"
     K, N = _two(f, "x", x)[1], _two(f, "y", y)[1]
+    _below_2_31(f, N | K)
     dev = x.get_device()
     p = _plan_arg(f, plan, dev)
     n, E = plan.route_slots, plan.num_local_experts
@@ -775,6 +798,7 @@ def moe_linear_fp8_wgrad(dy, x, x_sf, dw, accumulate=False, stream=None):
     f = "moe_linear_fp8_wgrad"
     M, N = _two(f, "dy", dy)
     K = _two(f, "x", x)[1]
+    _below_2_31(f, M | N | K)
     dev = dy.get_device()
     _check(lib().moe_linear_fp8_wgrad(
         _arg(f, "dy", dy, (M, N), _BF16, dev), _arg(f, "x", x, (M, K), _BYTE, dev),
@@ -787,6 +811,7 @@ def moe_grouped_linear_fp8_wgrad(dy, x, x_sf, plan: MoePlan, dw, accumulate=Fals
     range: dy bf16 [route_slots, N], x E4M3 [route_slots, K]."""
     f = "moe_grouped_linear_fp8_wgrad"
     N, K = _two(f, "dy", dy)[1], _two(f, "x", x)[1]
+    _below_2_31(f, N | K)
     dev = dy.get_device()
     p = _plan_arg(f, plan, dev)
     n, E = plan.route_slots, plan.num_local_experts
@@ -804,6 +829,7 @@ def moe_gated_act_fp8(h, y, y_sf, hq=None, hq_sf=None, plan: MoePlan | None = No
     its valid slots are the rows."""
     w = "moe_gated_act_fp8"
     rows, I = _two(w, "y", y)
+    _below_2_31(w, 2 * I)
     dev = y.get_device()
     p = None if plan is None else _plan_arg(w, plan, dev)
     if plan is not None:
@@ -823,6 +849,7 @@ def moe_gated_act_fp8_backward(hq, hq_sf, dy, dh=None, dq=None, dq_sf=None, plan
     [rows, 2 ceil(I / 128)]."""
     w = "moe_gated_act_fp8_backward"
     rows, I = _two(w, "dy", dy)
+    _below_2_31(w, 2 * I)
     dev = dy.get_device()
     p = None if plan is None else _plan_arg(w, plan, dev)
     if plan is not None:
