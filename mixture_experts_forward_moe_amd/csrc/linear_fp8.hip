@@ -290,20 +290,6 @@ struct Tile {
   static constexpr int NX = BM * 8 / NT, NW = BN * 8 / NT;      // LDS-DMA loads a wavefront and stage
 };
 
-// The four E8M0 bytes from block 4 g of a row of kb blocks, the first one lowest.
-// A word that reaches past the row's end is read from its last four bytes.
-DEV uint32_t scale_word(const uint8_t* row, int g, int kb) {
-  if (kb >= 4) {
-    const int at = min(4 * g, kb - 4);
-    uint32_t v;
-    __builtin_memcpy(&v, row + at, 4);
-    return v >> (8 * min(3, 4 * g - at));
-  }
-  uint32_t v = 0;
-  for (int i = 0; i < kb; i++) v |= (uint32_t)row[i] << (8 * i);
-  return v;
-}
-
 // One workgroup a tile at a time (a plan's tiles have BM rows), K in stages of 128 in a ring of buffers that
 // LDS-DMA fills.  A wavefront computes 16 TM rows by 16 TN columns, W's rows the
 // first operand: a lane then has 4 TN consecutive columns of one row of y, if
@@ -633,7 +619,7 @@ hipError_t launch_linear_fp8(const LinearFp8Params& a, hipStream_t s) {
     // rows 208, 621)
     switch (a.tile) {
       case 16: return launch_stream(a, s);
-      case 32: return launch_tile<Low>(a, s);
+      case 32: return launch_tile_as<Low, true>(a, s);  // (a plan's rows always leave in whole lines)
       case 64: return launch_tile<Small>(a, s);
       case 128: return launch_tile<Middle>(a, s);
       default: return launch_tile<Big>(a, s);  // 256
