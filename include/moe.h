@@ -720,8 +720,10 @@ moe_status_t moe_grouped_linear_fp8(const uint8_t* x, const uint8_t* x_sf, const
 /* moe_linear_fp8_wgrad: the gradient of a product's weights from its rows, kept in 8
  * bits by the forward pass:
  *   dw[n, k] = sum_m dy[m, n] x[m, k]   (+ dw[n, k] when accumulating)
- * dy bf16 [M, N]; x E4M3 [M, K] with x_sf; dw fp32 [N, K].  x is decoded exactly, the
- * products are exact and the sums fp32, in an order that depends on the shape alone.
+ * dy bf16 [M, N]; x E4M3 [M, K] with x_sf; dw fp32 [N, K].  x is decoded to bf16:
+ * exactly, if moe_quantize_fp8 made it (of other codes those of odd multiples of 2^-134
+ * or less, which bf16 does not hold, are rounded).  The products are exact and the sums
+ * fp32, in an order that depends on the shape alone.
  * M = 0: zeros.  N a multiple of 8, K of 16; dy, x and dw 16-byte aligned; M at most
  * 2^26, N and K at most 2^16 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, const uint8_t* x_sf, int M, int N, int K,

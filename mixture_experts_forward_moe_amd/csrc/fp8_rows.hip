@@ -4,7 +4,8 @@
 // A row is held as E4M3 codes with one E8M0 byte for each 128 values, the least
 // power of two that brings the block's largest value to 448 or less.  So the
 // codes of a block never overflow, decoding is exact in bf16 (a code times a
-// power of two), and the matrix instruction takes the bytes as they are.  An
+// power of two; under the least scales bf16's own steps keep the codes to multiples
+// of 2^-133), and the matrix instruction takes the bytes as they are.  An
 // infinity or a NaN has no part in the scale and becomes a NaN code: what
 // overflowed stays visible.
 //
@@ -321,8 +322,8 @@ DEV GatePart gate_part(float g, float u, const GateAct& p) {
 
 // y = f(g) up(u) of eight columns a lane, rounded to bf16 and quantised; g and u
 // quantised too where they are kept.  A plan's padding slots are passed over.
-// 65536 x 2048: 207 us, 4.5 TB/s (GeGLU 185), its gradient 248, 5.4 TB/s: HBM, and the
-// few rows' 3.2 to 3.6 us are a launch's and one trip to memory.
+// 65536 x 2048: 216 us, 4.4 TB/s (GeGLU 195), its gradient 255, 5.3 TB/s (244): HBM, and
+// the few rows' 3.3 to 3.7 us are a launch's and one trip to memory.
 template <int AK, int U>
 __global__ __launch_bounds__(256) void act_kernel(const ActParams a, int parts) {
   const int64_t w = wave_number(), row = w / parts;

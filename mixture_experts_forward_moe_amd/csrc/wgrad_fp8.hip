@@ -5,7 +5,8 @@
 // way; gfx950's transposing LDS read (ds_read_b64_tr_b16) turns 4 rows of 16
 // values into the fragments that the matrix instruction takes.  x's codes are
 // decoded to bf16 once a workgroup, on their way into LDS: a code times a power
-// of two is exact there, so the products are exact and the sums fp32.
+// of two is exact there (under the three least scales for the codes that bf16 values
+// were quantised to), so the products are exact and the sums fp32.
 #include "device_common.h"
 #include "dynamic_lds.h"
 #include "internal.h"
@@ -76,7 +77,8 @@ DEV int swizzle(int m) {
 // stages ahead, written into LDS two ahead between the multiplications, so that a
 // wavefront's fragments of the next stage are on their way at the barrier (with two
 // buffers, all of a stage written behind its last read: 16384 x 4096 x 6144 790 us,
-// now 748, 1.1 PFLOP/s; experts of 16384 tokens 1435, now 1320).  (LDS-DMA of dy is slower: the
+// now 735 - 750, 1.1 PFLOP/s; experts of 16384 tokens 1435, now 1200 - 1290; added onto
+// what dw holds 764 and 1930).  (LDS-DMA of dy is slower: the
 // compiler cannot tell its target from what a transposing read takes, and waits
 // for all of it.)  Rows past the end of the range are read as 0: the buffers
 // end there.
