@@ -638,8 +638,8 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
 
 /* Row quantisation of bf16 x [rows, cols], row stride in elements (0 =
  * contiguous; shorter than cols: MOE_ERR_INVALID_ARGUMENT).  cols a multiple of
- * 16, row strides of 8, x and q 16-byte aligned, rows * ceil(cols / 2048) at most
- * 2^25 (else MOE_ERR_UNSUPPORTED). */
+ * 16, at most 2^30, row strides of 8, x and q 16-byte aligned, rows * ceil(cols /
+ * 2048) at most 2^25 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_quantize_fp8(const uint16_t* x, int64_t x_row_stride, int64_t rows, int cols, uint8_t* q,
                               uint8_t* q_sf, moe_stream_t stream);
 
@@ -746,8 +746,8 @@ moe_status_t moe_grouped_linear_fp8_wgrad(const uint16_t* dy, const uint8_t* x, 
  *   f = min(g, limit) sigmoid(swiglu_alpha min(g, limit)), up = clamp(u, -limit, limit) + swiglu_beta
  * or MOE_ACT_GEGLU_TANH (with the SwiGLU parameters 1, 0, FLT_MAX); the other one:
  * MOE_ERR_UNSUPPORTED.  With a plan (else NULL) rows must be its route_slots, and its
- * valid slots are the rows.  I a multiple of 16; h, y and hq 16-byte aligned; rows *
- * ceil(I / 1024) at most 2^25 (else MOE_ERR_UNSUPPORTED). */
+ * valid slots are the rows.  I a multiple of 16, at most 2^29; h, y and hq 16-byte
+ * aligned; rows * ceil(I / 1024) at most 2^25 (else MOE_ERR_UNSUPPORTED). */
 moe_status_t moe_gated_act_fp8(const uint16_t* h, const moe_plan_t* plan, int64_t rows, int I, int activation,
                                float swiglu_alpha, float swiglu_beta, float swiglu_limit, uint8_t* y, uint8_t* y_sf,
                                uint8_t* hq, uint8_t* hq_sf, moe_stream_t stream);
