@@ -628,8 +628,9 @@ moe_status_t moe_linear_mx(const uint8_t* x, const uint8_t* x_sf, int x_elem, co
  *            largest finite |value| to 448 or less.  codes = value / scale,
  *            rounded to nearest even, from bf16.  An infinity or a NaN becomes a
  *            NaN code.  (The eight largest finite bf16, from 2^128 - 2^123 on, become
- *            2^128: an infinity for the products, fp32's largest value for the
- *            activation's gradient.)
+ *            2^128, and the products multiply that; as a value by itself it is an
+ *            infinity for the weights' gradient, fp32's largest value for the
+ *            activation's.)
  *  weights : E4M3 codes [N, K] and an fp32 scale for each block of 128 x 128,
  *            [ceil(N / 128), ceil(K / 128)]; the scales may be any finite value.
  * Rows in a plan's order are [route_slots, ..]; padding slots are neither read

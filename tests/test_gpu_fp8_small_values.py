@@ -1,5 +1,5 @@
-"""Rows at the lower end of bf16's range through the quantiser, the products and
-the weights' gradient: what the quantiser makes of them decodes exactly, in
+"""Rows at the ends of bf16's range through the quantiser, the products and the
+weights' gradient; at the lower one: what the quantiser makes of them decodes exactly, in
 bf16 too, and nothing is lost on the way to an fp32 result that has room."""
 import pytest
 import torch
@@ -49,3 +49,24 @@ def test_products(low, M):
     dw = torch.empty(N, K, device="cuda")
     moe.moe_linear_fp8_wgrad(dy, q, sf, dw)
     assert torch.equal(dw, torch.mm(dy.double().t().contiguous(), xv).float())
+
+
+@pytest.mark.parametrize("M", [4, 40])
+def test_the_largest_values(M):
+    """What is kept as 2^128 multiplies as that; the weights' gradient has an infinity of it."""
+    say(f"the largest values, {M} rows")
+    x = torch.zeros(M, K, dtype=BF16)
+    x[1, 3], x[2, 5], x[3, 7] = 3.38e38, -3.3e38, 3.2e38
+    q, sf = (torch.empty(M, c, dtype=BYTE, device="cuda") for c in (K, 3))
+    moe.moe_quantize_fp8(x.cuda(), q, sf)
+    kept = ref.rows(*ref.quantize(x))
+    assert kept[1, 3] == 2.0 ** 128 and kept[2, 5] == -2.0 ** 128 and kept[3, 7] < 2.0 ** 128
+    w = ref.encode(torch.full((N, K), 0.5).double()).cuda()
+    y = torch.empty(M, N, device="cuda")
+    moe.moe_linear_fp8(q, sf, w, torch.ones(2, 3, device="cuda"), y)
+    assert torch.equal(y.cpu(), (kept.sum(1, keepdim=True) * 0.5).float().expand(-1, N))
+    dw = torch.empty(N, K, device="cuda")
+    moe.moe_linear_fp8_wgrad(torch.full((M, N), 2.0 ** -9, dtype=BF16, device="cuda"), q, sf, dw)
+    want = (kept * 2.0 ** -9).sum(0)
+    want[3], want[5] = float("inf"), -float("inf")
+    assert torch.equal(dw.cpu(), want.float().expand(N, -1))
